@@ -97,7 +97,7 @@ def moe_align(topk_ids, E: int, block_size: int, capacity: Optional[int] = None,
     if expert_ids is None:
         expert_ids = torch.empty(max(cap // block_size, 1), dtype=torch.int32, device=dev)
     if num_tokens_post_padded is None:
-        num_tokens_post_padded = torch.empty(4, dtype=torch.int32, device=dev)
+        num_tokens_post_padded = torch.empty(1, dtype=torch.int32, device=dev)
     check(load().moe_align(_ptr(topk_ids), M, topk, E, block_size, _ptr(sorted_token_ids), _ptr(expert_ids),
                            _ptr(num_tokens_post_padded), cap, _stream(stream)), "moe_align")
     return sorted_token_ids, expert_ids, num_tokens_post_padded
