@@ -14,6 +14,9 @@
  *   sparse24_w4a16_gemm   2:4-sparse int4 dense linear layer, fp16 activations
  *   sparse24_w8a16_gemm   the same with 8-bit kept codes
  *   moe_fp8_w8a8_gemm     grouped GEMM with FP8 (E4M3) weights and activations
+ *   moe_route_grouped     router with softmax or sigmoid scores, a balancing bias and expert groups
+ *   moe_route_grouped_align  the same with the token sort (one kernel for small batches)
+ *   wq_rms_norm           residual addition + RMS norm, 16-bit and/or E4M3 output with scales
  * Beside them: dense_w4a16_gemm / dense_w8a16_gemm (one quantized weight
  * matrix, the same kernels with one expert) and wq_quantize_w8 (the int8
  * weights and scales from a 16-bit checkpoint on the device, at load time).
@@ -62,6 +65,7 @@ typedef int wq_status;
 
 #define WQ_F16 0
 #define WQ_BF16 1
+#define WQ_F32 2 /* router logits only */
 
 /* Stages of the grouped GEMM (moe_w4a16_gemm / moe_w8a16_gemm). */
 #define WQ_STAGE_GATE_UP 0 /* H = silu(A W_gate^T) * (A W_up^T), rows in sorted order       */
@@ -134,6 +138,83 @@ wq_status moe_route_align(const float* d_logits, int M, int E, int topk, int ren
                           float* d_topk_weights, int32_t* d_topk_ids, int32_t* d_sorted_token_ids,
                           int32_t* d_expert_ids, int32_t* d_num_tokens_post_padded, size_t capacity,
                           void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* moe_route_grouped                                                         */
+/* ------------------------------------------------------------------------ */
+/*
+ * Router with scores, a bias for balance and expert groups; one token per row
+ * of the logits.
+ *   s_e = softmax over all E logits, or 1 / (1 + exp(-l_e)) (scoring)
+ *   choice: without a bias by the logits themselves (the scores grow with
+ *     them); with one by c_e = float(s_e + bias_e).  The n_group groups of
+ *     E / n_group consecutive experts are valued by their best expert
+ *     (WQ_GROUP_MAX) or by the float sum of their two largest c
+ *     (WQ_GROUP_TOP2; c_e = float(s_e) without a bias); the topk_group best
+ *     groups are open, and the topk best experts of those are the slots, best
+ *     first.  Equal values: the lower group, the lower expert.
+ *   weights: routed_scale * s_j, and with renormalize over the sum of the
+ *     slots' s (the bias is not in them).
+ * Scores, sums and quotients are double, weights are rounded once to float.
+ *   d_logits        device [M, E], logits_dtype WQ_F32, WQ_F16 or WQ_BF16.
+ *                   -inf is a score of 0; a row whose scores are all 0, or
+ *                   whose slots' are, gets weights of 0.  With a NaN or +inf
+ *                   logit the weights of that row are unspecified (its ids
+ *                   still name topk different experts).
+ *   d_bias          device float [E] or NULL; -inf keeps an expert to the last
+ *   d_topk_weights  device float [M, topk] (out)
+ *   d_topk_ids      device int32 [M, topk] (out)
+ * Limits: those of moe_route; 1 <= n_group <= 64 dividing E, 1 <= topk_group <=
+ * n_group, topk <= topk_group * E / n_group, WQ_GROUP_TOP2 needs E / n_group
+ * >= 2; routed_scale finite.  With scoring WQ_SCORE_SOFTMAX, one group, no bias,
+ * scale 1 and float32 logits the slots are those of moe_route.
+ *
+ * moe_route_grouped_align: followed by moe_align, as moe_route_align (one
+ * kernel for batches of at most 16 tokens).
+ */
+#define WQ_SCORE_SOFTMAX 0
+#define WQ_SCORE_SIGMOID 1
+#define WQ_GROUP_MAX 0
+#define WQ_GROUP_TOP2 1
+wq_status moe_route_grouped(const void* d_logits, int logits_dtype, int M, int E, int topk, int scoring,
+                            const float* d_bias, int n_group, int topk_group, int group_score, int renormalize,
+                            float routed_scale, float* d_topk_weights, int32_t* d_topk_ids, void* stream);
+wq_status moe_route_grouped_align(const void* d_logits, int logits_dtype, int M, int E, int topk, int scoring,
+                                  const float* d_bias, int n_group, int topk_group, int group_score, int renormalize,
+                                  float routed_scale, int block_size, float* d_topk_weights, int32_t* d_topk_ids,
+                                  int32_t* d_sorted_token_ids, int32_t* d_expert_ids,
+                                  int32_t* d_num_tokens_post_padded, size_t capacity, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* wq_rms_norm                                                               */
+/* ------------------------------------------------------------------------ */
+/*
+ * The norm in front of a layer, with the residual's addition and the FP8
+ * layer's input codes.  Per row of n values, in float32:
+ *   s = x + residual (or x);  residual_out = s rounded to the act dtype
+ *   y = s / sqrt(mean(s^2) + eps) * weight;  out = y rounded to the act dtype
+ *   codes: E4M3 codes of y (not of out), clamped to +-448, ties to even, with
+ *     d_scales   a scale per row, written: c = max(max|y| / 448, 2^-100); the
+ *                code is that of y * (1 / c)
+ *     otherwise  static_scale: the code is that of y / static_scale
+ * s is not rounded before the norm.  Any one of residual_out, out and codes
+ * may be the only output.  Rows of bf16 values beyond float32's square range
+ * are scaled down first; a row with an infinity or a NaN gives what the
+ * formulas do (NaN codes are 0x7F or 0xFF, the row scale skips NaNs).
+ *   d_x, d_residual, d_residual_out, d_out: [rows, n] act dtype, row strides in
+ *     elements (>= n); d_residual, d_residual_out, d_out may be NULL
+ *   d_weight [n] act dtype, NULL for ones; d_codes uint8 [rows, n] or NULL;
+ *   d_scales float [rows] or NULL
+ * residual_out and out may each be x or residual (same pointer and stride); any
+ * other overlap of an output with an input or output is refused.  16-byte
+ * accesses where n and the strides are multiples of 8, single values otherwise.
+ * Limits: n <= 2^30; eps finite and >= 1e-30; static_scale (codes without
+ * d_scales) finite and > 0.  rows = 0 launches nothing.
+ */
+wq_status wq_rms_norm(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
+                      const void* d_weight, int rows, int n, float eps, int act_dtype, void* d_residual_out,
+                      int64_t residual_out_stride, void* d_out, int64_t out_stride, uint8_t* d_codes, float* d_scales,
+                      float static_scale, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Grouped GEMMs                                                             */

@@ -1,0 +1,159 @@
+"""Refusals of the serving operators around the quantised layers, before any
+device work: through the C ABI (sizes, codes, pointers, overlaps) and in the
+Python binding (shapes, types, strides, which arguments go together)."""
+import ctypes as C
+
+import pytest
+import torch
+
+import weight_only_quantized_topk_amd as wq
+
+FAKE = 0x100000  # aligned, non-null: only ever seen by host-side validation
+
+
+def at(off=0):
+    return C.c_void_p(FAKE + off)
+
+
+def status(fn, *args):
+    L = wq.load()
+    st = getattr(L, fn)(*args)
+    return st, L.wq_last_error().decode()
+
+
+INV, UNS = wq.WQ_ERR_INVALID, wq.WQ_ERR_UNSUPPORTED
+BF = wq.WQ_BF16
+
+
+# ---------------------------------------------------------------------------
+# moe_route_grouped, moe_route_grouped_align
+# ---------------------------------------------------------------------------
+def route_args(align=False, **k):
+    d = dict(logits=at(), dt=2, M=4, E=64, topk=4, scoring=0, bias=None, n_group=8, topk_group=2, score=0, renorm=1,
+             scale=1.0, bs=16, w=at(), ids=at(), st=at(), ex=at(), nt=at(), cap=1024)
+    d.update(k)
+    a = [d[n] for n in ("logits", "dt", "M", "E", "topk", "scoring", "bias", "n_group", "topk_group", "score", "renorm",
+                        "scale")]
+    return a + ([d["bs"], d["w"], d["ids"], d["st"], d["ex"], d["nt"], d["cap"], None] if align
+                else [d["w"], d["ids"], None])
+
+
+@pytest.mark.parametrize("fn", ["moe_route_grouped", "moe_route_grouped_align"])
+@pytest.mark.parametrize("change,want", [
+    (dict(dt=3), INV), (dict(dt=-1), INV), (dict(M=-1), INV), (dict(topk=0), INV), (dict(topk=65), INV),
+    (dict(E=0), INV), (dict(E=2048, n_group=1, topk_group=1), UNS), (dict(topk=17, topk_group=8), UNS),
+    (dict(M=1 << 24), UNS), (dict(scoring=2), INV), (dict(score=2), INV), (dict(n_group=0), INV),
+    (dict(n_group=7), INV), (dict(n_group=-8), INV), (dict(E=256, n_group=128), UNS), (dict(topk_group=0), INV),
+    (dict(topk_group=9), INV), (dict(topk=9, topk_group=1), INV), (dict(n_group=64, topk_group=8, score=1), INV),
+    (dict(scale=float("nan")), INV), (dict(scale=float("inf")), INV), (dict(logits=None), INV), (dict(w=None), INV),
+    (dict(ids=None), INV), (dict(bias=at(4)), INV), (dict(logits=at(2)), INV)])
+def test_route_grouped_refusals(fn, change, want):
+    assert status(fn, *route_args(fn.endswith("align"), **change))[0] == want
+
+
+def test_route_grouped_align_refusals():
+    for change, want in ((dict(bs=24), UNS), (dict(bs=0), UNS), (dict(cap=16), INV), (dict(cap=1032), INV),
+                         (dict(cap=1 << 31), UNS), (dict(st=None), INV), (dict(ex=at(8)), INV), (dict(nt=None), INV)):
+        assert status("moe_route_grouped_align", *route_args(True, **change))[0] == want, change
+    assert status("moe_route_grouped", *route_args(M=0, logits=None, w=None, ids=None))[0] == wq.WQ_OK
+
+
+def test_route_grouped_binding_refusals():
+    lg = torch.zeros((4, 64))
+    for call in (lambda **k: wq.moe_route_grouped(k.pop("logits", lg), k.pop("topk", 4), **k),
+                 lambda **k: wq.moe_route_grouped_align(k.pop("logits", lg), k.pop("topk", 4), 16, **k)):
+        with pytest.raises(TypeError):
+            call(logits=lg.double())
+        with pytest.raises(ValueError):
+            call(logits=torch.zeros(64))
+        with pytest.raises(ValueError):
+            call(logits=torch.zeros((4, 128))[:, ::2])
+        with pytest.raises(ValueError):
+            call(scoring="relu")
+        with pytest.raises(ValueError):
+            call(group_score="mean")
+        with pytest.raises(ValueError):
+            call(topk=0)
+        with pytest.raises(ValueError):
+            call(topk=1 << 32)
+        with pytest.raises(ValueError):
+            call(n_group=(1 << 32) + 1)
+        with pytest.raises(ValueError):
+            call(bias=torch.zeros(63))
+        with pytest.raises(TypeError):
+            call(bias=torch.zeros(64, dtype=torch.bfloat16))
+        with pytest.raises(ValueError):
+            call(topk_weights=torch.zeros((4, 5)))
+        with pytest.raises(TypeError):
+            call(topk_ids=torch.zeros((4, 4), dtype=torch.int64))
+    with pytest.raises(ValueError):
+        wq.moe_route_grouped_align(lg, 4, 0)
+    with pytest.raises(ValueError):
+        wq.moe_route_grouped_align(lg, 4, 16, sorted_token_ids=torch.zeros(16, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        wq.moe_route_grouped_align(lg, 4, 16, num_tokens_post_padded=torch.zeros(1))
+
+
+# ---------------------------------------------------------------------------
+# wq_rms_norm
+# ---------------------------------------------------------------------------
+MB = 1 << 20
+
+
+def norm_args(**k):
+    d = dict(x=at(), xs=512, r=at(MB), rs=512, w=at(2 * MB), rows=4, n=512, eps=1e-6, dt=BF, ro=at(3 * MB), ros=512,
+             out=at(4 * MB), os=512, codes=at(5 * MB), scales=at(6 * MB), static=0.0)
+    d.update(k)
+    return [d[n] for n in ("x", "xs", "r", "rs", "w", "rows", "n", "eps", "dt", "ro", "ros", "out", "os", "codes",
+                           "scales", "static")] + [None]
+
+
+@pytest.mark.parametrize("change", [
+    dict(dt=2), dict(dt=7), dict(rows=-1), dict(n=0), dict(eps=0.0), dict(eps=-1.0), dict(eps=float("nan")),
+    dict(eps=float("inf")), dict(ro=None, out=None, codes=None, scales=None), dict(codes=None), dict(scales=None),
+    dict(scales=None, static=float("inf")), dict(scales=None, static=-1.0), dict(xs=511), dict(rs=0), dict(ros=-512),
+    dict(os=8), dict(xs=1 << 62), dict(x=None), dict(x=at(2)), dict(out=at(4 * MB + 8)), dict(w=at(2 * MB + 4)),
+    dict(codes=at(5 * MB + 1)),
+    # overlaps: shifted rows, another stride, outputs on one another, on the weight, codes on x
+    dict(out=at(16)), dict(ro=at(MB + 512)), dict(out=at(), os=520), dict(ro=at(4 * MB)), dict(codes=at()),
+    dict(scales=at(4 * MB)), dict(out=at(2 * MB)), dict(scales=at(5 * MB)), dict(out=at(2 * MB - 1024)),
+    dict(x=at(4 * MB + 512), xs=1024, os=1024)])
+def test_rms_norm_refusals(change):
+    assert status("wq_rms_norm", *norm_args(**change))[0] == INV
+
+
+def test_rms_norm_no_rows_and_sizes():
+    assert status("wq_rms_norm", *norm_args(rows=0, x=None))[0] == wq.WQ_OK
+    assert status("wq_rms_norm", *norm_args(rows=0, ro=None, out=None, codes=None, scales=None))[0] == wq.WQ_OK
+    n = (1 << 30) + 8
+    assert status("wq_rms_norm", *norm_args(n=n, xs=n, rs=n, ros=n, os=n))[0] == UNS
+
+
+def test_rms_norm_allowed_overlaps_pass_the_checks():
+    """Exact in-place forms and rows in each other's gaps reach the device check (there is no device memory at these
+    addresses): the status is another one."""
+    for change in (dict(ro=at(MB)), dict(out=at()), dict(ro=at(), out=at(MB)), dict(w=None, r=None, rs=0),
+                   dict(x=at(4 * MB + 1024), xs=1024, os=1024), dict(out=at(4 * MB + 1024), os=1024, ro=at(4 * MB), ros=1024)):
+        st, msg = status("wq_rms_norm", *norm_args(**change))
+        assert st in (wq.WQ_ERR_DEVICE, wq.WQ_ERR_HIP), (change, msg)
+
+
+def test_rms_norm_binding_refusals():
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    w = torch.ones(64, dtype=torch.bfloat16)
+    bad_value = [dict(x=torch.zeros(64, dtype=torch.bfloat16)), dict(x=torch.zeros((4, 128), dtype=torch.bfloat16)[:, ::2]),
+                 dict(x=torch.zeros((1, 64), dtype=torch.bfloat16).expand(4, 64)), dict(x=x.float()),
+                 dict(weight=torch.ones(63, dtype=torch.bfloat16)), dict(quant="token"), dict(quant="static"),
+                 dict(quant="row", scale=1.0), dict(codes=torch.zeros((4, 64), dtype=torch.uint8)),
+                 dict(quant="static", scale=1.0, scales=torch.zeros(4)), dict(want_out=False, out=x.clone()),
+                 dict(residual_out=x.clone()), dict(residual=torch.zeros((4, 65), dtype=torch.bfloat16)),
+                 dict(quant="row", codes=torch.zeros((4, 128), dtype=torch.uint8)[:, :64])]
+    bad_type = [dict(weight=w.float()), dict(residual=x.half()), dict(out=x.float()),
+                dict(quant="row", codes=torch.zeros((4, 64), dtype=torch.int8)),
+                dict(quant="row", scales=torch.zeros(4, dtype=torch.bfloat16))]
+    for change in bad_value:
+        with pytest.raises(ValueError):
+            wq.rms_norm(change.pop("x", x), change.pop("weight", w), **change)
+    for change in bad_type:
+        with pytest.raises(TypeError):
+            wq.rms_norm(x, change.pop("weight", w), **change)

@@ -10,7 +10,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libwqmoe.so")
 
 WQ_OK, WQ_ERR_INVALID, WQ_ERR_UNSUPPORTED, WQ_ERR_DEVICE, WQ_ERR_HIP = 0, 1, 2, 3, 4
-WQ_F16, WQ_BF16 = 0, 1
+WQ_F16, WQ_BF16, WQ_F32 = 0, 1, 2
+WQ_SCORE_SOFTMAX, WQ_SCORE_SIGMOID = 0, 1
+WQ_GROUP_MAX, WQ_GROUP_TOP2 = 0, 1
 WQ_STAGE_GATE_UP, WQ_STAGE_DOWN, WQ_STAGE_RAW = 0, 1, 2
 WQ_PACK_INTERLEAVE_GATE_UP = 1
 WQ_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -18,6 +20,7 @@ WQ_NOALLOC_SCRATCH_BYTES = 64 << 20
 EXPORTS = (
     "wq_version", "wq_status_string", "wq_last_error",
     "moe_route", "moe_align_capacity", "moe_align", "moe_route_align", "moe_route_gate_up",
+    "moe_route_grouped", "moe_route_grouped_align", "wq_rms_norm",
     "moe_gemm_workspace_bytes", "moe_w4a16_gemm", "moe_w8a16_gemm", "moe_w8a16_gemm_noalloc",
     "sparse24_w4a16_gemm", "sparse24_w8a16_gemm", "wq_quantize_w8",
     "dense_gemm_workspace_bytes", "dense_w4a16_gemm", "dense_w8a16_gemm",
@@ -84,6 +87,10 @@ def load():
     L.moe_align_capacity.restype = sz
     L.moe_align.argtypes = [p, i, i, i, i, p, p, p, sz, p]
     L.moe_route_align.argtypes = [p, i, i, i, i, i, p, p, p, p, p, sz, p]
+    f, i64 = C.c_float, C.c_int64
+    L.moe_route_grouped.argtypes = [p, i, i, i, i, i, p, i, i, i, i, f, p, p, p]
+    L.moe_route_grouped_align.argtypes = [p, i, i, i, i, i, p, i, i, i, i, f, i, p, p, p, p, p, sz, p]
+    L.wq_rms_norm.argtypes = [p, i64, p, i64, p, i, i, f, i, p, i64, p, i64, p, p, f, p]
     L.moe_gemm_workspace_bytes.argtypes = [i, i, i, i, i, i, sz, i]
     L.moe_gemm_workspace_bytes.restype = sz
     L.moe_w4a16_gemm.argtypes = [C.POINTER(WqMoeGemmDesc), p]
@@ -114,12 +121,13 @@ def load():
     L.wq_pack_fp8_bytes.argtypes = [i, i, i]
     L.wq_pack_fp8_bytes.restype = sz
     L.wq_pack_fp8.argtypes = [i, i, i, p, p, p, i, p, p]
-    for f in ("moe_route", "moe_align", "moe_route_align", "moe_route_gate_up", "moe_w4a16_gemm", "moe_w8a16_gemm",
+    for fn in ("moe_route", "moe_align", "moe_route_align", "moe_route_gate_up", "moe_route_grouped",
+              "moe_route_grouped_align", "wq_rms_norm", "moe_w4a16_gemm", "moe_w8a16_gemm",
               "moe_w8a16_gemm_noalloc", "sparse24_w4a16_gemm",
               "sparse24_w8a16_gemm",
               "wq_quantize_w8", "dense_w4a16_gemm", "dense_w8a16_gemm", "wq_pack_w4",
               "wq_pack_w8", "wq_pack_sparse24", "moe_fp8_w8a8_gemm", "wq_pack_fp8"):
-        getattr(L, f).restype = i
+        getattr(L, fn).restype = i
     _lib = L
     return L
 

@@ -281,6 +281,196 @@ wq_status moe_route_align(const float* d_logits, int M, int E, int topk, int ren
 }
 
 // ---------------------------------------------------------------------------
+// moe_route_grouped: the arguments both calls share
+static wq_status route_grouped_args(wq::RouteGroupedArgs& g, const void* d_logits, int dtype, int M, int E, int topk,
+                                    int scoring, const float* d_bias, int n_group, int topk_group, int group_score,
+                                    int renormalize, float routed_scale, float* d_topk_weights, int32_t* d_topk_ids) {
+    WQ_REQUIRE(dtype == WQ_F32 || dtype == WQ_F16 || dtype == WQ_BF16, WQ_ERR_INVALID, "bad logits dtype %d", dtype);
+    WQ_REQUIRE(M >= 0, WQ_ERR_INVALID, "M = %d < 0", M);
+    WQ_REQUIRE(E >= 1 && topk >= 1 && topk <= E, WQ_ERR_INVALID, "need 1 <= topk <= E (topk %d, E %d)", topk, E);
+    WQ_REQUIRE(E <= 1024, WQ_ERR_UNSUPPORTED, "E = %d > 1024", E);
+    WQ_REQUIRE(topk <= 16, WQ_ERR_UNSUPPORTED, "topk = %d > 16", topk);
+    WQ_REQUIRE((int64_t)M * topk <= MAX_PAIRS, WQ_ERR_UNSUPPORTED, "M*topk > 2^24");
+    WQ_REQUIRE(scoring == WQ_SCORE_SOFTMAX || scoring == WQ_SCORE_SIGMOID, WQ_ERR_INVALID, "bad scoring %d", scoring);
+    WQ_REQUIRE(group_score == WQ_GROUP_MAX || group_score == WQ_GROUP_TOP2, WQ_ERR_INVALID, "bad group_score %d",
+               group_score);
+    WQ_REQUIRE(n_group >= 1 && E % n_group == 0, WQ_ERR_INVALID, "n_group %d does not divide E %d", n_group, E);
+    WQ_REQUIRE(n_group <= 64, WQ_ERR_UNSUPPORTED, "n_group = %d > 64", n_group);
+    WQ_REQUIRE(topk_group >= 1 && topk_group <= n_group, WQ_ERR_INVALID, "need 1 <= topk_group <= n_group (%d, %d)",
+               topk_group, n_group);
+    WQ_REQUIRE((int64_t)topk <= (int64_t)topk_group * (E / n_group), WQ_ERR_INVALID,
+               "topk %d > the %d open groups' %d experts", topk, topk_group, topk_group * (E / n_group));
+    WQ_REQUIRE(group_score != WQ_GROUP_TOP2 || n_group == 1 || E / n_group >= 2, WQ_ERR_INVALID,
+               "groups of one expert have no two best");
+    WQ_REQUIRE(std::isfinite(routed_scale), WQ_ERR_INVALID, "routed_scale is not finite");
+    if (M > 0) {
+        WQ_TRY(check_ptr(d_logits, "logits"));
+        if (d_bias) WQ_TRY(check_ptr(d_bias, "bias"));
+        WQ_TRY(check_ptr(d_topk_weights, "topk_weights"));
+        WQ_TRY(check_ptr(d_topk_ids, "topk_ids"));
+    }
+    g = wq::RouteGroupedArgs{d_logits, d_bias, d_topk_weights, d_topk_ids, dtype, M, E, topk, n_group, topk_group,
+                             scoring == WQ_SCORE_SIGMOID ? 1 : 0, group_score == WQ_GROUP_TOP2 ? 1 : 0,
+                             renormalize ? 1 : 0, routed_scale};
+    return WQ_OK;
+}
+
+static wq_status route_grouped_devs(const wq::RouteGroupedArgs& g) {
+    WQ_TRY(check_dev(g.logits, "logits"));
+    if (g.bias) WQ_TRY(check_dev(g.bias, "bias"));
+    WQ_TRY(check_dev(g.w_out, "topk_weights"));
+    WQ_TRY(check_dev(g.ids_out, "topk_ids"));
+    return WQ_OK;
+}
+
+wq_status moe_route_grouped(const void* d_logits, int logits_dtype, int M, int E, int topk, int scoring,
+                            const float* d_bias, int n_group, int topk_group, int group_score, int renormalize,
+                            float routed_scale, float* d_topk_weights, int32_t* d_topk_ids, void* stream) {
+    try {
+        wq::RouteGroupedArgs g{};
+        WQ_TRY(route_grouped_args(g, d_logits, logits_dtype, M, E, topk, scoring, d_bias, n_group, topk_group,
+                                  group_score, renormalize, routed_scale, d_topk_weights, d_topk_ids));
+        if (M == 0) return ok();
+        WQ_TRY(route_grouped_devs(g));
+        wq::launch_route_grouped(g, (hipStream_t)stream);
+        return after_launch("moe_route_grouped");
+    } catch (...) {
+        return fail(WQ_ERR_HIP, "moe_route_grouped: unexpected exception");
+    }
+}
+
+wq_status moe_route_grouped_align(const void* d_logits, int logits_dtype, int M, int E, int topk, int scoring,
+                                  const float* d_bias, int n_group, int topk_group, int group_score, int renormalize,
+                                  float routed_scale, int block_size, float* d_topk_weights, int32_t* d_topk_ids,
+                                  int32_t* d_sorted_token_ids, int32_t* d_expert_ids,
+                                  int32_t* d_num_tokens_post_padded, size_t capacity, void* stream) {
+    try {
+        wq::RouteGroupedArgs g{};
+        WQ_TRY(route_grouped_args(g, d_logits, logits_dtype, M, E, topk, scoring, d_bias, n_group, topk_group,
+                                  group_score, renormalize, routed_scale, d_topk_weights, d_topk_ids));
+        WQ_REQUIRE(valid_block_size(block_size), WQ_ERR_UNSUPPORTED, "block_size %d not in {16,32,64,128,256}",
+                   block_size);
+        const size_t need = moe_align_capacity(M, topk, E, block_size);
+        WQ_REQUIRE(capacity >= need, WQ_ERR_INVALID, "capacity %zu < required %zu", capacity, need);
+        WQ_REQUIRE(capacity % (size_t)block_size == 0, WQ_ERR_INVALID, "capacity not a multiple of block_size");
+        WQ_REQUIRE(capacity <= (size_t)0x7fffffff, WQ_ERR_UNSUPPORTED, "capacity too large");
+        WQ_TRY(check_ptr(d_sorted_token_ids, "sorted_token_ids"));
+        WQ_TRY(check_ptr(d_expert_ids, "expert_ids"));
+        WQ_TRY(check_ptr(d_num_tokens_post_padded, "num_tokens_post_padded"));
+        if (M > 0) WQ_TRY(route_grouped_devs(g));
+        WQ_TRY(check_dev(d_sorted_token_ids, "sorted_token_ids"));
+        WQ_TRY(check_dev(d_expert_ids, "expert_ids"));
+        WQ_TRY(check_dev(d_num_tokens_post_padded, "num_tokens_post_padded"));
+        hipStream_t s = (hipStream_t)stream;
+        if (M > 0 && wq::route_grouped_fused(M, topk)) {
+            wq::launch_route_grouped_align(g, block_size, d_sorted_token_ids, d_expert_ids, d_num_tokens_post_padded,
+                                           (int)capacity, s);
+            return after_launch("moe_route_grouped_align");
+        }
+        if (M > 0) {
+            wq::launch_route_grouped(g, s);
+            WQ_TRY(after_launch("moe_route_grouped_align"));
+        }
+        wq::launch_align(d_topk_ids, M * topk, E, block_size, d_sorted_token_ids, d_expert_ids,
+                         d_num_tokens_post_padded, (int)capacity, s);
+        return after_launch("moe_route_grouped_align");
+    } catch (...) {
+        return fail(WQ_ERR_HIP, "moe_route_grouped_align: unexpected exception");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// two arrays of `rows` rows (row starts `stride` bytes apart, `width` bytes
+// used of each) that share a byte
+static bool rows_overlap(const void* pa, int64_t sa, int64_t wa, const void* pb, int64_t sb, int64_t wb, int64_t rows) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(pa), b = reinterpret_cast<uintptr_t>(pb);
+    const uintptr_t ea = a + (uintptr_t)((rows - 1) * sa + wa), eb = b + (uintptr_t)((rows - 1) * sb + wb);
+    if (ea <= b || eb <= a) return false;
+    if (rows == 1 || sa != sb) return true;  // other strides over one range: taken to overlap
+    const uintptr_t d = b >= a ? (b - a) % (uintptr_t)sa : (uintptr_t)sa - 1 - (a - b - 1) % (uintptr_t)sa;
+    return !(d >= (uintptr_t)wa && d + (uintptr_t)wb <= (uintptr_t)sa);  // b's rows in the gaps of a's
+}
+
+wq_status wq_rms_norm(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
+                      const void* d_weight, int rows, int n, float eps, int act_dtype, void* d_residual_out,
+                      int64_t residual_out_stride, void* d_out, int64_t out_stride, uint8_t* d_codes, float* d_scales,
+                      float static_scale, void* stream) {
+    try {
+        const char* who = "wq_rms_norm";
+        WQ_REQUIRE(act_dtype == WQ_F16 || act_dtype == WQ_BF16, WQ_ERR_INVALID, "%s: bad act dtype", who);
+        WQ_REQUIRE(rows >= 0 && n >= 1, WQ_ERR_INVALID, "%s: bad sizes rows %d n %d", who, rows, n);
+        WQ_REQUIRE(n <= (1 << 30), WQ_ERR_UNSUPPORTED, "%s: n = %d > 2^30", who, n);
+        WQ_REQUIRE(std::isfinite(eps) && eps >= 1e-30f, WQ_ERR_INVALID, "%s: eps must be finite and >= 1e-30", who);
+        if (rows == 0) return ok();  // (empty arrays may have no address)
+        WQ_REQUIRE(d_residual_out || d_out || d_codes, WQ_ERR_INVALID, "%s: no output", who);
+        WQ_REQUIRE(d_codes || !d_scales, WQ_ERR_INVALID, "%s: row scales without codes", who);
+        WQ_REQUIRE(!d_codes || d_scales || (std::isfinite(static_scale) && static_scale > 0.0f), WQ_ERR_INVALID,
+                   "%s: static_scale must be finite and > 0", who);
+        struct Rows {
+            const void* p;
+            int64_t stride, width;  // bytes
+            const char* name;
+        };
+        const int64_t most = INT64_MAX / 4 / rows;
+        const Rows in[3] = {{d_x, x_stride * 2, (int64_t)n * 2, "x"},
+                            {d_residual, residual_stride * 2, (int64_t)n * 2, "residual"},
+                            {d_weight, 0, (int64_t)n * 2, "weight"}};
+        const Rows out[4] = {{d_residual_out, residual_out_stride * 2, (int64_t)n * 2, "residual_out"},
+                             {d_out, out_stride * 2, (int64_t)n * 2, "out"},
+                             {d_codes, n, n, "codes"},
+                             {d_scales, 4, 4, "scales"}};
+        const int64_t strides[4] = {x_stride, residual_stride, residual_out_stride, out_stride};
+        const void* strided[4] = {d_x, d_residual, d_residual_out, d_out};
+        for (int i = 0; i < 4; ++i)
+            WQ_REQUIRE(!strided[i] || (strides[i] >= n && strides[i] <= most), WQ_ERR_INVALID,
+                       "%s: row stride %lld (n %d)", who, (long long)strides[i], n);
+        WQ_TRY(check_ptr(d_x, "x"));
+        for (const Rows* a : {&in[1], &in[2], &out[0], &out[1], &out[2], &out[3]})
+            if (a->p) WQ_TRY(check_ptr(a->p, a->name));
+        for (int o = 0; o < 4; ++o) {
+            if (!out[o].p) continue;
+            for (int i = 0; i < 3; ++i) {
+                if (!in[i].p) continue;
+                const bool same = o < 2 && i < 2 && in[i].p == out[o].p && in[i].stride == out[o].stride;
+                // the weight is one row: every row of the output against it
+                const bool clash = i == 2 ? rows_overlap(out[o].p, 0, (rows - 1) * out[o].stride + out[o].width,
+                                                         in[i].p, 0, in[i].width, 1)
+                                          : rows_overlap(out[o].p, out[o].stride, out[o].width, in[i].p, in[i].stride,
+                                                         in[i].width, rows);
+                WQ_REQUIRE(same || !clash, WQ_ERR_INVALID, "%s: %s overlaps %s", who, out[o].name, in[i].name);
+            }
+            for (int p = 0; p < o; ++p)
+                WQ_REQUIRE(!out[p].p || !rows_overlap(out[o].p, out[o].stride, out[o].width, out[p].p, out[p].stride,
+                                                      out[p].width, rows),
+                           WQ_ERR_INVALID, "%s: %s overlaps %s", who, out[o].name, out[p].name);
+        }
+        WQ_TRY(check_dev(d_x, "x"));
+        for (const Rows* a : {&in[1], &in[2], &out[0], &out[1], &out[2], &out[3]})
+            if (a->p) WQ_TRY(check_dev(a->p, a->name));
+        wq::RmsNormArgs g{};
+        g.x = static_cast<const uint16_t*>(d_x);
+        g.r = static_cast<const uint16_t*>(d_residual);
+        g.w = static_cast<const uint16_t*>(d_weight);
+        g.r_out = static_cast<uint16_t*>(d_residual_out);
+        g.out = static_cast<uint16_t*>(d_out);
+        g.codes = d_codes;
+        g.scales = d_scales;
+        g.x_stride = x_stride;
+        g.r_stride = residual_stride;
+        g.ro_stride = residual_out_stride;
+        g.out_stride = out_stride;
+        g.rows = rows;
+        g.n = n;
+        g.eps = eps;
+        g.static_scale = static_scale;
+        wq::launch_rms_norm(g, act_dtype == WQ_BF16, (hipStream_t)stream);
+        return after_launch(who);
+    } catch (...) {
+        return fail(WQ_ERR_HIP, "wq_rms_norm: unexpected exception");
+    }
+}
+
+// ---------------------------------------------------------------------------
 // fp32 slabs of M*topk x n_out the DOWN stage may write (one per K slice)
 static int down_slabs(int M, int topk, int E, int n_out, int k_in) {
     return std::max(wq::prefill_down_split_max(M * topk, E, n_out, k_in), wq::tiny_down_slabs(M, k_in));

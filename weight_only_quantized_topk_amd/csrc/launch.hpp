@@ -30,6 +30,41 @@ bool route_align_fused(int M, int topk);
 void launch_route_align(const float* logits, int M, int E, int topk, int renormalize, float* w, int32_t* ids, int BS,
                         int32_t* sorted, int32_t* expert_ids, int32_t* ntpp, int cap, hipStream_t s);
 
+// route + sort with scores, a balancing bias and expert groups (route_grouped.hpp)
+struct RouteGroupedArgs {
+    const void* logits;       // [M, E] float32 / fp16 / bf16 (dtype: WQ_F32 / WQ_F16 / WQ_BF16)
+    const float* bias;        // [E] added to the scores for the choice only; or null
+    float* w_out;             // [M, topk]
+    int32_t* ids_out;         // [M, topk]
+    int dtype;
+    int M, E, topk;
+    int groups, topk_group;   // E / groups experts per group, topk_group groups open
+    int sigmoid;              // scores: 1 sigmoid, 0 softmax over all experts
+    int top2;                 // a group's value: 1 the sum of its two best scores, 0 its best expert
+    int renormalize;
+    float scale;              // routed weights are multiplied by it
+};
+void launch_route_grouped(const RouteGroupedArgs& g, hipStream_t s);
+// with the sort, in one kernel (M and M * topk within route_grouped_fused)
+bool route_grouped_fused(int M, int topk);
+void launch_route_grouped_align(const RouteGroupedArgs& g, int BS, int32_t* sorted, int32_t* expert_ids,
+                                int32_t* ntpp, int cap, hipStream_t s);
+
+// residual addition + RMS norm of rows (rms_norm.hip); strides in elements
+struct RmsNormArgs {
+    const uint16_t* x;
+    const uint16_t* r;        // residual, or null
+    const uint16_t* w;        // [n], or null for ones
+    uint16_t* r_out;          // x + r, or null
+    uint16_t* out;            // 16-bit output, or null
+    uint8_t* codes;           // E4M3 output [rows, n], or null
+    float* scales;            // row scales [rows] (written), or null: static_scale
+    int64_t x_stride, r_stride, ro_stride, out_stride;
+    int rows, n;
+    float eps, static_scale;
+};
+void launch_rms_norm(const RmsNormArgs& g, bool bf16, hipStream_t s);
+
 struct GemmArgs {
     const uint16_t* a;        // activations (x, gathered x, or H), 16-bit
     const uint8_t* w;         // packed weights, all experts

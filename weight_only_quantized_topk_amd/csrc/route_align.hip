@@ -20,6 +20,7 @@
 #include "common.hpp"
 #include "launch.hpp"
 #include "route_common.hpp"
+#include "route_grouped.hpp"
 
 #include <algorithm>
 
@@ -328,6 +329,76 @@ void launch_route_align(const float* logits, int M, int E, int topk, int renorma
                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     hipLaunchKernelGGL(route_align_kernel, dim3(1), dim3(ALIGN_THREADS), lds, s, logits, M, E, topk, renormalize, w,
                        ids, BS, id_bits(E), sorted, expert_ids, ntpp, cap);
+}
+
+// ---------------------------------------------------------------------------
+// moe_route_grouped: one wave per token (route_grouped.hpp), four tokens a
+// workgroup; with the sort for small batches in one workgroup, as
+// route_align_kernel: the pairs' experts stay in LDS, up to 64 pairs are sorted
+// by one wave, more by the whole workgroup.
+// ---------------------------------------------------------------------------
+template <int PL>
+__global__ __launch_bounds__(256) void route_grouped_kernel(RouteGroupedArgs g, int lpg, int per) {
+    const int m = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (m >= g.M) return;
+    route_token_grouped<PL>(g, m, threadIdx.x & 63, lpg, per, nullptr);
+}
+
+template <int PL>
+__global__ __launch_bounds__(ALIGN_THREADS) void route_grouped_align_kernel(RouteGroupedArgs g, int lpg, int per,
+                                                                            int BS, int nbits,
+                                                                            int32_t* __restrict__ sorted,
+                                                                            int32_t* __restrict__ expert_ids,
+                                                                            int32_t* __restrict__ ntpp, int cap) {
+    extern __shared__ int smem[];
+    const int lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6;
+    const int T = g.M * g.topk;
+    int* sids = smem;
+    if (wave < g.M) route_token_grouped<PL>(g, wave, lane, lpg, per, sids + wave * g.topk);
+    __syncthreads();
+    if (T <= ROUTE_ALIGN_WAVE_MAX) {
+        if (wave == 0) align_pairs(sids, T, BS, cap, lane, sorted, expert_ids, ntpp);
+        return;
+    }
+    align_body(sids, T, g.E, BS, nbits, sorted, expert_ids, ntpp, cap, smem + T);
+}
+
+// f(PL) for the experts a lane holds
+template <class F>
+static void with_per_lane(int per, F f) {
+    if (per <= 1) f(std::integral_constant<int, 1>{});
+    else if (per <= 2) f(std::integral_constant<int, 2>{});
+    else if (per <= 4) f(std::integral_constant<int, 4>{});
+    else if (per <= 8) f(std::integral_constant<int, 8>{});
+    else if (per <= 16) f(std::integral_constant<int, 16>{});
+    else f(std::integral_constant<int, 32>{});
+}
+
+void launch_route_grouped(const RouteGroupedArgs& g, hipStream_t s) {
+    const int lpg = grouped_lanes(g.groups), per = grouped_per_lane(g.E, g.groups);
+    with_per_lane(per, [&](auto P) {
+        hipLaunchKernelGGL(route_grouped_kernel<decltype(P)::value>, dim3((g.M + 3) / 4), dim3(256), 0, s, g, lpg, per);
+    });
+}
+
+bool route_grouped_fused(int M, int topk) { return route_align_fused(M, topk); }
+
+void launch_route_grouped_align(const RouteGroupedArgs& g, int BS, int32_t* sorted, int32_t* expert_ids,
+                                int32_t* ntpp, int cap, hipStream_t s) {
+    const int lpg = grouped_lanes(g.groups), per = grouped_per_lane(g.E, g.groups);
+    const int T = g.M * g.topk;
+    const bool one_wave = T <= ROUTE_ALIGN_WAVE_MAX;
+    const int threads = one_wave ? 64 * std::min(g.M, ALIGN_WAVES) : ALIGN_THREADS;
+    const size_t lds = sizeof(int) * ((size_t)T + (one_wave ? 0 : (size_t)g.E * ALIGN_WAVES));
+    with_per_lane(per, [&](auto P) {
+        constexpr int PL = decltype(P)::value;
+        if (lds > 65536)
+            (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&route_grouped_align_kernel<PL>),
+                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        hipLaunchKernelGGL(route_grouped_align_kernel<PL>, dim3(1), dim3(threads), lds, s, g, lpg, per, BS,
+                           id_bits(g.E), sorted, expert_ids, ntpp, cap);
+    });
 }
 
 }  // namespace wq

@@ -8,12 +8,12 @@ the packers, in its host code).  The names follow include/wqmoe.h.
 from __future__ import annotations
 
 import ctypes as C
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import numpy as np
 
 from . import _lib
-from ._lib import (WQ_BF16, WQ_F16, WQ_PACK_INTERLEAVE_GATE_UP, WQ_STAGE_DOWN, WQ_STAGE_GATE_UP, WQ_STAGE_RAW,
+from ._lib import (WQ_BF16, WQ_F16, WQ_F32, WQ_GROUP_MAX, WQ_GROUP_TOP2, WQ_SCORE_SIGMOID, WQ_SCORE_SOFTMAX, WQ_PACK_INTERLEAVE_GATE_UP, WQ_STAGE_DOWN, WQ_STAGE_GATE_UP, WQ_STAGE_RAW,
                    WqMoeGemmDesc, check, load)
 
 __all__ = [
@@ -21,7 +21,7 @@ __all__ = [
     "moe_route_gate_up",
     "moe_w8a16_gemm_noalloc", "sparse24_w4a16_gemm", "sparse24_w8a16_gemm", "quantize_w8", "dense_gemm_workspace_bytes", "dense_w4a16_gemm", "dense_w8a16_gemm",
     "pack_w4", "pack_w8", "pack_sparse24", "act_code", "moe_fp8_gemm_workspace_bytes", "moe_fp8_w8a8_gemm",
-    "pack_fp8",
+    "pack_fp8", "moe_route_grouped", "moe_route_grouped_align", "rms_norm", "RmsNormOut",
 ]
 
 
@@ -48,6 +48,47 @@ def act_code(dtype) -> int:
     if dtype == torch.bfloat16:
         return WQ_BF16
     raise ValueError("activation dtype must be float16 or bfloat16, got %s" % dtype)
+
+
+def _check(t, name: str, shape, dtypes, device=None, row_stride: bool = False):
+    """A tensor argument has the shape, one of the types, and is contiguous
+    (with row_stride: its last dimension is, and rows do not overlap)."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, the input on %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        rows, n = (t.shape if t.dim() == 2 else (0, 0))
+        if not row_stride or t.numel() and (t.stride(1) != 1 and n > 1 or t.stride(0) < n and rows > 1):
+            raise ValueError("%s must be contiguous%s, got strides %s"
+                             % (name, " in its rows" if row_stride else "", list(t.stride())))
+
+
+def _int32(**sizes):
+    """Sizes go through C int arguments, which would take them modulo 2^32."""
+    for name, v in sizes.items():
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise ValueError("%s = %d does not fit 32 bits" % (name, v))
+
+
+def _row_stride(t) -> int:
+    """The row stride of a [rows, n] tensor that _check has passed."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _keep_for(stream, *tensors):
+    """Memory allocated here for a call on another stream than the current one
+    is not handed out again before that stream is done with it."""
+    if stream is None:
+        return
+    torch = _torch()
+    if stream != torch.cuda.current_stream().cuda_stream:
+        s = torch.cuda.ExternalStream(stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
 
 
 def _np_ptr(a: Optional[np.ndarray]):
@@ -101,6 +142,155 @@ def moe_align(topk_ids, E: int, block_size: int, capacity: Optional[int] = None,
     check(load().moe_align(_ptr(topk_ids), M, topk, E, block_size, _ptr(sorted_token_ids), _ptr(expert_ids),
                            _ptr(num_tokens_post_padded), cap, _stream(stream)), "moe_align")
     return sorted_token_ids, expert_ids, num_tokens_post_padded
+
+
+_SCORING = {"softmax": WQ_SCORE_SOFTMAX, "sigmoid": WQ_SCORE_SIGMOID}
+_GROUP_SCORE = {"max": WQ_GROUP_MAX, "top2": WQ_GROUP_TOP2}
+
+
+def _grouped_args(logits, topk, scoring, bias, n_group, topk_group, group_score, topk_weights, topk_ids):
+    torch = _torch()
+    codes = {torch.float32: WQ_F32, torch.float16: WQ_F16, torch.bfloat16: WQ_BF16}
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, E], got %s" % list(logits.shape))
+    M, E = logits.shape
+    _int32(M=M, E=E, topk=topk, n_group=n_group, topk_group=topk_group)
+    _check(logits, "logits", (M, E), codes)
+    if scoring not in _SCORING or group_score not in _GROUP_SCORE:
+        raise ValueError("scoring %r not in %s or group_score %r not in %s"
+                         % (scoring, list(_SCORING), group_score, list(_GROUP_SCORE)))
+    dev = logits.device
+    if bias is not None:
+        _check(bias, "bias", (E,), (torch.float32,), dev)
+    if topk < 1:
+        raise ValueError("topk must be >= 1, got %d" % topk)
+    new = []
+    if topk_weights is None:
+        new.append(topk_weights := torch.empty((M, topk), dtype=torch.float32, device=dev))
+    else:
+        _check(topk_weights, "topk_weights", (M, topk), (torch.float32,), dev)
+    if topk_ids is None:
+        new.append(topk_ids := torch.empty((M, topk), dtype=torch.int32, device=dev))
+    else:
+        _check(topk_ids, "topk_ids", (M, topk), (torch.int32,), dev)
+    return M, E, codes[logits.dtype], topk_weights, topk_ids, new
+
+
+def moe_route_grouped(logits, topk: int, scoring: str = "softmax", bias=None, n_group: int = 1, topk_group: int = 1,
+                      group_score: str = "max", renormalize: bool = True, routed_scale: float = 1.0,
+                      topk_weights=None, topk_ids=None, stream=None):
+    """Router with softmax or sigmoid scores, a balancing bias (added for the
+    choice only) and expert groups, of which the topk_group best (by their best
+    expert, "max", or the sum of their two best scores, "top2") are open:
+    logits [M, E] float32 / fp16 / bf16 (device) -> (topk_weights [M, topk]
+    f32, topk_ids [M, topk] i32)."""
+    M, E, dt, topk_weights, topk_ids, new = _grouped_args(logits, topk, scoring, bias, n_group, topk_group,
+                                                          group_score, topk_weights, topk_ids)
+    check(load().moe_route_grouped(_ptr(logits), dt, M, E, topk, _SCORING[scoring], _ptr(bias), n_group, topk_group,
+                                   _GROUP_SCORE[group_score], int(bool(renormalize)), routed_scale,
+                                   _ptr(topk_weights), _ptr(topk_ids), _stream(stream)), "moe_route_grouped")
+    _keep_for(stream, *new)
+    return topk_weights, topk_ids
+
+
+def moe_route_grouped_align(logits, topk: int, block_size: int, scoring: str = "softmax", bias=None, n_group: int = 1,
+                            topk_group: int = 1, group_score: str = "max", renormalize: bool = True,
+                            routed_scale: float = 1.0, topk_weights=None, topk_ids=None, sorted_token_ids=None,
+                            expert_ids=None, num_tokens_post_padded=None, capacity: Optional[int] = None,
+                            stream=None):
+    """moe_route_grouped then moe_align in one call (one kernel for batches up
+    to 16 tokens) -> (topk_weights, topk_ids, sorted_token_ids [capacity],
+    expert_ids [capacity / block_size], num_tokens_post_padded [1]); buffers
+    not given are allocated, for the least capacity unless one is given."""
+    torch = _torch()
+    M, E, dt, topk_weights, topk_ids, new = _grouped_args(logits, topk, scoring, bias, n_group, topk_group,
+                                                          group_score, topk_weights, topk_ids)
+    _int32(block_size=block_size)
+    if block_size < 1:
+        raise ValueError("block_size must be >= 1, got %d" % block_size)
+    cap = moe_align_capacity(M, topk, E, block_size) if capacity is None else capacity
+    dev, i32 = logits.device, torch.int32
+    arrays = [(sorted_token_ids, "sorted_token_ids", cap), (expert_ids, "expert_ids", cap // block_size),
+              (num_tokens_post_padded, "num_tokens_post_padded", 1)]
+    for k, (t, name, n) in enumerate(arrays):
+        if t is None:
+            arrays[k] = torch.empty(max(n, 1), dtype=i32, device=dev)
+            new.append(arrays[k])
+        else:
+            if t.dim() != 1 or t.numel() < n:
+                raise ValueError("%s must hold %d values, got %s" % (name, n, list(t.shape)))
+            _check(t, name, t.shape, (i32,), dev)
+            arrays[k] = t
+    check(load().moe_route_grouped_align(_ptr(logits), dt, M, E, topk, _SCORING[scoring], _ptr(bias), n_group,
+                                         topk_group, _GROUP_SCORE[group_score], int(bool(renormalize)), routed_scale,
+                                         block_size, _ptr(topk_weights), _ptr(topk_ids), *map(_ptr, arrays), cap,
+                                         _stream(stream)), "moe_route_grouped_align")
+    _keep_for(stream, *new)
+    return (topk_weights, topk_ids, *arrays)
+
+
+class RmsNormOut(NamedTuple):
+    out: object       # [rows, n] act dtype, or None
+    residual: object  # [rows, n] act dtype, or None (no residual given)
+    codes: object     # [rows, n] uint8 E4M3 codes, or None
+    scales: object    # [rows] float32, or None (no row scales asked for)
+
+
+def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, quant: Optional[str] = None,
+             scale: Optional[float] = None, want_out: bool = True, out=None, residual_out=None, codes=None,
+             scales=None, stream=None) -> RmsNormOut:
+    """Residual addition + RMS norm of x [rows, n] bf16/fp16 (device; rows may be
+    strided): s = x + residual, y = s / sqrt(mean(s^2) + eps) * weight.  out is
+    y in x's type; with quant="row" codes are the E4M3 codes of y with one
+    written scale per row, with quant="static" those of y / scale (the FP8
+    layer's input in its two forms); residual is s in x's type.  Buffers not
+    given are allocated; out and residual_out may be x or residual."""
+    torch = _torch()
+    dt = act_code(x.dtype)
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, n], got %s" % list(x.shape))
+    rows, n = x.shape
+    _int32(rows=rows, n=n)
+    dev, same = x.device, (x.dtype,)
+    _check(x, "x", (rows, n), same, row_stride=True)
+    if weight is not None:
+        _check(weight, "weight", (n,), same, dev)
+    if quant not in (None, "row", "static"):
+        raise ValueError("quant must be None, 'row' or 'static', got %r" % (quant,))
+    if (quant == "static") != (scale is not None):
+        raise ValueError("scale goes with quant='static'")
+    if codes is not None and quant is None or scales is not None and quant != "row":
+        raise ValueError("codes go with quant, scales with quant='row'")
+    if out is not None and not want_out or residual_out is not None and residual is None:
+        raise ValueError("out goes with want_out, residual_out with a residual")
+    new = []
+
+    def buffer(t, name, shape, dtypes):
+        if t is None:
+            t = torch.empty(shape, dtype=dtypes[0], device=dev)
+            new.append(t)
+        else:
+            _check(t, name, shape, dtypes, dev, row_stride=dtypes is same)
+        return t
+
+    if residual is not None:
+        _check(residual, "residual", (rows, n), same, dev, row_stride=True)
+        residual_out = buffer(residual_out, "residual_out", (rows, n), same)
+    if want_out:
+        out = buffer(out, "out", (rows, n), same)
+    if quant is not None:
+        codes = buffer(codes, "codes", (rows, n), (torch.uint8, torch.float8_e4m3fn))
+    if quant == "row":
+        scales = buffer(scales, "scales", (rows,), (torch.float32,))
+
+    def strided(t):
+        return (None, 0) if t is None else (t.data_ptr(), _row_stride(t))
+
+    check(load().wq_rms_norm(*strided(x), *strided(residual), _ptr(weight), rows, n, eps, dt, *strided(residual_out),
+                             *strided(out), _ptr(codes), _ptr(scales), 0.0 if scale is None else scale,
+                             _stream(stream)), "wq_rms_norm")
+    _keep_for(stream, *new)
+    return RmsNormOut(out, residual_out, codes, scales)
 
 
 def moe_gemm_workspace_bytes(stage: int, M: int, topk: int, E: int, n_out: int, k_in: int, capacity: int,
