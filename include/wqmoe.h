@@ -14,9 +14,11 @@
  *   sparse24_w4a16_gemm   2:4-sparse int4 dense linear layer, fp16 activations
  *   sparse24_w8a16_gemm   the same with 8-bit kept codes
  *   moe_fp8_w8a8_gemm     grouped GEMM with FP8 (E4M3) weights and activations
+ *   moe_fp8_codes_gemm    its gate/up stage on E4M3 rows with a scale each
  *   moe_route_grouped     router with softmax or sigmoid scores, a balancing bias and expert groups
  *   moe_route_grouped_align  the same with the token sort (one kernel for small batches)
  *   wq_rms_norm           residual addition + RMS norm, 16-bit and/or E4M3 output with scales
+ *   dense_lora_gemm       low-rank adapters of many requests beside a dense projection
  * Beside them: dense_w4a16_gemm / dense_w8a16_gemm (one quantized weight
  * matrix, the same kernels with one expert) and wq_quantize_w8 (the int8
  * weights and scales from a 16-bit checkpoint on the device, at load time).
@@ -376,6 +378,19 @@ wq_status moe_w8a16_gemm_noalloc(const wq_moe_gemm_desc* d, void* stream);
 size_t moe_fp8_gemm_workspace_bytes(int stage, int M, int topk, int E, int n_out, int k_in);
 wq_status moe_fp8_w8a8_gemm(const wq_moe_gemm_desc* d, float in_scale, float out_scale, void* stream);
 
+/*
+ * moe_fp8_codes_gemm: the GATE_UP and RAW stages on an x that is E4M3 codes
+ * already (wq_rms_norm's), with a scale of its own for each row or one for all:
+ *   d->d_a        device uint8 [M, k_in]
+ *   d_row_scales  device float [M], or NULL: in_scale is the scale of every row
+ *   g, u = row scale * scale[row] * (x codes . weight codes); the rest as
+ *   moe_fp8_w8a8_gemm, d_workspace unused.  A NaN code in a token's row gives
+ *   NaN codes in its H rows, and in no other.
+ * Errors: those of moe_fp8_w8a8_gemm; WQ_ERR_INVALID for the DOWN stage.
+ */
+wq_status moe_fp8_codes_gemm(const wq_moe_gemm_desc* d, const float* d_row_scales, float in_scale, float out_scale,
+                             void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* 2:4-sparse W4A16 linear layer                                             */
 /* ------------------------------------------------------------------------ */
@@ -432,6 +447,35 @@ wq_status dense_w4a16_gemm(const void* d_x, int M, int K, int N, const void* d_w
                            size_t workspace_bytes, void* stream);
 wq_status dense_w8a16_gemm(const void* d_x, int M, int K, int N, const void* d_w_packed, const void* d_scales,
                            void* d_y, int act_dtype, void* d_workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Low-rank adapters beside the dense linear layer                           */
+/* ------------------------------------------------------------------------ */
+/*
+ * The adapters of many requests at once, added to the output of the shared
+ * projection (dense_w4a16_gemm, dense_w8a16_gemm or any other), in place:
+ *   y[m, n] += scales[a] * sum_r B_a[n, r] (sum_k A_a[r, k] x[m, k]),
+ *   a = adapter_ids[m]; rows whose id is outside [0, adapters) stay as they are
+ * Both sums are fp32, the inner one (the intermediate of R values per row) is
+ * not rounded to 16 bits; y is rounded once more.  Each row takes its own
+ * adapter's values only: infinities or NaN in another adapter or row do not
+ * reach it.  Rows of one adapter next to each other (a prompt) share one read
+ * of its weights; no order is asked for.
+ *   d_x [M, K], d_y [M, N] act dtype, row strides in elements (multiples of 8:
+ *     y may be a column range of a wider projection's output)
+ *   d_adapter_ids device int32 [M]
+ *   d_a [adapters, R, K], d_b [adapters, N, R] act dtype: adapters of lower rank
+ *     are padded with zeros in both; d_scales device float [adapters], NULL for ones
+ *   d_workspace: dense_lora_workspace_bytes() bytes (every value read from it
+ *     is written first, by the same call)
+ * Limits: K, N, R multiples of 8; M, N <= 2^24, R <= 1024.  y must not overlap
+ * any input or the workspace.  Calls sharing a workspace must be stream-ordered.
+ */
+size_t dense_lora_workspace_bytes(int M, int K, int N, int R, int adapters);
+wq_status dense_lora_gemm(const void* d_x, int64_t x_stride, int M, int K, int N, int R, int adapters,
+                          const int32_t* d_adapter_ids, const void* d_a, const void* d_b, const float* d_scales,
+                          void* d_y, int64_t y_stride, int act_dtype, void* d_workspace, size_t workspace_bytes,
+                          void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* ExpertsInt8 quantization at load time                                     */

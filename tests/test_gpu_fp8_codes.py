@@ -1,0 +1,179 @@
+"""moe_fp8_codes_gemm and the layer on E4M3 rows: against moe_fp8_w8a8_gemm on
+the same codes bit for bit (the kernels and their sums are the same), and the
+chain rms_norm -> router -> FP8 layer against a plain float64 form within the
+layer's float tolerance."""
+import numpy as np
+import pytest
+
+import gen
+import weight_only_quantized_topk_amd as wq
+from tests.gpu_common import need_gpu, say, torch
+from tests.helpers import assert_close_fp
+from tests.serving_ref import e4m3_values, rms_norm, route
+
+pytestmark = pytest.mark.gpu
+
+SPEC = gen.CFG_FP8.with_(name="fp8-codes", E=8, topk=2, K=512, N=384)
+_made = {}
+
+
+def setup():
+    if not _made:
+        wts = gen.make_fp8_weights(SPEC, seed_config=1501)
+        _made["it"] = wts, wq.pack_moe_fp8(wts.w1, wts.s1, wts.w2, wts.s2, torch.bfloat16, SPEC.a1, SPEC.a2)
+    return _made["it"]
+
+
+def batch(M, seed):
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 256, (M, SPEC.K)).astype(np.uint8)
+    codes[(codes & 0x7F) >= 0x70] &= 0x8F  # no NaN, and nothing above 28
+    ids = np.stack([rng.permutation(SPEC.E)[:SPEC.topk] for _ in range(M)]).astype(np.int32)
+    return codes, torch.from_numpy(ids).cuda()
+
+
+def call(stage, p, x, row_scales, ids, bs, in_scale):
+    """The stage on codes (uint8) or on 16-bit values."""
+    M = x.shape[0]
+    cap = wq.moe_align_capacity(M, SPEC.topk, SPEC.E, bs)
+    st, ex, nt = wq.moe_align(ids, SPEC.E, bs, cap)
+    out = (torch.zeros((cap, SPEC.N), dtype=torch.uint8, device="cuda") if stage == wq.WQ_STAGE_GATE_UP
+           else torch.zeros((M * SPEC.topk, 2 * SPEC.N), device="cuda"))
+    common = (M, SPEC.topk, SPEC.E, 2 * SPEC.N, SPEC.K, p.w1, p.s1, st, ex, nt, cap, bs)
+    if x.dtype == torch.uint8:
+        wq.moe_fp8_codes_gemm(stage, x, row_scales, *common, out, in_scale=in_scale, out_scale=SPEC.a2)
+    else:
+        ws = wq.moe_fp8_gemm_workspace_bytes(stage, M, SPEC.topk, SPEC.E, 2 * SPEC.N, SPEC.K)
+        work = torch.empty(ws, dtype=torch.uint8, device="cuda")
+        wq.moe_fp8_w8a8_gemm(stage, x, *common, None, out, work, in_scale, SPEC.a2)
+    torch.cuda.synchronize()
+    return out, st
+
+
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+@pytest.mark.parametrize("M", [1, 2, 16, 77, 300])
+def test_equals_the_quantising_call(M, bs):
+    """Rows with scales 2^-4 .. 2^-2: each row has the bits of the quantising call with that scale on codes * scale
+    (exact in bf16); one scale for all likewise."""
+    need_gpu()
+    wts, p = setup()
+    codes, ids = batch(M, M + bs)
+    dev = torch.from_numpy(codes).cuda()
+    value = torch.from_numpy(e4m3_values(codes)).cuda()
+    which = np.arange(M) % 3
+    scales = np.float32([2.0 ** -4, 2.0 ** -3, 2.0 ** -2])
+    rows = torch.from_numpy(scales[which]).cuda()
+    for stage in (wq.WQ_STAGE_GATE_UP, wq.WQ_STAGE_RAW):
+        say("codes", M, bs, stage)
+        got, st = call(stage, p, dev, rows, ids, bs, 1.0)
+        token = np.minimum(st.cpu().numpy() // SPEC.topk, M) if stage == wq.WQ_STAGE_GATE_UP else np.arange(M * SPEC.topk) // SPEC.topk
+        for k, s in enumerate(scales):
+            ref, _ = call(stage, p, (value * float(s)).bfloat16(), None, ids, bs, float(s))
+            one, _ = call(stage, p, dev, None, ids, bs, float(s))
+            of = torch.from_numpy(np.append(which, -1)[token] == k).cuda()
+            if M > 1 or stage == wq.WQ_STAGE_RAW:
+                assert torch.equal(one, ref) and torch.equal(got[of], ref[of])
+            else:  # one token: the quantising call has a launch shape of its own, whose sums may round apart
+                d = np.abs(e4m3_values(one.cpu().numpy()) - e4m3_values(ref.cpu().numpy()))
+                assert (d <= np.abs(e4m3_values(ref.cpu().numpy())) / 8 + 2.0 ** -9).all()
+                assert torch.equal(one[of], got[of])
+        if stage == wq.WQ_STAGE_GATE_UP:
+            pad = torch.from_numpy(token == M).cuda()
+            assert not bool(got[pad].any())
+
+
+@pytest.mark.parametrize("bs", [16, 128])
+def test_nan_rows_stay_their_own(bs):
+    need_gpu()
+    wts, p = setup()
+    codes, ids = batch(40, 3)
+    rows = torch.full((40,), 0.125, device="cuda")
+    ref, st = call(wq.WQ_STAGE_GATE_UP, p, torch.from_numpy(codes).cuda(), rows, ids, bs, 1.0)
+    codes[7, 5] = 0x7F
+    rows[9] = float("nan")
+    got, _ = call(wq.WQ_STAGE_GATE_UP, p, torch.from_numpy(codes).cuda(), rows, ids, bs, 1.0)
+    token = np.minimum(st.cpu().numpy() // SPEC.topk, 40)
+    hit = torch.from_numpy((token == 7) | (token == 9)).cuda()
+    assert torch.equal(got[~hit], ref[~hit])
+    assert np.isnan(e4m3_values(got[hit].cpu().numpy())).all()
+
+
+def layer_plain(wts, x, w, ids):
+    """float64 FP8 layer on dequantised rows x (H quantised to E4M3 with a2)."""
+    W1 = e4m3_values(wts.w1) * wts.s1.reshape(SPEC.E, 2 * SPEC.N, 1)
+    W2 = e4m3_values(wts.w2) * wts.s2.reshape(SPEC.E, SPEC.K, 1)
+    out = np.zeros((x.shape[0], SPEC.K))
+    for m in range(x.shape[0]):
+        for j in range(ids.shape[1]):
+            z = W1[ids[m, j]] @ x[m]
+            h = z[:SPEC.N] / (1 + np.exp(-z[:SPEC.N])) * z[SPEC.N:]
+            q = torch.from_numpy((h / SPEC.a2).clip(-448, 448)).float().to(torch.float8_e4m3fn).double().numpy()
+            out[m] += w[m, j] * (W2[ids[m, j]] @ (q * SPEC.a2))
+    return out
+
+
+@pytest.mark.parametrize("quant", ["row", "static"])
+@pytest.mark.parametrize("M", [1, 5, 33, 200])
+def test_norm_router_layer(M, quant):
+    """rms_norm (residual, codes) -> logits of its 16-bit output -> grouped router -> FP8 layer, eager and captured."""
+    need_gpu()
+    wts, p = setup()
+    g = torch.Generator().manual_seed(M)
+    x = torch.randn((M, SPEC.K), generator=g).bfloat16().cuda()
+    r = torch.randn((M, SPEC.K), generator=g).bfloat16().cuda()
+    nw = (1 + 0.1 * torch.randn(SPEC.K, generator=g)).bfloat16().cuda()
+    gate = (torch.randn((SPEC.E, SPEC.K), generator=g) / SPEC.K ** 0.5).cuda()
+    router = wq.Router("sigmoid", 0.05 * torch.randn(SPEC.E, generator=g).cuda(), 4, 2, "top2", True, 2.5)
+    run = wq.Fp8MoERunner(p, M, SPEC.topk, router=router)
+
+    def step():
+        n = wq.rms_norm(x, nw, 1e-6, residual=r, quant=quant, scale=SPEC.a1 if quant == "static" else None)
+        logits = n.out.float() @ gate.t()
+        return n, logits, run((n.codes, n.scales), logits)
+
+    n, logits, out = step()
+    torch.cuda.synchronize()
+    w_ref, ids_ref = route(logits.double().cpu().numpy(), SPEC.topk, "sigmoid", router.bias.double().cpu().numpy(), 4, 2,
+                           "top2", True, 2.5)
+    assert np.array_equal(run.ids.cpu().numpy(), ids_ref)
+    rows = e4m3_values(n.codes.cpu().numpy()) * (n.scales.double().cpu().numpy()[:, None] if quant == "row" else SPEC.a1)
+    # the codes stand for the norm's output: half a step (2^-4) and the row's smallest step
+    _, y = rms_norm(x.double().cpu().numpy(), r.double().cpu().numpy(), nw.double().cpu().numpy(), 1e-6)
+    step_ = rows.max() if quant == "static" else n.scales.double().cpu().numpy()[:, None]
+    assert (np.abs(rows - y) <= np.abs(y) * 0.0626 + (SPEC.a1 if quant == "static" else step_) * 2.0 ** -10).all()
+    assert_close_fp(out.float().cpu().numpy(), layer_plain(wts, rows, w_ref, ids_ref), "chain M=%d" % M)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()[2]
+    for k in range(4):
+        x.copy_(torch.roll(x, 1, 1))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = held.clone()
+        assert torch.equal(got, step()[2])
+
+
+def test_layers_with_a_router():
+    """fused_moe and fused_moe_fp8 with a router: its ids and weights in the 16-bit layers too."""
+    need_gpu()
+    spec = gen.CFG2.with_(name="w8-router", E=16, topk=4, K=256, N=128)
+    wts = gen.make_moe_weights(spec, seed_config=1502)
+    p = wq.pack_moe(8, wts.w1q, wts.s1, wts.w2q, wts.s2, torch.bfloat16, -1)
+    bias = torch.linspace(-0.1, 0.1, 16)
+    for M in (1, 3, 64, 300):
+        x = torch.randn((M, 256)).bfloat16().cuda()
+        logits = torch.randn((M, 16)).bfloat16()
+        how = dict(scoring="sigmoid", n_group=4, topk_group=2, group_score="top2", routed_scale=2.5)
+        out, aux = wq.fused_moe(x, logits.cuda(), p, 4, keep=True, router=wq.Router(bias=bias.cuda(), **how))
+        torch.cuda.synchronize()
+        w, ids = route(logits.double().numpy(), 4, bias=bias.double().numpy(), **how)
+        assert np.array_equal(aux["topk_ids"].cpu().numpy(), ids)
+        import oracle
+        ref = oracle.moe_layer_from_weights(wts, x.float().cpu().numpy(), w.astype(np.float32), ids)["out"]
+        assert_close_fp(out.float().cpu().numpy(), ref, "router layer M=%d" % M)

@@ -157,3 +157,120 @@ def test_rms_norm_binding_refusals():
     for change in bad_type:
         with pytest.raises(TypeError):
             wq.rms_norm(x, change.pop("weight", w), **change)
+
+
+# ---------------------------------------------------------------------------
+# moe_fp8_codes_gemm
+# ---------------------------------------------------------------------------
+def codes_desc(**k):
+    d = wq.ops.WqMoeGemmDesc()
+    d.struct_size = C.sizeof(d)
+    v = dict(stage=0, act_dtype=BF, M=4, topk=2, E=8, n_out=256, k_in=256, group_size=-1, capacity=128, block_size=16,
+             d_a=FAKE, d_w_packed=FAKE, d_scales=FAKE, d_sorted_token_ids=FAKE, d_expert_ids=FAKE,
+             d_num_tokens_post_padded=FAKE, d_out=FAKE)
+    v.update(k)
+    for n, x in v.items():
+        setattr(d, n, x)
+    return C.byref(d)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(stage=1), INV), (dict(stage=5), INV), (dict(k_in=200), UNS), (dict(n_out=250), UNS), (dict(d_a=None), INV),
+    (dict(d_a=FAKE + 1), INV), (dict(block_size=24), UNS), (dict(capacity=16), INV), (dict(topk=9), INV),
+    (dict(d_k_perm=FAKE), INV)])
+def test_codes_gemm_refusals(change, want):
+    assert status("moe_fp8_codes_gemm", codes_desc(**change), at(), 1.0, 1.0, None)[0] == want
+
+
+def test_codes_gemm_scales():
+    for rows, one, out in ((None, 0.0, 1.0), (None, float("nan"), 1.0), (None, -1.0, 1.0), (at(), 1.0, 0.0),
+                           (at(), 1.0, float("inf")), (at(4), 1.0, 1.0)):
+        assert status("moe_fp8_codes_gemm", codes_desc(), rows, one, out, None)[0] == INV
+    assert status("moe_fp8_codes_gemm", None, None, 1.0, 1.0, None)[0] == INV
+    assert status("moe_fp8_codes_gemm", codes_desc(M=0), at(), 1.0, 1.0, None)[0] == wq.WQ_OK
+
+
+def test_codes_gemm_binding_refusals():
+    i32 = torch.zeros(128, dtype=torch.int32)
+
+    def call(codes=torch.zeros((4, 256), dtype=torch.uint8), rows=torch.ones(4),
+             out=torch.zeros((128, 128), dtype=torch.uint8), stage=wq.WQ_STAGE_GATE_UP):
+        wq.moe_fp8_codes_gemm(stage, codes, rows, 4, 2, 8, 256, 256, i32, i32, i32, i32, i32, 128, 16, out)
+
+    for change in (dict(codes=torch.zeros((4, 255), dtype=torch.uint8)), dict(rows=torch.ones(5)),
+                   dict(out=torch.zeros((64, 128), dtype=torch.uint8)),
+                   dict(stage=wq.WQ_STAGE_RAW, out=torch.zeros((8, 128))),
+                   dict(codes=torch.zeros((4, 512), dtype=torch.uint8)[:, :256])):
+        with pytest.raises(ValueError):
+            call(**change)
+    for change in (dict(codes=torch.zeros((4, 256), dtype=torch.bfloat16)), dict(rows=torch.ones(4).double()),
+                   dict(out=torch.zeros((128, 128)))):
+        with pytest.raises(TypeError):
+            call(**change)
+
+
+# ---------------------------------------------------------------------------
+# dense_lora_gemm
+# ---------------------------------------------------------------------------
+def lora_args(**k):
+    d = dict(x=at(), xs=512, M=4, K=512, N=256, R=16, L=3, ids=at(MB), a=at(2 * MB), b=at(3 * MB), s=at(4 * MB),
+             y=at(5 * MB), ys=256, dt=BF, ws=at(6 * MB), wsb=1 << 24)
+    d.update(k)
+    return [d[n] for n in ("x", "xs", "M", "K", "N", "R", "L", "ids", "a", "b", "s", "y", "ys", "dt", "ws", "wsb")] + [None]
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(dt=2), INV), (dict(M=-1), INV), (dict(K=0), INV), (dict(N=-8), INV), (dict(R=0), INV), (dict(L=0), INV),
+    (dict(K=508), UNS), (dict(N=252), UNS), (dict(R=12), UNS), (dict(R=1032), UNS), (dict(M=(1 << 24) + 1), UNS),
+    (dict(xs=504), INV), (dict(ys=0), INV), (dict(xs=516), UNS), (dict(ys=260), UNS), (dict(wsb=64), INV),
+    (dict(x=None), INV), (dict(ids=None), INV), (dict(a=None), INV), (dict(b=at(2)), INV), (dict(s=at(4)), INV),
+    (dict(y=None), INV), (dict(ws=None), INV),
+    # overlaps
+    (dict(y=at()), INV), (dict(y=at(MB)), INV), (dict(y=at(2 * MB)), INV), (dict(y=at(6 * MB)), INV),
+    (dict(ws=at(3 * MB)), INV), (dict(ws=at()), INV), (dict(y=at(16)), INV)])
+def test_lora_refusals(change, want):
+    assert status("dense_lora_gemm", *lora_args(**change))[0] == want
+
+
+def test_lora_workspace_and_empty():
+    L = wq.load()
+    assert L.dense_lora_workspace_bytes(0, 512, 256, 16, 3) == 0
+    assert L.dense_lora_workspace_bytes(4, 500, 256, 16, 3) == 0
+    assert L.dense_lora_workspace_bytes(4, 512, 256, 16, 3) >= 4 * 16 * 4
+    need = L.dense_lora_workspace_bytes(4, 512, 256, 16, 3)
+    assert status("dense_lora_gemm", *lora_args(wsb=need - 1))[0] == INV
+    assert status("dense_lora_gemm", *lora_args(M=0, x=None, y=None, ids=None, ws=None, wsb=0))[0] == wq.WQ_OK
+    # y in the gaps of x's rows (one buffer) passes the host's checks
+    st, msg = status("dense_lora_gemm", *lora_args(xs=1024, y=at(1024), ys=1024))
+    assert st in (wq.WQ_ERR_DEVICE, wq.WQ_ERR_HIP), msg
+
+
+def test_lora_binding_refusals():
+    bf = torch.bfloat16
+    x, y = torch.zeros((4, 512), dtype=bf), torch.zeros((4, 256), dtype=bf)
+    ids, s = torch.zeros(4, dtype=torch.int32), torch.ones(3)
+    a, b = torch.zeros((3, 16, 512), dtype=bf), torch.zeros((3, 256, 16), dtype=bf)
+    good = dict(x=x, adapter_ids=ids, a=a, b=b, scales=s, y=y)
+    for change in (dict(x=x[0]), dict(a=a[0]), dict(b=b[:2]), dict(a=torch.zeros((3, 16, 504), dtype=bf)), dict(y=y[:3]),
+                   dict(adapter_ids=ids[:3]), dict(scales=s[:2]), dict(y=torch.zeros((4, 512), dtype=bf)[:, ::2]),
+                   dict(b=torch.zeros((3, 16, 256), dtype=bf).transpose(1, 2)), dict(x=x.float()),
+                   dict(workspace=torch.zeros((64, 2), dtype=torch.uint8)[:, 0])):
+        with pytest.raises(ValueError):
+            wq.dense_lora_gemm(**{**good, **change})
+    for change in (dict(y=y.half()), dict(a=a.half()), dict(adapter_ids=ids.long()), dict(scales=s.to(bf))):
+        with pytest.raises(TypeError):
+            wq.dense_lora_gemm(**{**good, **change})
+
+
+def test_pack_lora():
+    low = [(torch.randn(r, 64), torch.randn(32, r), 0.5 * r) for r in (3, 8, 20)]
+    a, b, s = wq.pack_lora(low, torch.bfloat16, device="cpu")
+    assert a.shape == (3, 24, 64) and b.shape == (3, 32, 24) and s.tolist() == [1.5, 4.0, 10.0]
+    for i, (A, B, _) in enumerate(low):
+        r = A.shape[0]
+        assert torch.equal(a[i, :r], A.bfloat16()) and torch.equal(b[i, :, :r], B.bfloat16())
+        assert not a[i, r:].any() and not b[i, :, r:].any()
+    for bad in ([], [(torch.randn(3, 64), torch.randn(32, 4), 1.0)],
+                [(torch.randn(3, 64), torch.randn(32, 3), 1.0), (torch.randn(3, 65), torch.randn(32, 3), 1.0)]):
+        with pytest.raises(ValueError):
+            wq.pack_lora(bad, torch.bfloat16, device="cpu")

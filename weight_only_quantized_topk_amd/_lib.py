@@ -24,9 +24,10 @@ EXPORTS = (
     "moe_gemm_workspace_bytes", "moe_w4a16_gemm", "moe_w8a16_gemm", "moe_w8a16_gemm_noalloc",
     "sparse24_w4a16_gemm", "sparse24_w8a16_gemm", "wq_quantize_w8",
     "dense_gemm_workspace_bytes", "dense_w4a16_gemm", "dense_w8a16_gemm",
+    "dense_lora_workspace_bytes", "dense_lora_gemm",
     "wq_pack_w4_bytes", "wq_pack_w8_bytes", "wq_pack_w4", "wq_pack_w8",
     "wq_pack_sparse24_vals_bytes", "wq_pack_sparse24_meta_bytes", "wq_pack_sparse24",
-    "moe_fp8_gemm_workspace_bytes", "moe_fp8_w8a8_gemm", "wq_pack_fp8_bytes", "wq_pack_fp8",
+    "moe_fp8_gemm_workspace_bytes", "moe_fp8_w8a8_gemm", "moe_fp8_codes_gemm", "wq_pack_fp8_bytes", "wq_pack_fp8",
 )
 
 
@@ -104,6 +105,9 @@ def load():
     L.dense_gemm_workspace_bytes.restype = sz
     L.dense_w4a16_gemm.argtypes = [p, i, i, i, p, p, i, p, p, i, p, sz, p]
     L.dense_w8a16_gemm.argtypes = [p, i, i, i, p, p, p, i, p, sz, p]
+    L.dense_lora_workspace_bytes.argtypes = [i, i, i, i, i]
+    L.dense_lora_workspace_bytes.restype = sz
+    L.dense_lora_gemm.argtypes = [p, i64, i, i, i, i, i, p, p, p, p, p, i64, i, p, sz, p]
     L.wq_pack_w4_bytes.argtypes = [i, i, i]
     L.wq_pack_w4_bytes.restype = sz
     L.wq_pack_w8_bytes.argtypes = [i, i, i]
@@ -118,6 +122,7 @@ def load():
     L.moe_fp8_gemm_workspace_bytes.argtypes = [i, i, i, i, i, i]
     L.moe_fp8_gemm_workspace_bytes.restype = sz
     L.moe_fp8_w8a8_gemm.argtypes = [C.POINTER(WqMoeGemmDesc), C.c_float, C.c_float, p]
+    L.moe_fp8_codes_gemm.argtypes = [C.POINTER(WqMoeGemmDesc), p, f, f, p]
     L.wq_pack_fp8_bytes.argtypes = [i, i, i]
     L.wq_pack_fp8_bytes.restype = sz
     L.wq_pack_fp8.argtypes = [i, i, i, p, p, p, i, p, p]
@@ -125,8 +130,8 @@ def load():
               "moe_route_grouped_align", "wq_rms_norm", "moe_w4a16_gemm", "moe_w8a16_gemm",
               "moe_w8a16_gemm_noalloc", "sparse24_w4a16_gemm",
               "sparse24_w8a16_gemm",
-              "wq_quantize_w8", "dense_w4a16_gemm", "dense_w8a16_gemm", "wq_pack_w4",
-              "wq_pack_w8", "wq_pack_sparse24", "moe_fp8_w8a8_gemm", "wq_pack_fp8"):
+              "wq_quantize_w8", "dense_w4a16_gemm", "dense_w8a16_gemm", "dense_lora_gemm", "wq_pack_w4",
+              "wq_pack_w8", "wq_pack_sparse24", "moe_fp8_w8a8_gemm", "moe_fp8_codes_gemm", "wq_pack_fp8"):
         getattr(L, fn).restype = i
     _lib = L
     return L

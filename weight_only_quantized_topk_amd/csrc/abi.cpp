@@ -752,14 +752,17 @@ size_t moe_fp8_gemm_workspace_bytes(int stage, int M, int topk, int E, int n_out
     return 0;
 }
 
-static wq_status fp8_gemm(const wq_moe_gemm_desc* d, float in_scale, float out_scale, void* stream) {
-    const char* who = "moe_fp8_w8a8_gemm";
+// codes: d_a holds E4M3 codes of x, with a scale per row (row_scales) or
+// in_scale for all; nothing is quantised and no workspace is needed
+static wq_status fp8_gemm(const wq_moe_gemm_desc* d, float in_scale, float out_scale, void* stream, const char* who,
+                          bool codes = false, const float* row_scales = nullptr) {
     WQ_REQUIRE(d != nullptr, WQ_ERR_INVALID, "%s: desc is NULL", who);
     WQ_REQUIRE(d->struct_size >= sizeof(wq_moe_gemm_desc), WQ_ERR_INVALID, "%s: struct_size %zu < %zu", who,
                d->struct_size, sizeof(wq_moe_gemm_desc));
     const int stage = d->stage;
     WQ_REQUIRE(stage == WQ_STAGE_GATE_UP || stage == WQ_STAGE_DOWN || stage == WQ_STAGE_RAW, WQ_ERR_INVALID,
                "%s: bad stage %d", who, stage);
+    WQ_REQUIRE(!codes || stage != WQ_STAGE_DOWN, WQ_ERR_INVALID, "%s: the DOWN stage takes moe_fp8_w8a8_gemm", who);
     WQ_REQUIRE(d->act_dtype == WQ_F16 || d->act_dtype == WQ_BF16, WQ_ERR_INVALID, "%s: bad act dtype", who);
     WQ_REQUIRE(d->M >= 0 && d->topk >= 1 && d->E >= 1 && d->topk <= d->E, WQ_ERR_INVALID,
                "%s: bad M/topk/E (%d/%d/%d)", who, d->M, d->topk, d->E);
@@ -772,7 +775,7 @@ static wq_status fp8_gemm(const wq_moe_gemm_desc* d, float in_scale, float out_s
                "%s: n_out %d not a multiple of %d", who, d->n_out, stage == WQ_STAGE_GATE_UP ? 32 : 16);
     WQ_REQUIRE(d->group_size == -1, WQ_ERR_UNSUPPORTED, "%s: FP8 weights take per-column scales (-1)", who);
     WQ_REQUIRE(d->d_k_perm == nullptr, WQ_ERR_INVALID, "%s: no act-order for FP8 weights", who);
-    WQ_REQUIRE(std::isfinite(in_scale) && in_scale > 0.0f, WQ_ERR_INVALID, "%s: in_scale must be finite and > 0",
+    WQ_REQUIRE(row_scales || (std::isfinite(in_scale) && in_scale > 0.0f), WQ_ERR_INVALID, "%s: in_scale must be finite and > 0",
                who);
     WQ_REQUIRE(stage != WQ_STAGE_GATE_UP || (std::isfinite(out_scale) && out_scale > 0.0f), WQ_ERR_INVALID,
                "%s: out_scale must be finite and > 0", who);
@@ -781,7 +784,7 @@ static wq_status fp8_gemm(const wq_moe_gemm_desc* d, float in_scale, float out_s
     WQ_REQUIRE(d->capacity >= need_cap && d->capacity % (size_t)d->block_size == 0 &&
                    d->capacity <= (size_t)0x7fffffff,
                WQ_ERR_INVALID, "%s: capacity %zu (need >= %zu, multiple of block_size)", who, d->capacity, need_cap);
-    const size_t ws = moe_fp8_gemm_workspace_bytes(stage, d->M, d->topk, d->E, d->n_out, d->k_in);
+    const size_t ws = codes ? 0 : moe_fp8_gemm_workspace_bytes(stage, d->M, d->topk, d->E, d->n_out, d->k_in);
     WQ_REQUIRE(d->workspace_bytes >= ws, WQ_ERR_INVALID, "%s: workspace %zu < required %zu", who, d->workspace_bytes,
                ws);
     const bool large = wq::fp8_prefill_supported(d->n_out, d->k_in, d->block_size);
@@ -798,7 +801,8 @@ static wq_status fp8_gemm(const wq_moe_gemm_desc* d, float in_scale, float out_s
     WQ_TRY(check_ptr(d->d_num_tokens_post_padded, "num_tokens_post_padded"));
     WQ_TRY(check_ptr(d->d_out, "out"));
     if (stage == WQ_STAGE_DOWN) WQ_TRY(check_ptr(d->d_topk_weights, "topk_weights"));
-    WQ_TRY(check_ptr(d->d_workspace, "workspace"));
+    if (!codes) WQ_TRY(check_ptr(d->d_workspace, "workspace"));
+    if (row_scales) WQ_TRY(check_ptr(row_scales, "row_scales"));
     WQ_TRY(check_dev(d->d_a, "a"));
     WQ_TRY(check_dev(d->d_w_packed, "w_packed"));
     WQ_TRY(check_dev(d->d_scales, "scales"));
@@ -807,7 +811,8 @@ static wq_status fp8_gemm(const wq_moe_gemm_desc* d, float in_scale, float out_s
     WQ_TRY(check_dev(d->d_num_tokens_post_padded, "num_tokens_post_padded"));
     WQ_TRY(check_dev(d->d_out, "out"));
     if (stage == WQ_STAGE_DOWN) WQ_TRY(check_dev(d->d_topk_weights, "topk_weights"));
-    WQ_TRY(check_dev(d->d_workspace, "workspace"));
+    if (!codes) WQ_TRY(check_dev(d->d_workspace, "workspace"));
+    if (row_scales) WQ_TRY(check_dev(row_scales, "row_scales"));
 
     hipStream_t s = (hipStream_t)stream;
     const bool bf16 = d->act_dtype == WQ_BF16;
@@ -828,7 +833,12 @@ static wq_status fp8_gemm(const wq_moe_gemm_desc* d, float in_scale, float out_s
     g.cap = (int)d->capacity;
     g.in_scale = in_scale;
     g.out_scale = out_scale;
-    if (stage == WQ_STAGE_DOWN) {
+    if (codes) {
+        g.a = static_cast<const uint8_t*>(d->d_a);
+        g.a_direct = 0;
+        g.x_codes = 1;
+        g.row_scales = row_scales;
+    } else if (stage == WQ_STAGE_DOWN) {
         g.a = static_cast<const uint8_t*>(d->d_a);  // H codes in sorted order
         g.a_direct = 1;
         if (wq::fp8_down_combine_supported(d->M, d->topk, d->n_out, d->k_in)) {
@@ -859,9 +869,18 @@ static wq_status fp8_gemm(const wq_moe_gemm_desc* d, float in_scale, float out_s
 
 wq_status moe_fp8_w8a8_gemm(const wq_moe_gemm_desc* d, float in_scale, float out_scale, void* stream) {
     try {
-        return fp8_gemm(d, in_scale, out_scale, stream);
+        return fp8_gemm(d, in_scale, out_scale, stream, "moe_fp8_w8a8_gemm");
     } catch (...) {
         return fail(WQ_ERR_HIP, "moe_fp8_w8a8_gemm: unexpected exception");
+    }
+}
+
+wq_status moe_fp8_codes_gemm(const wq_moe_gemm_desc* d, const float* d_row_scales, float in_scale, float out_scale,
+                             void* stream) {
+    try {
+        return fp8_gemm(d, in_scale, out_scale, stream, "moe_fp8_codes_gemm", true, d_row_scales);
+    } catch (...) {
+        return fail(WQ_ERR_HIP, "moe_fp8_codes_gemm: unexpected exception");
     }
 }
 
@@ -1070,6 +1089,95 @@ wq_status dense_w8a16_gemm(const void* d_x, int M, int K, int N, const void* d_w
                           workspace_bytes, stream, "dense_w8a16_gemm");
     } catch (...) {
         return fail(WQ_ERR_HIP, "dense_w8a16_gemm: unexpected exception");
+    }
+}
+
+// ---------------------------------------------------------------------------
+static const char* lora_sizes(int M, int K, int N, int R, int adapters) {
+    if (M < 0 || K <= 0 || N <= 0 || R <= 0 || adapters <= 0) return "sizes must be positive (M >= 0)";
+    if (M > MAX_PAIRS || N > (1 << 24) || R > 1024) return "M or N > 2^24, or rank > 1024";
+    if (K % 8 || N % 8 || R % 8) return "K, N and the rank must be multiples of 8";
+    return nullptr;
+}
+
+size_t dense_lora_workspace_bytes(int M, int K, int N, int R, int adapters) {
+    if (M == 0 || lora_sizes(M, K, N, R, adapters)) return 0;
+    return round256((size_t)wq::lora_k_slices(M, K, R) * M * R * sizeof(float));
+}
+
+wq_status dense_lora_gemm(const void* d_x, int64_t x_stride, int M, int K, int N, int R, int adapters,
+                          const int32_t* d_adapter_ids, const void* d_a, const void* d_b, const float* d_scales,
+                          void* d_y, int64_t y_stride, int act_dtype, void* d_workspace, size_t workspace_bytes,
+                          void* stream) {
+    try {
+        const char* who = "dense_lora_gemm";
+        WQ_REQUIRE(act_dtype == WQ_F16 || act_dtype == WQ_BF16, WQ_ERR_INVALID, "%s: bad act dtype", who);
+        WQ_REQUIRE(M >= 0 && K > 0 && N > 0 && R > 0 && adapters > 0, WQ_ERR_INVALID,
+                   "%s: bad sizes M %d K %d N %d rank %d adapters %d", who, M, K, N, R, adapters);
+        const char* bad = lora_sizes(M, K, N, R, adapters);
+        WQ_REQUIRE(!bad, WQ_ERR_UNSUPPORTED, "%s: %s", who, bad);
+        if (M == 0) return ok();
+        const int64_t most = INT64_MAX / 4 / M;
+        WQ_REQUIRE(x_stride >= K && x_stride <= most, WQ_ERR_INVALID, "%s: x row stride %lld (K %d)", who,
+                   (long long)x_stride, K);
+        WQ_REQUIRE(y_stride >= N && y_stride <= most, WQ_ERR_INVALID, "%s: y row stride %lld (N %d)", who,
+                   (long long)y_stride, N);
+        WQ_REQUIRE(x_stride % 8 == 0 && y_stride % 8 == 0, WQ_ERR_UNSUPPORTED,
+                   "%s: row strides must be multiples of 8 (%lld, %lld)", who, (long long)x_stride,
+                   (long long)y_stride);
+        const size_t need = dense_lora_workspace_bytes(M, K, N, R, adapters);
+        WQ_REQUIRE(workspace_bytes >= need, WQ_ERR_INVALID, "%s: workspace %zu < required %zu", who, workspace_bytes,
+                   need);
+        struct Flat {
+            const void* p;
+            size_t bytes;
+            const char* name;
+        };
+        const Flat flat[5] = {{d_adapter_ids, (size_t)M * 4, "adapter_ids"},
+                              {d_a, (size_t)adapters * R * K * 2, "a"},
+                              {d_b, (size_t)adapters * N * R * 2, "b"},
+                              {d_scales, (size_t)adapters * 4, "scales"},
+                              {d_workspace, need, "workspace"}};
+        WQ_TRY(check_ptr(d_x, "x"));
+        WQ_TRY(check_ptr(d_y, "y"));
+        for (const Flat& f : flat)
+            if (f.p || &f != &flat[3]) WQ_TRY(check_ptr(f.p, f.name));
+        WQ_REQUIRE(!rows_overlap(d_x, x_stride * 2, (int64_t)K * 2, d_y, y_stride * 2, (int64_t)N * 2, M),
+                   WQ_ERR_INVALID, "%s: y overlaps x", who);
+        const int64_t x_span = ((M - 1) * x_stride + K) * 2, y_span = ((M - 1) * y_stride + N) * 2;
+        for (const Flat& f : flat)
+            WQ_REQUIRE(!f.p || !rows_overlap(d_y, 0, y_span, f.p, 0, (int64_t)f.bytes, 1), WQ_ERR_INVALID,
+                       "%s: y overlaps %s", who, f.name);
+        for (int i = 0; i < 4; ++i)
+            WQ_REQUIRE(!flat[i].p || !rows_overlap(d_workspace, 0, (int64_t)need, flat[i].p, 0,
+                                                   (int64_t)flat[i].bytes, 1),
+                       WQ_ERR_INVALID, "%s: the workspace overlaps %s", who, flat[i].name);
+        WQ_REQUIRE(!rows_overlap(d_workspace, 0, (int64_t)need, d_x, 0, x_span, 1), WQ_ERR_INVALID,
+                   "%s: the workspace overlaps x", who);
+        WQ_TRY(check_dev(d_x, "x"));
+        WQ_TRY(check_dev(d_y, "y"));
+        for (const Flat& f : flat)
+            if (f.p) WQ_TRY(check_dev(f.p, f.name));
+        wq::LoraArgs g{};
+        g.x = static_cast<const uint16_t*>(d_x);
+        g.ids = d_adapter_ids;
+        g.a = static_cast<const uint16_t*>(d_a);
+        g.b = static_cast<const uint16_t*>(d_b);
+        g.scales = d_scales;
+        g.y = static_cast<uint16_t*>(d_y);
+        g.t = static_cast<float*>(d_workspace);
+        g.x_stride = x_stride;
+        g.y_stride = y_stride;
+        g.M = M;
+        g.K = K;
+        g.N = N;
+        g.R = R;
+        g.adapters = adapters;
+        g.ks = wq::lora_k_slices(M, K, R);
+        wq::launch_lora(g, act_dtype == WQ_BF16, (hipStream_t)stream);
+        return after_launch(who);
+    } catch (...) {
+        return fail(WQ_ERR_HIP, "dense_lora_gemm: unexpected exception");
     }
 }
 

@@ -56,6 +56,26 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return (uint32_t)w;
 }
 
+// the scale of a pair's A row: its token's own (x codes that the caller
+// quantised row by row), or the tensor's
+template <int STAGE>
+__device__ __forceinline__ float a_row_scale(const Fp8GemmArgs& g, int pair, int T) {
+    if constexpr (STAGE != STAGE_DOWN) {
+        if (g.row_scales) return pair < T ? g.row_scales[pair / g.topk] : 0.0f;
+    }
+    return g.in_scale;
+}
+
+// H codes: e4m3x4, and a NaN code for a NaN where the caller's codes may hold one
+__device__ __forceinline__ uint32_t h_codes(const Fp8GemmArgs& g, const float (&h)[4]) {
+    uint32_t w = e4m3x4(h[0], h[1], h[2], h[3]);
+    if (g.x_codes) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w |= h[i] != h[i] ? 0x7Fu << (8 * i) : 0u;
+    }
+    return w;
+}
+
 __device__ __forceinline__ u32x8 cat8(const u32x4& lo, const u32x4& hi) {
     return u32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
@@ -201,6 +221,7 @@ __global__ __launch_bounds__(64 * NW) void fp8_decode_kernel(Fp8GemmArgs g) {
             const int r = item % R;
             const int p = (sb_first + s0 + r) * 16 + (lane & 15);
             const int pair = g.sorted[p];
+            const float a_scale = a_row_scale<STAGE>(g, pair, T);
             if constexpr (STAGE == STAGE_GATE_UP) {
                 const int tg = 2 * pp, tu = 2 * pp + 1;
                 f32x4 gv = red[0][tg][r][lane], uv = red[0][tu][r][lane];
@@ -214,12 +235,11 @@ __global__ __launch_bounds__(64 * NW) void fp8_decode_kernel(Fp8GemmArgs g) {
                 float h[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float gt = gv[i] * g.in_scale * se[(NT * unit + tg) * TILE_ROWS + rowq + i];
-                    const float up = uv[i] * g.in_scale * se[(NT * unit + tu) * TILE_ROWS + rowq + i];
+                    const float gt = gv[i] * a_scale * se[(NT * unit + tg) * TILE_ROWS + rowq + i];
+                    const float up = uv[i] * a_scale * se[(NT * unit + tu) * TILE_ROWS + rowq + i];
                     h[i] = pair < T ? __fdiv_rn(silu_f32(gt) * up, g.out_scale) : 0.0f;
                 }
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.out) + (size_t)p * N + hcol) =
-                    e4m3x4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.out) + (size_t)p * N + hcol) = h_codes(g, h);
             } else {
                 if (pair < T) {
                     f32x4 o = red[0][pp][r][lane];
@@ -228,7 +248,7 @@ __global__ __launch_bounds__(64 * NW) void fp8_decode_kernel(Fp8GemmArgs g) {
                     const int row = (NT * unit + pp) * TILE_ROWS + rowq;
                     const float rw = (STAGE == STAGE_DOWN) ? g.topk_w[pair] : 1.0f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = o[i] * g.in_scale * se[row + i] * rw;
+                    for (int i = 0; i < 4; ++i) o[i] = o[i] * a_scale * se[row + i] * rw;
                     *reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + (size_t)pair * g.n_out + row) = o;
                 }
             }
@@ -510,6 +530,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void fp8_prefill_kernel(Fp8GemmArgs g
     for (int j = 0; j < TJ; ++j) {
         const int p = row0 + 16 * j + brow;
         const int pair = g.sorted[p];
+        const float a_scale = a_row_scale<STAGE>(g, pair, T);
         if constexpr (STAGE == STAGE_GATE_UP) {
             const int N = g.n_out / 2;
 #pragma unroll
@@ -519,12 +540,11 @@ __global__ __launch_bounds__(NW * 64, OCC) void fp8_prefill_kernel(Fp8GemmArgs g
                 float h[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float gt = acc[2 * qq][j][r] * g.in_scale * se[gtile * TILE_ROWS + 4 * g4 + r];
-                    const float up = acc[2 * qq + 1][j][r] * g.in_scale * se[(gtile + 1) * TILE_ROWS + 4 * g4 + r];
+                    const float gt = acc[2 * qq][j][r] * a_scale * se[gtile * TILE_ROWS + 4 * g4 + r];
+                    const float up = acc[2 * qq + 1][j][r] * a_scale * se[(gtile + 1) * TILE_ROWS + 4 * g4 + r];
                     h[r] = (pair < T) ? __fdiv_rn(silu_f32(gt) * up, g.out_scale) : 0.0f;
                 }
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.out) + (size_t)p * N + hcol) =
-                    e4m3x4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.out) + (size_t)p * N + hcol) = h_codes(g, h);
             }
         } else {
             if (pair < T) {
@@ -534,7 +554,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void fp8_prefill_kernel(Fp8GemmArgs g
                     const int n0 = (rt0 + t) * TILE_ROWS + 4 * g4;
                     f32x4 o;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) o[r] = acc[t][j][r] * g.in_scale * se[n0 + r] * rw;
+                    for (int r = 0; r < 4; ++r) o[r] = acc[t][j][r] * a_scale * se[n0 + r] * rw;
                     *reinterpret_cast<f32x4*>(yslab + (size_t)pair * g.n_out + n0) = o;
                 }
             }

@@ -65,6 +65,22 @@ struct RmsNormArgs {
 };
 void launch_rms_norm(const RmsNormArgs& g, bool bf16, hipStream_t s);
 
+// low-rank adapters added to a dense projection's output (lora.hip); strides in elements
+struct LoraArgs {
+    const uint16_t* x;        // [M, K]
+    const int32_t* ids;       // [M], an adapter outside [0, adapters): none
+    const uint16_t* a;        // [adapters, R, K]
+    const uint16_t* b;        // [adapters, N, R]
+    const float* scales;      // [adapters], or null for ones
+    uint16_t* y;              // [M, N], added to
+    float* t;                 // workspace: [ks, M, R]
+    int64_t x_stride, y_stride;
+    int M, K, N, R, adapters;
+    int ks;                   // lora_k_slices(M, K, R)
+};
+int lora_k_slices(int M, int K, int R);
+void launch_lora(const LoraArgs& g, bool bf16, hipStream_t s);
+
 struct GemmArgs {
     const uint16_t* a;        // activations (x, gathered x, or H), 16-bit
     const uint8_t* w;         // packed weights, all experts
@@ -110,6 +126,9 @@ struct Fp8GemmArgs {
     float out_scale;          // GATE_UP: scale H is quantised with (a2)
     const uint16_t* x16;      // GATE_UP of one token: its 16-bit row, quantised in the kernel (a unused); else null
     int x_bf16;               // x16's type: 1 bf16, 0 fp16
+    // GATE_UP / RAW on codes that the caller quantised (moe_fp8_codes_gemm):
+    int x_codes;              // 1: and NaN results keep a NaN code in H
+    const float* row_scales;  // the tokens' own scales [M], or null: in_scale
 };
 
 // GATE_UP of one token on the small-batch kernel: x quantised inside the GEMM

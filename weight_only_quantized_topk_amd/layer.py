@@ -23,6 +23,29 @@ PREFILL_BLOCK_THIN = 64
 
 
 @dataclass
+class Router:
+    """How a layer routes, where the plain softmax of moe_route is not it: the
+    arguments of moe_route_grouped beside the logits and top-k."""
+    scoring: str = "softmax"
+    bias: Optional[object] = None  # float32 [E], on the device
+    n_group: int = 1
+    topk_group: int = 1
+    group_score: str = "max"
+    renormalize: bool = True
+    routed_scale: float = 1.0
+
+
+def _route_align(r, logits, stream):
+    """The routing arrays of a runner's batch (its buffers), by its router."""
+    if r.router is None:
+        ops.moe_route_align(logits, r.topk, r.renormalize, r.bs, r.w, r.ids, r.st, r.ex, r.nt, r.cap, stream=stream)
+    else:
+        ops.moe_route_grouped_align(logits, r.topk, r.bs, **vars(r.router), topk_weights=r.w, topk_ids=r.ids,
+                                    sorted_token_ids=r.st, expert_ids=r.ex, num_tokens_post_padded=r.nt,
+                                    capacity=r.cap, stream=stream)
+
+
+@dataclass
 class PackedMoE:
     bits: int
     E: int
@@ -100,12 +123,13 @@ def choose_block_size(M: int, topk: int, E: int, bits: int = 8) -> int:
 class MoERunner:
     """The hot path for one batch shape with every buffer allocated up front, so
     a call allocates nothing.  marks: optional 3 events recorded on the stream
-    after alignment, after GATE_UP and after DOWN (stage timing)."""
+    after alignment, after GATE_UP and after DOWN (stage timing).  router: the
+    scores, bias and groups to route with (renormalize is then the router's)."""
 
     def __init__(self, p: PackedMoE, M: int, topk: int, renormalize: bool = True, block_size: Optional[int] = None,
-                 device="cuda"):
+                 device="cuda", router: Optional[Router] = None):
         import torch
-        self.p, self.M, self.topk, self.renormalize = p, M, topk, renormalize
+        self.p, self.M, self.topk, self.renormalize, self.router = p, M, topk, renormalize, router
         self.bs = choose_block_size(M, topk, p.E, p.bits) if block_size is None else block_size
         self.cap = ops.moe_align_capacity(M, topk, p.E, self.bs)
         dev = torch.device(device)
@@ -123,14 +147,15 @@ class MoERunner:
         self.out = torch.empty((M, p.K), dtype=p.act, device=dev)
         # the smallest batches route inside the GATE_UP call (moe_route_gate_up: without act-order one launch,
         # with it the routing launch also gathers the permuted rows)
-        if act_order:
+        if router is not None:
+            self.route_in_gate_up = False
+        elif act_order:
             self.route_in_gate_up = 1 <= M <= 16 and M * topk <= 64 and p.E <= 64 and self.cap <= 1024
         else:
             self.route_in_gate_up = (M * topk <= 16 and p.E <= 64 and self.bs in (16, 32) and self.cap <= 1024)
 
     def route_align(self, logits, stream=None):
-        ops.moe_route_align(logits, self.topk, self.renormalize, self.bs, self.w, self.ids, self.st, self.ex,
-                            self.nt, self.cap, stream=stream)
+        _route_align(self, logits, stream)
 
     def route_gate_up(self, x, logits, stream=None):
         q = self.p
@@ -205,10 +230,10 @@ class MoERunner:
 
 
 def fused_moe(x, logits, p: PackedMoE, topk: int, renormalize: bool = True, block_size: Optional[int] = None,
-              stream=None, keep=False):
+              stream=None, keep=False, router: Optional[Router] = None):
     """x [M, K] act, logits [M, E] float32 -> out [M, K] act.  With keep=True also
     returns a dict of the intermediate device buffers."""
-    r = MoERunner(p, x.shape[0], topk, renormalize, block_size, device=x.device)
+    r = MoERunner(p, x.shape[0], topk, renormalize, block_size, device=x.device, router=router)
     out = r(x, logits, stream=stream)
     return (out, r.aux()) if keep else out
 
@@ -252,12 +277,14 @@ def pack_moe_fp8(w1: np.ndarray, s1: np.ndarray, w2: np.ndarray, s2: np.ndarray,
 class Fp8MoERunner:
     """The FP8 W8A8 hot path for one batch shape, buffers allocated up front:
     route -> align -> GATE_UP (x quantised with a1, H written as E4M3 codes of
-    h / a2) -> DOWN (routed-weight sum, rounded once to the activation type)."""
+    h / a2) -> DOWN (routed-weight sum, rounded once to the activation type).
+    x may also be a pair (codes [M, K] uint8, row scales [M] float32, or None
+    for codes quantised with a1): the codes of rms_norm, taken as they are."""
 
     def __init__(self, p: PackedFp8MoE, M: int, topk: int, renormalize: bool = True,
-                 block_size: Optional[int] = None, device="cuda"):
+                 block_size: Optional[int] = None, device="cuda", router: Optional[Router] = None):
         import torch
-        self.p, self.M, self.topk, self.renormalize = p, M, topk, renormalize
+        self.p, self.M, self.topk, self.renormalize, self.router = p, M, topk, renormalize, router
         self.bs = choose_block_size(M, topk, p.E, 8) if block_size is None else block_size
         self.cap = ops.moe_align_capacity(M, topk, p.E, self.bs)
         dev = torch.device(device)
@@ -274,11 +301,15 @@ class Fp8MoERunner:
         self.out = torch.empty((M, p.K), dtype=p.act, device=dev)
 
     def route_align(self, logits, stream=None):
-        ops.moe_route_align(logits, self.topk, self.renormalize, self.bs, self.w, self.ids, self.st, self.ex,
-                            self.nt, self.cap, stream=stream)
+        _route_align(self, logits, stream)
 
     def gate_up(self, x, stream=None):
         q = self.p
+        if isinstance(x, tuple):
+            codes, row_scales = x
+            ops.moe_fp8_codes_gemm(WQ_STAGE_GATE_UP, codes, row_scales, self.M, self.topk, q.E, 2 * q.N, q.K, q.w1,
+                                   q.s1, self.st, self.ex, self.nt, self.cap, self.bs, self.h, q.a1, q.a2, stream)
+            return
         ops.moe_fp8_w8a8_gemm(WQ_STAGE_GATE_UP, x, self.M, self.topk, q.E, 2 * q.N, q.K, q.w1, q.s1, self.st,
                               self.ex, self.nt, self.cap, self.bs, None, self.h, self.work1, q.a1, q.a2, stream,
                               q.act_code)
@@ -299,8 +330,9 @@ class Fp8MoERunner:
 
 
 def fused_moe_fp8(x, logits, p: PackedFp8MoE, topk: int, renormalize: bool = True,
-                  block_size: Optional[int] = None, stream=None, keep=False):
-    """x [M, K] act, logits [M, E] float32 -> out [M, K] act (FP8 W8A8 experts)."""
-    r = Fp8MoERunner(p, x.shape[0], topk, renormalize, block_size, device=x.device)
+                  block_size: Optional[int] = None, stream=None, keep=False, router: Optional[Router] = None):
+    """x [M, K] act, or (codes, row scales or None) -> out [M, K] act with logits [M, E] float32 (FP8 W8A8 experts)."""
+    first = x[0] if isinstance(x, tuple) else x
+    r = Fp8MoERunner(p, first.shape[0], topk, renormalize, block_size, device=first.device, router=router)
     out = r(x, logits, stream=stream)
     return (out, r.aux()) if keep else out

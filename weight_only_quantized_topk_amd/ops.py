@@ -21,7 +21,8 @@ __all__ = [
     "moe_route_gate_up",
     "moe_w8a16_gemm_noalloc", "sparse24_w4a16_gemm", "sparse24_w8a16_gemm", "quantize_w8", "dense_gemm_workspace_bytes", "dense_w4a16_gemm", "dense_w8a16_gemm",
     "pack_w4", "pack_w8", "pack_sparse24", "act_code", "moe_fp8_gemm_workspace_bytes", "moe_fp8_w8a8_gemm",
-    "pack_fp8", "moe_route_grouped", "moe_route_grouped_align", "rms_norm", "RmsNormOut",
+    "pack_fp8", "moe_route_grouped", "moe_route_grouped_align", "rms_norm", "RmsNormOut", "moe_fp8_codes_gemm",
+    "Lora", "pack_lora", "dense_lora_gemm", "dense_lora_workspace_bytes",
 ]
 
 
@@ -405,6 +406,29 @@ def moe_fp8_w8a8_gemm(stage, a, M, topk, E, n_out, k_in, w_packed, scales, sorte
     return out
 
 
+def moe_fp8_codes_gemm(stage, codes, row_scales, M, topk, E, n_out, k_in, w_packed, scales, sorted_token_ids,
+                       expert_ids, num_tokens_post_padded, capacity, block_size, out, in_scale: float = 1.0,
+                       out_scale: float = 1.0, stream=None):
+    """The GATE_UP (-> H codes [capacity, n_out / 2]) or RAW (-> fp32 [M * topk,
+    n_out]) stage of moe_fp8_w8a8_gemm on E4M3 codes [M, k_in] (rms_norm's),
+    with row_scales [M] float32 or, for None, in_scale for every row."""
+    torch = _torch()
+    _int32(M=M, topk=topk, E=E, n_out=n_out, k_in=k_in, block_size=block_size)
+    f8 = (torch.uint8, torch.float8_e4m3fn)
+    _check(codes, "codes", (M, k_in), f8)
+    if row_scales is not None:
+        _check(row_scales, "row_scales", (M,), (torch.float32,), codes.device)
+    if stage == WQ_STAGE_GATE_UP:
+        _check(out, "out", (max(capacity, 1), n_out // 2), f8, codes.device)
+    elif stage == WQ_STAGE_RAW:
+        _check(out, "out", (M * topk, n_out), (torch.float32,), codes.device)
+    d = _desc(stage, codes, M, topk, E, n_out, k_in, w_packed, scales, -1, None, sorted_token_ids, expert_ids,
+              num_tokens_post_padded, capacity, block_size, None, out, None, WQ_BF16)
+    check(load().moe_fp8_codes_gemm(C.byref(d), _ptr(row_scales), in_scale, out_scale, _stream(stream)),
+          "moe_fp8_codes_gemm")
+    return out
+
+
 def _sparse24(fn, x, vals, meta, scales, N, out, group_size, stream):
     torch = _torch()
     M, K = x.shape
@@ -429,7 +453,76 @@ def dense_gemm_workspace_bytes(M: int, K: int, N: int, act_order: bool = False) 
     return int(load().dense_gemm_workspace_bytes(M, K, N, int(bool(act_order))))
 
 
-def _dense(fn, x, N, w_packed, scales, extra, out, workspace, stream, act_order):
+class Lora(NamedTuple):
+    """The adapters of a batch beside one projection: stacked weights of one
+    rank (pack_lora pads lower ones) and every row's adapter (-1: none)."""
+    adapter_ids: object  # [M] int32
+    a: object            # [adapters, rank, K] act dtype
+    b: object            # [adapters, N, rank] act dtype
+    scales: object       # [adapters] float32, or None for ones
+
+
+def pack_lora(adapters, act, device="cuda"):
+    """Adapters [(A [r, K], B [N, r], scale), ...] of any ranks -> (a [L, R, K],
+    b [L, N, R], scales [L] float32) on the device, R the largest rank rounded
+    up to 8, lower ranks padded with zeros."""
+    torch = _torch()
+    act_code(act)
+    if not adapters:
+        raise ValueError("no adapters")
+    K, N = adapters[0][0].shape[1], adapters[0][1].shape[0]
+    for A, B, _ in adapters:
+        if A.dim() != 2 or B.dim() != 2 or A.shape[1] != K or B.shape[0] != N or A.shape[0] != B.shape[1]:
+            raise ValueError("adapters must be A [r, %d], B [%d, r], got %s, %s" % (K, N, list(A.shape), list(B.shape)))
+    R = max(8, -(-max(A.shape[0] for A, _, _ in adapters) // 8) * 8)
+    a = torch.zeros((len(adapters), R, K), dtype=act)
+    b = torch.zeros((len(adapters), N, R), dtype=act)
+    for i, (A, B, _) in enumerate(adapters):
+        a[i, :A.shape[0]] = A
+        b[i, :, :B.shape[1]] = B
+    scales = torch.tensor([float(s) for _, _, s in adapters], dtype=torch.float32)
+    return a.to(device), b.to(device), scales.to(device)
+
+
+def dense_lora_workspace_bytes(M: int, K: int, N: int, R: int, adapters: int) -> int:
+    return int(load().dense_lora_workspace_bytes(M, K, N, R, adapters))
+
+
+def dense_lora_gemm(x, adapter_ids, a, b, scales, y, workspace=None, stream=None):
+    """Adds the rows' own adapters to y in place: y[m] += scales[i] * (x[m] a[i]^T)
+    b[i]^T with i = adapter_ids[m] (rows with an id outside [0, adapters) stay as
+    they are).  x [M, K], y [M, N] bf16/fp16 (device; rows may be strided), a
+    [adapters, rank, K] and b [adapters, N, rank] in their type, scales
+    [adapters] float32 or None for ones.  Returns y."""
+    torch = _torch()
+    dt = act_code(x.dtype)
+    if x.dim() != 2 or y.dim() != 2 or a.dim() != 3:
+        raise ValueError("x must be [M, K], y [M, N], a [adapters, rank, K], got %s, %s, %s"
+                         % (list(x.shape), list(y.shape), list(a.shape)))
+    (M, K), N, (L, R, _) = x.shape, y.shape[1], a.shape
+    _int32(M=M, K=K, N=N, rank=R, adapters=L)
+    dev, same = x.device, (x.dtype,)
+    _check(x, "x", (M, K), same, row_stride=True)
+    _check(y, "y", (M, N), same, dev, row_stride=True)
+    _check(a, "a", (L, R, K), same, dev)
+    _check(b, "b", (L, N, R), same, dev)
+    _check(adapter_ids, "adapter_ids", (M,), (torch.int32,), dev)
+    if scales is not None:
+        _check(scales, "scales", (L,), (torch.float32,), dev)
+    new = []
+    if workspace is None:
+        workspace = torch.empty(dense_lora_workspace_bytes(M, K, N, R, L), dtype=torch.uint8, device=dev)
+        new.append(workspace)
+    elif not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be contiguous on %s" % dev)
+    check(load().dense_lora_gemm(_ptr(x), _row_stride(x), M, K, N, R, L, _ptr(adapter_ids), _ptr(a), _ptr(b),
+                                 _ptr(scales), _ptr(y), _row_stride(y), dt, _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)), "dense_lora_gemm")
+    _keep_for(stream, *new)
+    return y
+
+
+def _dense(fn, x, N, w_packed, scales, extra, out, workspace, stream, act_order, lora):
     torch = _torch()
     M, K = x.shape
     if out is None:
@@ -439,21 +532,24 @@ def _dense(fn, x, N, w_packed, scales, extra, out, workspace, stream, act_order)
         workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=x.device)
     check(fn(_ptr(x), M, K, N, _ptr(w_packed), _ptr(scales), *extra, _ptr(out), act_code(x.dtype), _ptr(workspace),
              workspace.numel(), _stream(stream)), fn.__name__)
+    if lora is not None:
+        dense_lora_gemm(x, lora.adapter_ids, lora.a, lora.b, lora.scales, out, stream=stream)
     return out
 
 
 def dense_w4a16_gemm(x, N: int, w_packed, scales, group_size: int = 128, k_perm=None, out=None, workspace=None,
-                     stream=None):
+                     stream=None, lora: Optional[Lora] = None):
     """Dense int4 linear: x [M, K] fp16 (device) -> y [M, N] fp16, weights
-    packed by pack_w4 with E = 1."""
+    packed by pack_w4 with E = 1; lora: the rows' adapters, added to y."""
     return _dense(load().dense_w4a16_gemm, x, N, w_packed, scales, (group_size, _ptr(k_perm)), out, workspace,
-                  stream, k_perm is not None)
+                  stream, k_perm is not None, lora)
 
 
-def dense_w8a16_gemm(x, N: int, w_packed, scales, out=None, workspace=None, stream=None):
+def dense_w8a16_gemm(x, N: int, w_packed, scales, out=None, workspace=None, stream=None,
+                     lora: Optional[Lora] = None):
     """Dense int8 linear: x [M, K] bf16/fp16 (device) -> y [M, N], weights
-    packed by pack_w8 with E = 1."""
-    return _dense(load().dense_w8a16_gemm, x, N, w_packed, scales, (), out, workspace, stream, False)
+    packed by pack_w8 with E = 1; lora: the rows' adapters, added to y."""
+    return _dense(load().dense_w8a16_gemm, x, N, w_packed, scales, (), out, workspace, stream, False, lora)
 
 
 def quantize_w8(w, q=None, scales=None, stream=None):
