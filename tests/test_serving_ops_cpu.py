@@ -221,7 +221,7 @@ def lora_args(**k):
 
 @pytest.mark.parametrize("change,want", [
     (dict(dt=2), INV), (dict(M=-1), INV), (dict(K=0), INV), (dict(N=-8), INV), (dict(R=0), INV), (dict(L=0), INV),
-    (dict(K=508), UNS), (dict(N=252), UNS), (dict(R=12), UNS), (dict(R=1032), UNS), (dict(M=(1 << 24) + 1), UNS),
+    (dict(K=508), UNS), (dict(N=252), UNS), (dict(R=12), UNS), (dict(R=264), UNS), (dict(M=(1 << 24) + 1), UNS),
     (dict(xs=504), INV), (dict(ys=0), INV), (dict(xs=516), UNS), (dict(ys=260), UNS), (dict(wsb=64), INV),
     (dict(x=None), INV), (dict(ids=None), INV), (dict(a=None), INV), (dict(b=at(2)), INV), (dict(s=at(4)), INV),
     (dict(y=None), INV), (dict(ws=None), INV),
