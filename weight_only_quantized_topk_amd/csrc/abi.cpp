@@ -1122,6 +1122,9 @@ wq_status dense_lora_gemm(const void* d_x, int64_t x_stride, int M, int K, int N
                    (long long)x_stride, K);
         WQ_REQUIRE(y_stride >= N && y_stride <= most, WQ_ERR_INVALID, "%s: y row stride %lld (N %d)", who,
                    (long long)y_stride, N);
+        WQ_REQUIRE(y_stride <= (1 << 25), WQ_ERR_UNSUPPORTED, "%s: y row stride %lld > 2^25", who,
+                   (long long)y_stride);
+        WQ_REQUIRE((int64_t)N * R <= INT32_MAX, WQ_ERR_UNSUPPORTED, "%s: N * rank >= 2^31", who);
         WQ_REQUIRE(x_stride % 8 == 0 && y_stride % 8 == 0, WQ_ERR_UNSUPPORTED,
                    "%s: row strides must be multiples of 8 (%lld, %lld)", who, (long long)x_stride,
                    (long long)y_stride);

@@ -74,6 +74,16 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
     u += 0x7fffu + ((u >> 16) & 1u);
     return (uint16_t)(u >> 16);
 }
+// two floats as a dword of 16-bit values, by the packed hardware conversions
+// (the same rounding, to nearest even; a NaN stays one)
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+template <bool BF16>
+__device__ __forceinline__ uint32_t f32_to_act2(float lo, float hi) {
+    const f32x2 v = {lo, hi};
+    if constexpr (BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
 template <bool BF16>
 __device__ __forceinline__ float act_to_f32(uint16_t h) {
     if constexpr (BF16) return bf16_to_f32(h);

@@ -13,8 +13,8 @@
 //
 // The intermediate t stays in fp32's precision: it is scaled by a power of two
 // to at most 1 per token (fp16 has the range then) and split in two 16-bit
-// parts, hi + lo, whose products with the same B rows are both taken, as the
-// two halves of one 32-deep matrix instruction's reduction (16 ranks each).
+// parts, hi + lo, which are both multiplied by the B rows (one register load of
+// 32 ranks serves two matrix instructions).
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -24,7 +24,6 @@ namespace wq {
 
 namespace {
 
-constexpr int RANK_GROUP = 64;  // ranks of one workgroup of the first product
 constexpr int WAVES = 4;
 
 // The wave's index as a scalar: what is decided by it is a branch of the whole
@@ -52,12 +51,14 @@ __device__ __forceinline__ TileIds tile_ids(const LoraArgs& g, int tile, int lan
 }
 
 // t = x A^T of the tile's tokens over one slice of K and one group of 16 RT
-// ranks.  Four waves take the 32-channel steps of the slice in turn, DEPTH of
-// a wave's steps in flight; D's columns are tokens, its rows ranks; the waves'
-// sums are added in LDS in wave order.  Loads are unconditional: rows past M or
-// R read the last one (their results are dropped), steps past the slice its
-// last step; the channels past the last whole step go through a step of their
-// own with zeros on both sides.
+// ranks.  Four waves take the 64-channel steps of the slice in turn (a row's 128
+// bytes, one cache line, by one wave), DEPTH of a wave's steps in flight; D's
+// columns are tokens, its rows ranks; the waves' sums are added in LDS in wave
+// order.  Loads are unconditional: rows past M or R read the last one (their
+// results are dropped), steps past the slice its last step; the channels past
+// the last whole step go through a step of their own with zeros on both sides.
+constexpr int STEP = 64;
+
 template <bool BF16, int TS, int RT, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
     __shared__ f32x4 red[WAVES][TS][RT][64];
@@ -68,7 +69,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
     const int slice = blockIdx.z % g.ks, r0 = blockIdx.z / g.ks * (16 * RT);
 
     const TileIds ids = tile_ids<16 * TS>(g, tile, lane);
-    const int steps = g.K / 32;
+    const int steps = g.K / STEP;
     const int s0 = (int)((int64_t)slice * steps / g.ks), s1 = (int)((int64_t)(slice + 1) * steps / g.ks);
     const int mine_steps = s0 + wave < s1 ? (s1 - s0 - wave + WAVES - 1) / WAVES : 0;
 
@@ -92,14 +93,23 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
         for (int t = 0; t < TS; ++t)
 #pragma unroll
             for (int r = 0; r < RT; ++r) acc[t][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+        auto multiply = [&](const u32x4 (&av)[RT], const u32x4 (&xv)[TS]) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int t = 0; t < TS; ++t) acc[t][r] = mfma16x16x32<BF16>(av[r], xv[t], acc[t][r]);
+        };
         if (mine_steps > 0) {
-            u32x4 xv[DEPTH][TS], av[DEPTH][RT];
+            u32x4 xv[DEPTH][2][TS], av[DEPTH][2][RT];
             auto load = [&](int i, int b) {
-                const int c = 32 * (s0 + wave + WAVES * min(i, mine_steps - 1));
+                const int c = STEP * (s0 + wave + WAVES * min(i, mine_steps - 1));
 #pragma unroll
-                for (int t = 0; t < TS; ++t) xv[b][t] = ldg128(xr[t] + c);
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int r = 0; r < RT; ++r) av[b][r] = ldg128(ar[r] + c);
+                    for (int t = 0; t < TS; ++t) xv[b][h][t] = ldg128(xr[t] + c + 32 * h);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) av[b][h][r] = ldg128(ar[r] + c + 32 * h);
+                }
             };
 #pragma unroll
             for (int d = 0; d < DEPTH; ++d) load(d, d);
@@ -107,27 +117,25 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
 #pragma unroll
                 for (int d = 0; d < DEPTH; ++d) {
                     if (i + d < mine_steps) {
-#pragma unroll
-                        for (int r = 0; r < RT; ++r)
-#pragma unroll
-                            for (int t = 0; t < TS; ++t) acc[t][r] = mfma16x16x32<BF16>(av[d][r], xv[d][t], acc[t][r]);
+                        multiply(av[d][0], xv[d][0]);
+                        multiply(av[d][1], xv[d][1]);
                     }
                     if (i + DEPTH < mine_steps) load(i + DEPTH + d, d);
                 }
             }
         }
-        if (g.K % 32 && slice == g.ks - 1 && wave == WAVES - 1) {
-            const int c = 32 * steps;
-            const bool in = c + 8 * q < g.K;
+        if (g.K % STEP && slice == g.ks - 1 && wave == WAVES - 1) {
             const u32x4 none = u32x4{0u, 0u, 0u, 0u};
-            u32x4 xv[TS];
 #pragma unroll
-            for (int t = 0; t < TS; ++t) xv[t] = in ? ldg128(xr[t] + c) : none;
+            for (int h = 0; h < 2; ++h) {
+                const int c = STEP * steps + 32 * h;
+                const bool in = c + 8 * q < g.K;
+                u32x4 xv[TS], av[RT];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const u32x4 av = in ? ldg128(ar[r] + c) : none;
+                for (int t = 0; t < TS; ++t) xv[t] = in ? ldg128(xr[t] + c) : none;
 #pragma unroll
-                for (int t = 0; t < TS; ++t) acc[t][r] = mfma16x16x32<BF16>(av, xv[t], acc[t][r]);
+                for (int r = 0; r < RT; ++r) av[r] = in ? ldg128(ar[r] + c) : none;
+                multiply(av, xv);
             }
         }
 #pragma unroll
@@ -150,30 +158,30 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
     }
 }
 
-constexpr int MAX_RANK = 256;
-
 // y += scale * t B^T for the tile's tokens and a range of outputs.  A pass: the
 // workgroup adds up the K slices of its tokens' t (8 threads a token, 8 ranks
-// each at a time), splits the sums and leaves them in LDS as matrix operands;
-// then each wave takes 64 outputs at a time.  An operand of 16 ranks holds,
-// by lane group, hi of ranks 0-7, hi of 8-15, lo of 0-7, lo of 8-15, against
-// B's ranks 0-7, 8-15, 0-7, 8-15.  Weight tile k holds outputs 16 (row / 4) +
-// 4 k + row % 4 of the 64, so that a lane's four results of the four tiles are
-// 16 outputs in a row of one token: two 16-byte accesses of y.  The B rows and
-// y of the next 64 outputs are in flight while these are added.
-template <bool BF16, int TS, int RT>
-__global__ __launch_bounds__(64 * WAVES) void lora_up_kernel(LoraArgs g, int per_wave) {
+// each at a time), splits the sums and leaves them in LDS as matrix operands
+// of 32 ranks, high and low parts; then each wave takes 64 outputs at a time.
+// Weight tile k holds outputs 32 (k / 2) + 8 (row / 4) + 4 (k % 2) + row % 4 of
+// the 64, so that a lane's results of two tiles are 8 outputs in a row of one
+// token (a 16-byte access) and the four lane groups' are 32: whole 64-byte
+// pieces of y.  (With a lane's 16 results in a row, two accesses each touched
+// half of every piece, and prompts took 1.5 times as long.)  The B rows and y of the next 64 outputs are in
+// flight while these are added.  RC: chunks of 32 ranks held at a time; RG:
+// groups of 64 ranks a token's t takes.
+template <bool BF16, int TS, int RC, int RG>
+__global__ __launch_bounds__(64 * WAVES, RG == 1 ? 3 : 2) void lora_up_kernel(LoraArgs g, int per_wave) {
     constexpr int TOKENS = 16 * TS;
-    extern __shared__ u32x4 frag[];  // [TS][R / 16 rounded up][64]
+    extern __shared__ u32x4 frag[];  // [TS][R / 32 rounded up][hi, lo][64]
     __shared__ float back[TOKENS];   // what a token's products are multiplied by
     const int lane = threadIdx.x & 63;
     const int wave = wave_index();
     const int col = lane & 15, q = lane >> 4;
     const int tile = blockIdx.x;
     const TileIds ids = tile_ids<TOKENS>(g, tile, lane);
-    const int chunks = (g.R + 15) / 16;
-    const int n_first = (blockIdx.y * WAVES + wave) * 64 * per_wave;
-    const int n_count = max(0, min(per_wave, (g.N - n_first + 63) / 64));
+    const int chunks = (g.R + 31) / 32;
+    const int n_first = blockIdx.y * (64 * WAVES * per_wave) + 64 * wave;  // the waves side by side
+    const int n_count = max(0, min(per_wave, (g.N - n_first + 64 * WAVES - 1) / (64 * WAVES)));
 
     uint64_t left = ids.first;
     for (int j = 0; left; ++j, left &= left - 1) {
@@ -182,29 +190,29 @@ __global__ __launch_bounds__(64 * WAVES) void lora_up_kernel(LoraArgs g, int per
         const uint64_t mine = __ballot(ids.id == a);
         const uint16_t* bw = g.b + (size_t)a * g.N * g.R;
 
-        u32x4 bv[RT][4];
+        u32x4 bv[RC][4];
         u32x4 yv[TS][2];
+        // (ranks past R: the last ones, replaced by zeros before use)
         auto load_b = [&](int n0, int c0) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const int rank = min(16 * (c0 + r) + 8 * (q & 1), g.R - 8);
+            for (int k = 0; k < 4; ++k) {
+                const int n = min(n0 + 32 * (k >> 1) + 8 * (col >> 2) + 4 * (k & 1) + (col & 3), g.N - 1);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int n = min(n0 + 16 * (col >> 2) + 4 * k + (col & 3), g.N - 1);
-                    bv[r][k] = ldg128(bw + (size_t)n * g.R + rank);
-                }
+                for (int r = 0; r < RC; ++r)
+                    bv[r][k] = ldg128(bw + (uint32_t)(n * g.R + min(32 * (c0 + r) + 8 * q, g.R - 8)));
             }
         };
-        auto y_at = [&](int t, int n0) {
-            return g.y + (int64_t)(tile * TOKENS + 16 * t + col) * g.y_stride + n0 + 16 * q;
-        };
+        // a token's outputs start (16 t + col) rows below the tile's first
+        uint16_t* yt = g.y + (int64_t)tile * TOKENS * g.y_stride;
+        auto y_at = [&](int t, int n) { return yt + (uint32_t)((16 * t + col) * (int)g.y_stride + n); };
         auto load_y = [&](int n0) {
 #pragma unroll
             for (int t = 0; t < TS; ++t)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (((mine >> (16 * t + col)) & 1ull) && n0 + 16 * q + 8 * h < g.N)
-                        yv[t][h] = ldg128(y_at(t, n0) + 8 * h);
+                for (int h = 0; h < 2; ++h) {
+                    const int n = n0 + 32 * h + 8 * q;
+                    if (((mine >> (16 * t + col)) & 1ull) && n < g.N) yv[t][h] = ldg128(y_at(t, n));
+                }
         };
         if (n_count > 0) {
             load_b(n_first, 0);
@@ -215,11 +223,11 @@ __global__ __launch_bounds__(64 * WAVES) void lora_up_kernel(LoraArgs g, int per
         if (tok < TOKENS) {
             const int gr = threadIdx.x & 7;
             const float* src = g.t + (size_t)min(tile * TOKENS + tok, g.M - 1) * g.R;
-            float v[MAX_RANK / RANK_GROUP][8];
+            float v[RG][8];
             float top = 0.0f;
 #pragma unroll
-            for (int w = 0; w < MAX_RANK / RANK_GROUP; ++w) {
-                const int rank = RANK_GROUP * w + 8 * gr;
+            for (int w = 0; w < RG; ++w) {
+                const int rank = 64 * w + 8 * gr;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[w][i] = 0.0f;
                 if (rank < g.R) {
@@ -243,9 +251,9 @@ __global__ __launch_bounds__(64 * WAVES) void lora_up_kernel(LoraArgs g, int per
             const float f = __uint_as_float((253u - e) << 23);  // 2^(126 - e)
             if (gr == 0) back[tok] = __uint_as_float((e + 1u) << 23) * (g.scales ? g.scales[a] : 1.0f);
 #pragma unroll
-            for (int w = 0; w < MAX_RANK / RANK_GROUP; ++w) {
-                const int c = 4 * w + (gr >> 1);
-                if (c >= chunks) break;
+            for (int w = 0; w < RG; ++w) {
+                const int c = 2 * w + (gr >> 2);
+                if (c >= chunks) break;  // (ranks past R in the last chunk are written, as zeros)
                 u32x4 hi, lo;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -260,38 +268,43 @@ __global__ __launch_bounds__(64 * WAVES) void lora_up_kernel(LoraArgs g, int per
                     hi[i] = h[0] | (h[1] << 16);
                     lo[i] = l[0] | (l[1] << 16);
                 }
-                u32x4* to = frag + ((tok >> 4) * chunks + c) * 64 + 16 * (gr & 1) + (tok & 15);
+                u32x4* to = frag + ((tok >> 4) * chunks + c) * 128 + 16 * (gr & 3) + (tok & 15);
                 to[0] = hi;
-                to[32] = lo;
+                to[64] = lo;
             }
         }
         __syncthreads();
 
         for (int i = 0; i < n_count; ++i) {
-            const int n0 = n_first + 64 * i;
+            const int n0 = n_first + 64 * WAVES * i;
             f32x4 acc[TS][4];
 #pragma unroll
             for (int t = 0; t < TS; ++t)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[t][k] = f32x4{0.f, 0.f, 0.f, 0.f};
-            for (int c0 = 0; c0 < chunks; c0 += RT) {
+            for (int c0 = 0; c0 < chunks; c0 += RC) {
                 if (c0 > 0) load_b(n0, c0);
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
+                for (int r = 0; r < RC; ++r) {
                     if (c0 + r >= chunks) break;
-                    if (16 * (c0 + r) + 8 == g.R) {  // half a chunk: zeros on both sides
+                    if (32 * (c0 + r + 1) > g.R) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) bv[r][k] = (q & 1) ? u32x4{0u, 0u, 0u, 0u} : bv[r][k];
+                        for (int k = 0; k < 4; ++k)
+                            bv[r][k] = 32 * (c0 + r) + 8 * q < g.R ? bv[r][k] : u32x4{0u, 0u, 0u, 0u};
                     }
 #pragma unroll
                     for (int t = 0; t < TS; ++t) {
-                        const u32x4 tv = frag[(t * chunks + c0 + r) * 64 + lane];
+                        const u32x4* tv = frag + (t * chunks + c0 + r) * 128 + lane;
+                        const u32x4 hi = tv[0], lo = tv[64];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) acc[t][k] = mfma16x16x32<BF16>(bv[r][k], tv, acc[t][k]);
+                        for (int k = 0; k < 4; ++k) {
+                            acc[t][k] = mfma16x16x32<BF16>(bv[r][k], hi, acc[t][k]);
+                            acc[t][k] = mfma16x16x32<BF16>(bv[r][k], lo, acc[t][k]);
+                        }
                     }
                 }
             }
-            if (i + 1 < n_count) load_b(n0 + 64, 0);
+            if (i + 1 < n_count) load_b(n0 + 64 * WAVES, 0);
             u32x4 out[TS][2];
 #pragma unroll
             for (int t = 0; t < TS; ++t) {
@@ -304,16 +317,18 @@ __global__ __launch_bounds__(64 * WAVES) void lora_up_kernel(LoraArgs g, int per
                         const uint32_t d = yv[t][h][w];
                         const float v0 = act_to_f32<BF16>((uint16_t)d) + acc[t][k >> 2][k & 3] * f;
                         const float v1 = act_to_f32<BF16>((uint16_t)(d >> 16)) + acc[t][k >> 2][(k & 3) + 1] * f;
-                        out[t][h][w] = (uint32_t)f32_to_act<BF16>(v0) | ((uint32_t)f32_to_act<BF16>(v1) << 16);
+                        out[t][h][w] = f32_to_act2<BF16>(v0, v1);
                     }
             }
-            if (i + 1 < n_count) load_y(n0 + 64);
+            if (i + 1 < n_count) load_y(n0 + 64 * WAVES);
 #pragma unroll
             for (int t = 0; t < TS; ++t)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (((mine >> (16 * t + col)) & 1ull) && n0 + 16 * q + 8 * h < g.N)
-                        *reinterpret_cast<u32x4*>(y_at(t, n0) + 8 * h) = out[t][h];
+                for (int h = 0; h < 2; ++h) {
+                    const int n = n0 + 32 * h + 8 * q;
+                    if (((mine >> (16 * t + col)) & 1ull) && n < g.N)
+                        *reinterpret_cast<u32x4*>(y_at(t, n)) = out[t][h];
+                }
         }
         __syncthreads();
     }
@@ -332,14 +347,18 @@ void launch_cfg(const LoraArgs& g, hipStream_t s) {
     // passes side by side: a workgroup for each adapter of a tile while there are few tiles
     const int most = std::min(std::min(16 * TS, g.adapters), g.M);
     const int side = std::max(1, std::min(most, 1024 / std::max(1, tiles * g.ks * groups)));
-    hipLaunchKernelGGL((lora_down_kernel<BF16, TS, RT, 4>), dim3(tiles, side, g.ks * groups), dim3(64 * WAVES), 0, s,
+    hipLaunchKernelGGL((lora_down_kernel<BF16, TS, RT, 2>), dim3(tiles, side, g.ks * groups), dim3(64 * WAVES), 0, s,
                        g);
     const int blocks = (g.N + 64 * WAVES - 1) / (64 * WAVES);
     const int per_wave = std::max(1, std::min(4, (int)((int64_t)blocks * tiles / 1024)));
     const int ranges = (blocks + per_wave - 1) / per_wave;
     const int side2 = (int)std::max<int64_t>(1, std::min<int64_t>(most, 1024 / ((int64_t)tiles * ranges)));
-    hipLaunchKernelGGL((lora_up_kernel<BF16, TS, RT>), dim3(tiles, ranges, side2), dim3(64 * WAVES),
-                       sizeof(u32x4) * 64 * TS * ((g.R + 15) / 16), s, g, per_wave);
+    const dim3 grid(tiles, ranges, side2);
+    const size_t lds = sizeof(u32x4) * 128 * TS * ((g.R + 31) / 32);
+    if (g.R <= 64)
+        hipLaunchKernelGGL((lora_up_kernel<BF16, TS, (RT + 1) / 2, 1>), grid, dim3(64 * WAVES), lds, s, g, per_wave);
+    else
+        hipLaunchKernelGGL((lora_up_kernel<BF16, TS, 2, 4>), grid, dim3(64 * WAVES), lds, s, g, per_wave);
 }
 
 template <bool BF16, int TS>
@@ -353,12 +372,12 @@ void launch_ts(const LoraArgs& g, hipStream_t s) {
 
 }  // namespace
 
-// K slices of the first product: workgroups to fill the chip, at least 2 steps
-// of 32 channels for each of their four waves
+// K slices of the first product: workgroups to fill the chip, a step of
+// 64 channels at least for each of their four waves
 int lora_k_slices(int M, int K, int R) {
     const int rows = 16 * tile_rows(M), ranks = 16 * rank_tiles(R);
     const int wgs = (M + rows - 1) / rows * ((R + ranks - 1) / ranks);
-    return std::max(1, std::min(std::min(16, 512 / std::max(1, wgs)), K / 32 / (2 * WAVES)));
+    return std::max(1, std::min(std::min(16, 512 / std::max(1, wgs)), K / STEP / WAVES));
 }
 
 void launch_lora(const LoraArgs& g, bool bf16, hipStream_t s) {

@@ -90,8 +90,7 @@ __device__ __forceinline__ void store_vec(uint16_t* p, const float (&v)[VEC]) {
     if constexpr (VEC == 8) {
         u32x4 d;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            d[j] = (uint32_t)f32_to_act<BF16>(v[2 * j]) | ((uint32_t)f32_to_act<BF16>(v[2 * j + 1]) << 16);
+        for (int j = 0; j < 4; ++j) d[j] = f32_to_act2<BF16>(v[2 * j], v[2 * j + 1]);
         *reinterpret_cast<u32x4*>(p) = d;
     } else {
         *p = f32_to_act<BF16>(v[0]);
