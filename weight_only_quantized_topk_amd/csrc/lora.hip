@@ -24,7 +24,10 @@ namespace wq {
 
 namespace {
 
-constexpr int WAVES = 4;
+constexpr int UP_WAVES = 4;
+// waves of the first product's workgroups: more where there are few of them
+constexpr int down_waves(int ts) { return ts == 1 ? 8 : 4; }
+constexpr int MAX_SLICES = 4;
 
 // The wave's index as a scalar: what is decided by it is a branch of the whole
 // wave (a matrix instruction does not look at the lanes' mask, so one under a
@@ -51,7 +54,7 @@ __device__ __forceinline__ TileIds tile_ids(const LoraArgs& g, int tile, int lan
 }
 
 // t = x A^T of the tile's tokens over one slice of K and one group of 16 RT
-// ranks.  Four waves take the 64-channel steps of the slice in turn (a row's 128
+// ranks.  The waves take the 64-channel steps of the slice in turn (a row's 128
 // bytes, one cache line, by one wave), DEPTH of a wave's steps in flight; D's
 // columns are tokens, its rows ranks; the waves' sums are added in LDS in wave
 // order.  Loads are unconditional: rows past M or R read the last one (their
@@ -59,7 +62,7 @@ __device__ __forceinline__ TileIds tile_ids(const LoraArgs& g, int tile, int lan
 // the last whole step go through a step of their own with zeros on both sides.
 constexpr int STEP = 64;
 
-template <bool BF16, int TS, int RT, int DEPTH>
+template <bool BF16, int TS, int RT, int WAVES, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
     __shared__ f32x4 red[WAVES][TS][RT][64];
     const int lane = threadIdx.x & 63;
@@ -68,7 +71,6 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
     const int tile = blockIdx.x;
     const int slice = blockIdx.z % g.ks, r0 = blockIdx.z / g.ks * (16 * RT);
 
-    const TileIds ids = tile_ids<16 * TS>(g, tile, lane);
     const int steps = g.K / STEP;
     const int s0 = (int)((int64_t)slice * steps / g.ks), s1 = (int)((int64_t)(slice + 1) * steps / g.ks);
     const int mine_steps = s0 + wave < s1 ? (s1 - s0 - wave + WAVES - 1) / WAVES : 0;
@@ -77,7 +79,21 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
 #pragma unroll
     for (int t = 0; t < TS; ++t)
         xr[t] = g.x + (int64_t)min(tile * 16 * TS + 16 * t + col, g.M - 1) * g.x_stride + 8 * q;
+    u32x4 xv[DEPTH][2][TS], av[DEPTH][2][RT];
+    auto channel = [&](int i) { return STEP * (s0 + wave + WAVES * min(i, mine_steps - 1)); };
+    auto load_x = [&](int i, int b) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < TS; ++t) xv[b][h][t] = ldg128(xr[t] + channel(i) + 32 * h);
+    };
+    if (mine_steps > 0) {  // on its way while the tile's adapters are found
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) load_x(d, d);
+    }
+    const TileIds ids = tile_ids<16 * TS>(g, tile, lane);
 
+    bool first = true;
     uint64_t left = ids.first;
     for (int j = 0; left; ++j, left &= left - 1) {
         if (j % (int)gridDim.y != (int)blockIdx.y) continue;
@@ -100,19 +116,18 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
                 for (int t = 0; t < TS; ++t) acc[t][r] = mfma16x16x32<BF16>(av[r], xv[t], acc[t][r]);
         };
         if (mine_steps > 0) {
-            u32x4 xv[DEPTH][2][TS], av[DEPTH][2][RT];
-            auto load = [&](int i, int b) {
-                const int c = STEP * (s0 + wave + WAVES * min(i, mine_steps - 1));
+            auto load_a = [&](int i, int b) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int t = 0; t < TS; ++t) xv[b][h][t] = ldg128(xr[t] + c + 32 * h);
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) av[b][h][r] = ldg128(ar[r] + c + 32 * h);
-                }
+                    for (int r = 0; r < RT; ++r) av[b][h][r] = ldg128(ar[r] + channel(i) + 32 * h);
             };
 #pragma unroll
-            for (int d = 0; d < DEPTH; ++d) load(d, d);
+            for (int d = 0; d < DEPTH; ++d) {
+                if (!first) load_x(d, d);
+                load_a(d, d);
+            }
+            first = false;
             for (int i = 0; i < mine_steps; i += DEPTH) {
 #pragma unroll
                 for (int d = 0; d < DEPTH; ++d) {
@@ -120,7 +135,10 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
                         multiply(av[d][0], xv[d][0]);
                         multiply(av[d][1], xv[d][1]);
                     }
-                    if (i + DEPTH < mine_steps) load(i + DEPTH + d, d);
+                    if (i + DEPTH < mine_steps) {
+                        load_x(i + DEPTH + d, d);
+                        load_a(i + DEPTH + d, d);
+                    }
                 }
             }
         }
@@ -130,12 +148,12 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
             for (int h = 0; h < 2; ++h) {
                 const int c = STEP * steps + 32 * h;
                 const bool in = c + 8 * q < g.K;
-                u32x4 xv[TS], av[RT];
+                u32x4 xl[TS], al[RT];
 #pragma unroll
-                for (int t = 0; t < TS; ++t) xv[t] = in ? ldg128(xr[t] + c) : none;
+                for (int t = 0; t < TS; ++t) xl[t] = in ? ldg128(xr[t] + c) : none;
 #pragma unroll
-                for (int r = 0; r < RT; ++r) av[r] = in ? ldg128(ar[r] + c) : none;
-                multiply(av, xv);
+                for (int r = 0; r < RT; ++r) al[r] = in ? ldg128(ar[r] + c) : none;
+                multiply(al, xl);
             }
         }
 #pragma unroll
@@ -158,10 +176,10 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
     }
 }
 
-// y += scale * t B^T for the tile's tokens and a range of outputs.  A pass: the
+// y += scale * t B^T for the tile's tokens and a range of outputs.  The
 // workgroup adds up the K slices of its tokens' t (8 threads a token, 8 ranks
 // each at a time), splits the sums and leaves them in LDS as matrix operands
-// of 32 ranks, high and low parts; then each wave takes 64 outputs at a time.
+// of 32 ranks, high and low parts; in a pass each wave takes 64 outputs at a time.
 // Weight tile k holds outputs 32 (k / 2) + 8 (row / 4) + 4 (k % 2) + row % 4 of
 // the 64, so that a lane's results of two tiles are 8 outputs in a row of one
 // token (a 16-byte access) and the four lane groups' are 32: whole 64-byte
@@ -170,7 +188,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
 // flight while these are added.  RC: chunks of 32 ranks held at a time; RG:
 // groups of 64 ranks a token's t takes.
 template <bool BF16, int TS, int RC, int RG>
-__global__ __launch_bounds__(64 * WAVES, RG == 1 ? 3 : 2) void lora_up_kernel(LoraArgs g, int per_wave) {
+__global__ __launch_bounds__(64 * UP_WAVES, RG == 1 ? 3 : 2) void lora_up_kernel(LoraArgs g, int per_wave) {
     constexpr int TOKENS = 16 * TS;
     extern __shared__ u32x4 frag[];  // [TS][R / 32 rounded up][hi, lo][64]
     __shared__ float back[TOKENS];   // what a token's products are multiplied by
@@ -178,10 +196,70 @@ __global__ __launch_bounds__(64 * WAVES, RG == 1 ? 3 : 2) void lora_up_kernel(Lo
     const int wave = wave_index();
     const int col = lane & 15, q = lane >> 4;
     const int tile = blockIdx.x;
-    const TileIds ids = tile_ids<TOKENS>(g, tile, lane);
     const int chunks = (g.R + 31) / 32;
-    const int n_first = blockIdx.y * (64 * WAVES * per_wave) + 64 * wave;  // the waves side by side
-    const int n_count = max(0, min(per_wave, (g.N - n_first + 64 * WAVES - 1) / (64 * WAVES)));
+    const int n_first = blockIdx.y * (64 * UP_WAVES * per_wave) + 64 * wave;  // the waves side by side
+    const int n_count = max(0, min(per_wave, (g.N - n_first + 64 * UP_WAVES - 1) / (64 * UP_WAVES)));
+
+    const int tok = threadIdx.x >> 3;
+    if (tok < TOKENS) {
+        const int gr = threadIdx.x & 7;
+        const int m = min(tile * TOKENS + tok, g.M - 1);
+        const int id = g.ids[m];
+        const float scale = g.scales && id >= 0 && id < g.adapters ? g.scales[id] : 1.0f;
+        const float* src = g.t + (size_t)m * g.R;
+        float v[RG][8];
+        float top = 0.0f;
+#pragma unroll
+        for (int w = 0; w < RG; ++w) {
+            const int rank = 64 * w + 8 * gr;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[w][i] = 0.0f;
+            if (rank < g.R) {
+#pragma unroll 4
+                for (int z = 0; z < g.ks; ++z) {
+                    const f32x4 p0 = *reinterpret_cast<const f32x4*>(src + (size_t)z * g.M * g.R + rank);
+                    const f32x4 p1 = *reinterpret_cast<const f32x4*>(src + (size_t)z * g.M * g.R + rank + 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[w][i] += p0[i];
+                        v[w][4 + i] += p1[i];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[w][i]));
+            }
+        }
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+        const uint32_t e = min(__float_as_uint(top) >> 23, 252u);
+        const float f = __uint_as_float((253u - e) << 23);  // 2^(126 - e)
+        if (gr == 0) back[tok] = __uint_as_float((e + 1u) << 23) * scale;
+#pragma unroll
+        for (int w = 0; w < RG; ++w) {
+            const int c = 2 * w + (gr >> 2);
+            if (c >= chunks) break;  // (ranks past R in the last chunk are written, as zeros)
+            u32x4 hi, lo;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t h[2], l[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float s = v[w][2 * i + k] * f;
+                    h[k] = f32_to_act<BF16>(s);
+                    // an infinity is all in its high part
+                    l[k] = fabsf(s) < __builtin_inff() ? f32_to_act<BF16>(s - act_to_f32<BF16>((uint16_t)h[k])) : 0;
+                }
+                hi[i] = h[0] | (h[1] << 16);
+                lo[i] = l[0] | (l[1] << 16);
+            }
+            u32x4* to = frag + ((tok >> 4) * chunks + c) * 128 + 16 * (gr & 3) + (tok & 15);
+            to[0] = hi;
+            to[64] = lo;
+        }
+    }
+
+    const TileIds ids = tile_ids<TOKENS>(g, tile, lane);
+    __syncthreads();
 
     uint64_t left = ids.first;
     for (int j = 0; left; ++j, left &= left - 1) {
@@ -219,64 +297,9 @@ __global__ __launch_bounds__(64 * WAVES, RG == 1 ? 3 : 2) void lora_up_kernel(Lo
             load_y(n_first);
         }
 
-        const int tok = threadIdx.x >> 3;
-        if (tok < TOKENS) {
-            const int gr = threadIdx.x & 7;
-            const float* src = g.t + (size_t)min(tile * TOKENS + tok, g.M - 1) * g.R;
-            float v[RG][8];
-            float top = 0.0f;
-#pragma unroll
-            for (int w = 0; w < RG; ++w) {
-                const int rank = 64 * w + 8 * gr;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[w][i] = 0.0f;
-                if (rank < g.R) {
-#pragma unroll 4
-                    for (int z = 0; z < g.ks; ++z) {
-                        const f32x4 p0 = *reinterpret_cast<const f32x4*>(src + (size_t)z * g.M * g.R + rank);
-                        const f32x4 p1 = *reinterpret_cast<const f32x4*>(src + (size_t)z * g.M * g.R + rank + 4);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            v[w][i] += p0[i];
-                            v[w][4 + i] += p1[i];
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[w][i]));
-                }
-            }
-#pragma unroll
-            for (int off = 1; off < 8; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-            const uint32_t e = min(__float_as_uint(top) >> 23, 252u);
-            const float f = __uint_as_float((253u - e) << 23);  // 2^(126 - e)
-            if (gr == 0) back[tok] = __uint_as_float((e + 1u) << 23) * (g.scales ? g.scales[a] : 1.0f);
-#pragma unroll
-            for (int w = 0; w < RG; ++w) {
-                const int c = 2 * w + (gr >> 2);
-                if (c >= chunks) break;  // (ranks past R in the last chunk are written, as zeros)
-                u32x4 hi, lo;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t h[2], l[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float s = v[w][2 * i + k] * f;
-                        h[k] = f32_to_act<BF16>(s);
-                        // an infinity is all in its high part
-                        l[k] = fabsf(s) < __builtin_inff() ? f32_to_act<BF16>(s - act_to_f32<BF16>((uint16_t)h[k])) : 0;
-                    }
-                    hi[i] = h[0] | (h[1] << 16);
-                    lo[i] = l[0] | (l[1] << 16);
-                }
-                u32x4* to = frag + ((tok >> 4) * chunks + c) * 128 + 16 * (gr & 3) + (tok & 15);
-                to[0] = hi;
-                to[64] = lo;
-            }
-        }
-        __syncthreads();
 
         for (int i = 0; i < n_count; ++i) {
-            const int n0 = n_first + 64 * WAVES * i;
+            const int n0 = n_first + 64 * UP_WAVES * i;
             f32x4 acc[TS][4];
 #pragma unroll
             for (int t = 0; t < TS; ++t)
@@ -304,7 +327,7 @@ __global__ __launch_bounds__(64 * WAVES, RG == 1 ? 3 : 2) void lora_up_kernel(Lo
                     }
                 }
             }
-            if (i + 1 < n_count) load_b(n0 + 64 * WAVES, 0);
+            if (i + 1 < n_count) load_b(n0 + 64 * UP_WAVES, 0);
             u32x4 out[TS][2];
 #pragma unroll
             for (int t = 0; t < TS; ++t) {
@@ -320,7 +343,7 @@ __global__ __launch_bounds__(64 * WAVES, RG == 1 ? 3 : 2) void lora_up_kernel(Lo
                         out[t][h][w] = f32_to_act2<BF16>(v0, v1);
                     }
             }
-            if (i + 1 < n_count) load_y(n0 + 64 * WAVES);
+            if (i + 1 < n_count) load_y(n0 + 64 * UP_WAVES);
 #pragma unroll
             for (int t = 0; t < TS; ++t)
 #pragma unroll
@@ -330,7 +353,6 @@ __global__ __launch_bounds__(64 * WAVES, RG == 1 ? 3 : 2) void lora_up_kernel(Lo
                         *reinterpret_cast<u32x4*>(y_at(t, n)) = out[t][h];
                 }
         }
-        __syncthreads();
     }
 }
 
@@ -347,18 +369,18 @@ void launch_cfg(const LoraArgs& g, hipStream_t s) {
     // passes side by side: a workgroup for each adapter of a tile while there are few tiles
     const int most = std::min(std::min(16 * TS, g.adapters), g.M);
     const int side = std::max(1, std::min(most, 1024 / std::max(1, tiles * g.ks * groups)));
-    hipLaunchKernelGGL((lora_down_kernel<BF16, TS, RT, 2>), dim3(tiles, side, g.ks * groups), dim3(64 * WAVES), 0, s,
+    hipLaunchKernelGGL((lora_down_kernel<BF16, TS, RT, down_waves(TS), 2>), dim3(tiles, side, g.ks * groups), dim3(64 * down_waves(TS)), 0, s,
                        g);
-    const int blocks = (g.N + 64 * WAVES - 1) / (64 * WAVES);
+    const int blocks = (g.N + 64 * UP_WAVES - 1) / (64 * UP_WAVES);
     const int per_wave = std::max(1, std::min(4, (int)((int64_t)blocks * tiles / 1024)));
     const int ranges = (blocks + per_wave - 1) / per_wave;
     const int side2 = (int)std::max<int64_t>(1, std::min<int64_t>(most, 1024 / ((int64_t)tiles * ranges)));
     const dim3 grid(tiles, ranges, side2);
     const size_t lds = sizeof(u32x4) * 128 * TS * ((g.R + 31) / 32);
     if (g.R <= 64)
-        hipLaunchKernelGGL((lora_up_kernel<BF16, TS, (RT + 1) / 2, 1>), grid, dim3(64 * WAVES), lds, s, g, per_wave);
+        hipLaunchKernelGGL((lora_up_kernel<BF16, TS, (RT + 1) / 2, 1>), grid, dim3(64 * UP_WAVES), lds, s, g, per_wave);
     else
-        hipLaunchKernelGGL((lora_up_kernel<BF16, TS, 2, 4>), grid, dim3(64 * WAVES), lds, s, g, per_wave);
+        hipLaunchKernelGGL((lora_up_kernel<BF16, TS, 2, 4>), grid, dim3(64 * UP_WAVES), lds, s, g, per_wave);
 }
 
 template <bool BF16, int TS>
@@ -372,12 +394,12 @@ void launch_ts(const LoraArgs& g, hipStream_t s) {
 
 }  // namespace
 
-// K slices of the first product: workgroups to fill the chip, a step of
-// 64 channels at least for each of their four waves
+// K slices of the first product: workgroups to fill the chip, at most 4 (the
+// second product adds them up), a step of 64 channels at least for each wave
 int lora_k_slices(int M, int K, int R) {
-    const int rows = 16 * tile_rows(M), ranks = 16 * rank_tiles(R);
+    const int ts = tile_rows(M), rows = 16 * ts, ranks = 16 * rank_tiles(R);
     const int wgs = (M + rows - 1) / rows * ((R + ranks - 1) / ranks);
-    return std::max(1, std::min(std::min(16, 512 / std::max(1, wgs)), K / STEP / WAVES));
+    return std::max(1, std::min(std::min(MAX_SLICES, 512 / std::max(1, wgs)), K / STEP / down_waves(ts)));
 }
 
 void launch_lora(const LoraArgs& g, bool bf16, hipStream_t s) {
