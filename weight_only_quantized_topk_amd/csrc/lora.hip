@@ -15,8 +15,7 @@
 // to at most 1 per token (fp16 has the range then) and split in two 16-bit
 // parts, hi + lo, which are both multiplied by the B rows (one register load of
 // 32 ranks serves two matrix instructions).
-#include "common.hpp"
-#include "launch.hpp"
+#include "lora_common.hpp"
 
 #include <algorithm>
 
@@ -25,33 +24,7 @@ namespace wq {
 namespace {
 
 constexpr int UP_WAVES = 4;
-// waves of the first product's workgroups: more where there are few of them
-constexpr int down_waves(int ts) { return ts == 1 ? 8 : 4; }
-constexpr int MAX_SLICES = 4;
-
-// The wave's index as a scalar: what is decided by it is a branch of the whole
-// wave (a matrix instruction does not look at the lanes' mask, so one under a
-// lane-wise condition would run all the same)
-__device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
-
-// The adapters of a tile of up to 64 tokens: lane i holds token i's (-1: none,
-// an id out of range counts as none), first marks each one's first token
-struct TileIds {
-    int id;
-    uint64_t first;
-};
-template <int TOKENS>
-__device__ __forceinline__ TileIds tile_ids(const LoraArgs& g, int tile, int lane) {
-    TileIds t;
-    const int m = tile * TOKENS + lane;
-    t.id = (lane < TOKENS && m < g.M) ? g.ids[m] : -1;
-    if (t.id < 0 || t.id >= g.adapters) t.id = -1;
-    bool seen = t.id < 0;
-#pragma unroll
-    for (int i = 0; i < TOKENS; ++i) seen = seen || (i < lane && __builtin_amdgcn_readlane(t.id, i) == t.id);
-    t.first = __ballot(!seen);
-    return t;
-}
+constexpr int DOWN_WAVES = 8;
 
 // t = x A^T of the tile's tokens over one slice of K and one group of 16 RT
 // ranks.  The waves take the 64-channel steps of the slice in turn (a row's 128
@@ -60,8 +33,6 @@ __device__ __forceinline__ TileIds tile_ids(const LoraArgs& g, int tile, int lan
 // order.  Loads are unconditional: rows past M or R read the last one (their
 // results are dropped), steps past the slice its last step; the channels past
 // the last whole step go through a step of their own with zeros on both sides.
-constexpr int STEP = 64;
-
 template <bool BF16, int TS, int RT, int WAVES, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
     __shared__ f32x4 red[WAVES][TS][RT][64];
@@ -71,7 +42,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
     const int tile = blockIdx.x;
     const int slice = blockIdx.z % g.ks, r0 = blockIdx.z / g.ks * (16 * RT);
 
-    const int steps = g.K / STEP;
+    const int steps = g.K / LORA_STEP;
     const int s0 = (int)((int64_t)slice * steps / g.ks), s1 = (int)((int64_t)(slice + 1) * steps / g.ks);
     const int mine_steps = s0 + wave < s1 ? (s1 - s0 - wave + WAVES - 1) / WAVES : 0;
 
@@ -80,7 +51,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
     for (int t = 0; t < TS; ++t)
         xr[t] = g.x + (int64_t)min(tile * 16 * TS + 16 * t + col, g.M - 1) * g.x_stride + 8 * q;
     u32x4 xv[DEPTH][2][TS], av[DEPTH][2][RT];
-    auto channel = [&](int i) { return STEP * (s0 + wave + WAVES * min(i, mine_steps - 1)); };
+    auto channel = [&](int i) { return LORA_STEP * (s0 + wave + WAVES * min(i, mine_steps - 1)); };
     auto load_x = [&](int i, int b) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -142,11 +113,11 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
                 }
             }
         }
-        if (g.K % STEP && slice == g.ks - 1 && wave == WAVES - 1) {
+        if (g.K % LORA_STEP && slice == g.ks - 1 && wave == WAVES - 1) {
             const u32x4 none = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int c = STEP * steps + 32 * h;
+                const int c = LORA_STEP * steps + 32 * h;
                 const bool in = c + 8 * q < g.K;
                 u32x4 xl[TS], al[RT];
 #pragma unroll
@@ -203,59 +174,14 @@ __global__ __launch_bounds__(64 * UP_WAVES, RG == 1 ? 3 : 2) void lora_up_kernel
     const int tok = threadIdx.x >> 3;
     if (tok < TOKENS) {
         const int gr = threadIdx.x & 7;
-        const int m = min(tile * TOKENS + tok, g.M - 1);
-        const int id = g.ids[m];
-        const float scale = g.scales && id >= 0 && id < g.adapters ? g.scales[id] : 1.0f;
-        const float* src = g.t + (size_t)m * g.R;
-        float v[RG][8];
-        float top = 0.0f;
-#pragma unroll
-        for (int w = 0; w < RG; ++w) {
-            const int rank = 64 * w + 8 * gr;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[w][i] = 0.0f;
-            if (rank < g.R) {
-#pragma unroll 4
-                for (int z = 0; z < g.ks; ++z) {
-                    const f32x4 p0 = *reinterpret_cast<const f32x4*>(src + (size_t)z * g.M * g.R + rank);
-                    const f32x4 p1 = *reinterpret_cast<const f32x4*>(src + (size_t)z * g.M * g.R + rank + 4);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[w][i] += p0[i];
-                        v[w][4 + i] += p1[i];
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[w][i]));
-            }
-        }
-#pragma unroll
-        for (int off = 1; off < 8; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-        const uint32_t e = min(__float_as_uint(top) >> 23, 252u);
-        const float f = __uint_as_float((253u - e) << 23);  // 2^(126 - e)
-        if (gr == 0) back[tok] = __uint_as_float((e + 1u) << 23) * scale;
-#pragma unroll
-        for (int w = 0; w < RG; ++w) {
+        const float f = split_token<BF16, RG>(g, min(tile * TOKENS + tok, g.M - 1), gr, [&](int w, u32x4 hi, u32x4 lo) {
             const int c = 2 * w + (gr >> 2);
-            if (c >= chunks) break;  // (ranks past R in the last chunk are written, as zeros)
-            u32x4 hi, lo;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t h[2], l[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float s = v[w][2 * i + k] * f;
-                    h[k] = f32_to_act<BF16>(s);
-                    // an infinity is all in its high part
-                    l[k] = fabsf(s) < __builtin_inff() ? f32_to_act<BF16>(s - act_to_f32<BF16>((uint16_t)h[k])) : 0;
-                }
-                hi[i] = h[0] | (h[1] << 16);
-                lo[i] = l[0] | (l[1] << 16);
-            }
+            if (c >= chunks) return;  // (ranks past R in the last chunk are written, as zeros)
             u32x4* to = frag + ((tok >> 4) * chunks + c) * 128 + 16 * (gr & 3) + (tok & 15);
             to[0] = hi;
             to[64] = lo;
-        }
+        });
+        if (gr == 0) back[tok] = f;
     }
 
     const TileIds ids = tile_ids<TOKENS>(g, tile, lane);
@@ -356,23 +282,22 @@ __global__ __launch_bounds__(64 * UP_WAVES, RG == 1 ? 3 : 2) void lora_up_kernel
     }
 }
 
-// 16-token tiles up to 512 tokens (workgroups to fill the chip), 32 above (the
-// adapters' weights are read once per tile)
-int tile_rows(int M) { return M <= 512 ? 1 : 2; }
+constexpr int TS = 1;  // 16-token tiles: workgroups to fill the chip
+
 // ranks a workgroup takes at a time, in tiles of 16
 int rank_tiles(int R) { return R <= 16 ? 1 : (R <= 32 ? 2 : 4); }
 
-template <bool BF16, int TS, int RT>
+template <bool BF16, int RT>
 void launch_cfg(const LoraArgs& g, hipStream_t s) {
     const int tiles = (g.M + 16 * TS - 1) / (16 * TS);
     const int groups = (g.R + 16 * RT - 1) / (16 * RT);
     // passes side by side: a workgroup for each adapter of a tile while there are few tiles
     const int most = std::min(std::min(16 * TS, g.adapters), g.M);
     const int side = std::max(1, std::min(most, 1024 / std::max(1, tiles * g.ks * groups)));
-    hipLaunchKernelGGL((lora_down_kernel<BF16, TS, RT, down_waves(TS), 2>), dim3(tiles, side, g.ks * groups), dim3(64 * down_waves(TS)), 0, s,
-                       g);
+    hipLaunchKernelGGL((lora_down_kernel<BF16, TS, RT, DOWN_WAVES, 2>), dim3(tiles, side, g.ks * groups),
+                       dim3(64 * DOWN_WAVES), 0, s, g);
     const int blocks = (g.N + 64 * UP_WAVES - 1) / (64 * UP_WAVES);
-    const int per_wave = std::max(1, std::min(4, (int)((int64_t)blocks * tiles / 1024)));
+    const int per_wave = (int)std::max<int64_t>(1, std::min<int64_t>(4, (int64_t)blocks * tiles / 1024));
     const int ranges = (blocks + per_wave - 1) / per_wave;
     const int side2 = (int)std::max<int64_t>(1, std::min<int64_t>(most, 1024 / ((int64_t)tiles * ranges)));
     const dim3 grid(tiles, ranges, side2);
@@ -383,12 +308,12 @@ void launch_cfg(const LoraArgs& g, hipStream_t s) {
         hipLaunchKernelGGL((lora_up_kernel<BF16, TS, 2, 4>), grid, dim3(64 * UP_WAVES), lds, s, g, per_wave);
 }
 
-template <bool BF16, int TS>
-void launch_ts(const LoraArgs& g, hipStream_t s) {
+template <bool BF16>
+void launch_t(const LoraArgs& g, hipStream_t s) {
     switch (rank_tiles(g.R)) {
-        case 1: return launch_cfg<BF16, TS, 1>(g, s);
-        case 2: return launch_cfg<BF16, TS, 2>(g, s);
-        default: return launch_cfg<BF16, TS, 4>(g, s);
+        case 1: return launch_cfg<BF16, 1>(g, s);
+        case 2: return launch_cfg<BF16, 2>(g, s);
+        default: return launch_cfg<BF16, 4>(g, s);
     }
 }
 
@@ -397,15 +322,16 @@ void launch_ts(const LoraArgs& g, hipStream_t s) {
 // K slices of the first product: workgroups to fill the chip, at most 4 (the
 // second product adds them up), a step of 64 channels at least for each wave
 int lora_k_slices(int M, int K, int R) {
-    const int ts = tile_rows(M), rows = 16 * ts, ranks = 16 * rank_tiles(R);
+    if (lora_wide(M, R)) return lora_wide_k_slices(M, K, R);
+    const int rows = 16 * TS, ranks = 16 * rank_tiles(R);
     const int wgs = (M + rows - 1) / rows * ((R + ranks - 1) / ranks);
-    return std::max(1, std::min(std::min(MAX_SLICES, 512 / std::max(1, wgs)), K / STEP / down_waves(ts)));
+    return std::max(1, std::min(std::min(LORA_MAX_SLICES, 512 / std::max(1, wgs)), K / LORA_STEP / DOWN_WAVES));
 }
 
 void launch_lora(const LoraArgs& g, bool bf16, hipStream_t s) {
-    const bool wide = tile_rows(g.M) > 1;
-    if (bf16) wide ? launch_ts<true, 2>(g, s) : launch_ts<true, 1>(g, s);
-    else wide ? launch_ts<false, 2>(g, s) : launch_ts<false, 1>(g, s);
+    if (lora_wide(g.M, g.R)) return launch_lora_wide(g, bf16, s);
+    if (bf16) launch_t<true>(g, s);
+    else launch_t<false>(g, s);
 }
 
 }  // namespace wq
