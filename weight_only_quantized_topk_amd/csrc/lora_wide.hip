@@ -15,6 +15,12 @@ namespace wq {
 
 namespace {
 
+#ifndef OCC
+#define OCC 3
+#define PERMAX 8
+#define PERWG 1024
+#define KSWG 256
+#endif
 constexpr int DOWN_WAVES = 8;
 constexpr int UP_WAVES = 4;
 // a wave's lanes exchange values through LDS that no other wave touches: the
@@ -28,7 +34,7 @@ constexpr int TS = 2;  // 16-token tiles of the first product's workgroups
 
 // t = x A^T: 32 tokens, one slice of K, 16 RT ranks a workgroup; its waves take
 // the 64-channel steps of the slice in turn.  A wave's step: its 32 x rows and
-// 16 RT rank rows of 128 bytes go through registers (one step ahead) into the
+// 16 RT rank rows of 128 bytes go through registers (two steps ahead) into the
 // wave's own part of LDS, piece c of row r in slot c ^ (r % 8), so that the 8
 // lanes of an access phase fall on different banks both ways; no barrier.
 template <bool BF16, int RT>
@@ -66,14 +72,13 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void lora_wide_down_kernel(LoraArg
         for (int t = 0; t < TS; ++t)
 #pragma unroll
             for (int r = 0; r < RT; ++r) acc[t][r] = f32x4{0.f, 0.f, 0.f, 0.f};
-        u32x4 v[LOADS];
-        auto load = [&](int s) {
+        u32x4 va[LOADS], vb[LOADS];
+        auto load = [&](int s, u32x4 (&v)[LOADS]) {
             const int c = min(LORA_STEP * s + 8 * piece, g.K - 8);
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) v[i] = ldg128(row[i] + c);
         };
-        if (s0 < s1) load(s0);
-        for (int s = s0; s < s1; s += DOWN_WAVES) {
+        auto step = [&](int s, u32x4 (&v)[LOADS]) {
             if (LORA_STEP * (s + 1) > g.K) {  // channels past K: zeros on both sides
 #pragma unroll
                 for (int i = 0; i < LOADS; ++i)
@@ -82,7 +87,7 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void lora_wide_down_kernel(LoraArg
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) own[(8 * i + lrow) * 8 + (piece ^ lrow)] = v[i];
             wave_lds_order();
-            if (s + DOWN_WAVES < s1) load(s + DOWN_WAVES);
+            if (s + 2 * DOWN_WAVES < s1) load(s + 2 * DOWN_WAVES, v);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int slot = (q + 4 * h) ^ (col & 7);
@@ -97,6 +102,12 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void lora_wide_down_kernel(LoraArg
                 }
             }
             wave_lds_order();
+        };
+        if (s0 < s1) load(s0, va);
+        if (s0 + DOWN_WAVES < s1) load(s0 + DOWN_WAVES, vb);
+        for (int s = s0; s < s1; s += 2 * DOWN_WAVES) {
+            step(s, va);
+            if (s + DOWN_WAVES < s1) step(s + DOWN_WAVES, vb);
         }
         __syncthreads();
         f32x4* red = reinterpret_cast<f32x4*>(lds);
@@ -128,7 +139,7 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void lora_wide_down_kernel(LoraArg
 // slot p ^ (n / 8) of its row (of CP slots): 8 lanes of a read, rows 8 apart,
 // fall on different banks.  RC: chunks of 32 ranks.
 template <bool BF16, int RC>
-__global__ __launch_bounds__(64 * UP_WAVES, RC <= 2 ? 3 : 1) void lora_wide_up_kernel(LoraArgs g, int per, int ranges) {
+__global__ __launch_bounds__(64 * UP_WAVES, RC <= 2 ? OCC : 1) void lora_wide_up_kernel(LoraArgs g, int per, int ranges) {
     constexpr int CP = 4 * RC;                    // slots of a B row
     constexpr int STAGE = 128 * CP / (64 * UP_WAVES);  // pieces a thread moves per step
     constexpr int BUF = 128 * CP;
@@ -272,7 +283,7 @@ template <bool BF16, int RC>
 void launch_up(const LoraArgs& g, hipStream_t s) {
     const int tiles = (g.M + 63) / 64;
     const int blocks = (g.N + 127) / 128;
-    const int per = (int)std::max<int64_t>(1, std::min<int64_t>(8, (int64_t)blocks * tiles / 1024));
+    const int per = (int)std::max<int64_t>(1, std::min<int64_t>(PERMAX, (int64_t)blocks * tiles / PERWG));
     const int ranges = (blocks + per - 1) / per;
     const int side = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(64, g.adapters), 1024 / ((int64_t)tiles * ranges)));
     hipLaunchKernelGGL((lora_wide_up_kernel<BF16, RC>), dim3((unsigned)(tiles * ranges), side), dim3(64 * UP_WAVES), 0,
@@ -300,7 +311,7 @@ bool lora_wide(int M, int R) { return M > 512 && R <= 128; }
 int lora_wide_k_slices(int M, int K, int R) {
     const int ranks = 16 * rank_tiles(R);
     const int wgs = (M + 16 * TS - 1) / (16 * TS) * ((R + ranks - 1) / ranks);
-    return std::max(1, std::min(std::min(LORA_MAX_SLICES, 256 / std::max(1, wgs)), K / LORA_STEP / DOWN_WAVES));
+    return std::max(1, std::min(std::min(LORA_MAX_SLICES, KSWG / std::max(1, wgs)), K / LORA_STEP / DOWN_WAVES));
 }
 
 void launch_lora_wide(const LoraArgs& g, bool bf16, hipStream_t s) {
