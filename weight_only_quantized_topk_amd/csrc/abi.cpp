@@ -58,9 +58,12 @@ wq_status check_ptr(const void* p, const char* name) {
 }
 
 // device check: the pointer is device (or managed) memory of the current device
-wq_status check_dev(const void* p, const char* name) {
-    int cur = -1;
-    if (hipGetDevice(&cur) != hipSuccess) return fail(WQ_ERR_HIP, "hipGetDevice failed");
+wq_status current_device(int* cur) {
+    if (hipGetDevice(cur) != hipSuccess) return fail(WQ_ERR_HIP, "hipGetDevice failed");
+    return WQ_OK;
+}
+
+wq_status check_dev(const void* p, const char* name, int cur) {
     hipPointerAttribute_t attr;
     if (hipPointerGetAttributes(&attr, p) != hipSuccess) {
         (void)hipGetLastError();
@@ -71,6 +74,12 @@ wq_status check_dev(const void* p, const char* name) {
     if (attr.type == hipMemoryTypeDevice && attr.device != cur)
         return fail(WQ_ERR_DEVICE, "%s lives on device %d, current device is %d", name, attr.device, cur);
     return WQ_OK;
+}
+
+wq_status check_dev(const void* p, const char* name) {
+    int cur = -1;
+    const wq_status st = current_device(&cur);
+    return st != WQ_OK ? st : check_dev(p, name, cur);
 }
 
 #define WQ_TRY(expr)                      \
@@ -315,11 +324,11 @@ static wq_status route_grouped_args(wq::RouteGroupedArgs& g, const void* d_logit
     return WQ_OK;
 }
 
-static wq_status route_grouped_devs(const wq::RouteGroupedArgs& g) {
-    WQ_TRY(check_dev(g.logits, "logits"));
-    if (g.bias) WQ_TRY(check_dev(g.bias, "bias"));
-    WQ_TRY(check_dev(g.w_out, "topk_weights"));
-    WQ_TRY(check_dev(g.ids_out, "topk_ids"));
+static wq_status route_grouped_devs(const wq::RouteGroupedArgs& g, int cur) {
+    WQ_TRY(check_dev(g.logits, "logits", cur));
+    if (g.bias) WQ_TRY(check_dev(g.bias, "bias", cur));
+    WQ_TRY(check_dev(g.w_out, "topk_weights", cur));
+    WQ_TRY(check_dev(g.ids_out, "topk_ids", cur));
     return WQ_OK;
 }
 
@@ -331,7 +340,9 @@ wq_status moe_route_grouped(const void* d_logits, int logits_dtype, int M, int E
         WQ_TRY(route_grouped_args(g, d_logits, logits_dtype, M, E, topk, scoring, d_bias, n_group, topk_group,
                                   group_score, renormalize, routed_scale, d_topk_weights, d_topk_ids));
         if (M == 0) return ok();
-        WQ_TRY(route_grouped_devs(g));
+        int cur = -1;
+        WQ_TRY(current_device(&cur));
+        WQ_TRY(route_grouped_devs(g, cur));
         wq::launch_route_grouped(g, (hipStream_t)stream);
         return after_launch("moe_route_grouped");
     } catch (...) {
@@ -357,10 +368,12 @@ wq_status moe_route_grouped_align(const void* d_logits, int logits_dtype, int M,
         WQ_TRY(check_ptr(d_sorted_token_ids, "sorted_token_ids"));
         WQ_TRY(check_ptr(d_expert_ids, "expert_ids"));
         WQ_TRY(check_ptr(d_num_tokens_post_padded, "num_tokens_post_padded"));
-        if (M > 0) WQ_TRY(route_grouped_devs(g));
-        WQ_TRY(check_dev(d_sorted_token_ids, "sorted_token_ids"));
-        WQ_TRY(check_dev(d_expert_ids, "expert_ids"));
-        WQ_TRY(check_dev(d_num_tokens_post_padded, "num_tokens_post_padded"));
+        int cur = -1;
+        WQ_TRY(current_device(&cur));
+        if (M > 0) WQ_TRY(route_grouped_devs(g, cur));
+        WQ_TRY(check_dev(d_sorted_token_ids, "sorted_token_ids", cur));
+        WQ_TRY(check_dev(d_expert_ids, "expert_ids", cur));
+        WQ_TRY(check_dev(d_num_tokens_post_padded, "num_tokens_post_padded", cur));
         hipStream_t s = (hipStream_t)stream;
         if (M > 0 && wq::route_grouped_fused(M, topk)) {
             wq::launch_route_grouped_align(g, block_size, d_sorted_token_ids, d_expert_ids, d_num_tokens_post_padded,
@@ -444,9 +457,11 @@ wq_status wq_rms_norm(const void* d_x, int64_t x_stride, const void* d_residual,
                                                       out[p].width, rows),
                            WQ_ERR_INVALID, "%s: %s overlaps %s", who, out[o].name, out[p].name);
         }
-        WQ_TRY(check_dev(d_x, "x"));
+        int cur = -1;
+        WQ_TRY(current_device(&cur));
+        WQ_TRY(check_dev(d_x, "x", cur));
         for (const Rows* a : {&in[1], &in[2], &out[0], &out[1], &out[2], &out[3]})
-            if (a->p) WQ_TRY(check_dev(a->p, a->name));
+            if (a->p) WQ_TRY(check_dev(a->p, a->name, cur));
         wq::RmsNormArgs g{};
         g.x = static_cast<const uint16_t*>(d_x);
         g.r = static_cast<const uint16_t*>(d_residual);
@@ -1157,10 +1172,12 @@ wq_status dense_lora_gemm(const void* d_x, int64_t x_stride, int M, int K, int N
                        WQ_ERR_INVALID, "%s: the workspace overlaps %s", who, flat[i].name);
         WQ_REQUIRE(!rows_overlap(d_workspace, 0, (int64_t)need, d_x, 0, x_span, 1), WQ_ERR_INVALID,
                    "%s: the workspace overlaps x", who);
-        WQ_TRY(check_dev(d_x, "x"));
-        WQ_TRY(check_dev(d_y, "y"));
+        int cur = -1;
+        WQ_TRY(current_device(&cur));
+        WQ_TRY(check_dev(d_x, "x", cur));
+        WQ_TRY(check_dev(d_y, "y", cur));
         for (const Flat& f : flat)
-            if (f.p) WQ_TRY(check_dev(f.p, f.name));
+            if (f.p) WQ_TRY(check_dev(f.p, f.name, cur));
         wq::LoraArgs g{};
         g.x = static_cast<const uint16_t*>(d_x);
         g.ids = d_adapter_ids;

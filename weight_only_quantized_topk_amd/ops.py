@@ -36,10 +36,12 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream):
+    """The HIP stream of a call: the one given, or torch's current one on the
+    current device (its raw handle; a Stream object costs 2.5 us a call)."""
     if stream is not None:
-        return C.c_void_p(stream)
-    torch = _torch()
-    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return stream
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def act_code(dtype) -> int:
@@ -54,7 +56,9 @@ def act_code(dtype) -> int:
 def _check(t, name: str, shape, dtypes, device=None, row_stride: bool = False):
     """A tensor argument has the shape, one of the types, and is contiguous
     (with row_stride: its last dimension is, and rows do not overlap)."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape == shape and t.dtype in dtypes and t.is_contiguous() and (device is None or t.device == device):
+        return
+    if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
@@ -253,10 +257,11 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, quant: Optional[s
     rows, n = x.shape
     _int32(rows=rows, n=n)
     dev, same = x.device, (x.dtype,)
-    _check(x, "x", (rows, n), same, row_stride=True)
+    shape = x.shape
+    _check(x, "x", shape, same, row_stride=True)
     if weight is not None:
         _check(weight, "weight", (n,), same, dev)
-    if quant not in (None, "row", "static"):
+    if quant is not None and quant not in ("row", "static"):
         raise ValueError("quant must be None, 'row' or 'static', got %r" % (quant,))
     if (quant == "static") != (scale is not None):
         raise ValueError("scale goes with quant='static'")
@@ -266,30 +271,37 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, quant: Optional[s
         raise ValueError("out goes with want_out, residual_out with a residual")
     new = []
 
-    def buffer(t, name, shape, dtypes):
+    def like_x(t, name):
         if t is None:
-            t = torch.empty(shape, dtype=dtypes[0], device=dev)
+            t = torch.empty_like(x, memory_format=torch.contiguous_format)
             new.append(t)
         else:
-            _check(t, name, shape, dtypes, dev, row_stride=dtypes is same)
+            _check(t, name, shape, same, dev, row_stride=True)
         return t
 
+    rs = ros = os_ = 0  # row strides of what there is
     if residual is not None:
-        _check(residual, "residual", (rows, n), same, dev, row_stride=True)
-        residual_out = buffer(residual_out, "residual_out", (rows, n), same)
+        _check(residual, "residual", shape, same, dev, row_stride=True)
+        residual_out = like_x(residual_out, "residual_out")
+        rs, ros = _row_stride(residual), _row_stride(residual_out)
     if want_out:
-        out = buffer(out, "out", (rows, n), same)
+        out = like_x(out, "out")
+        os_ = _row_stride(out)
     if quant is not None:
-        codes = buffer(codes, "codes", (rows, n), (torch.uint8, torch.float8_e4m3fn))
-    if quant == "row":
-        scales = buffer(scales, "scales", (rows,), (torch.float32,))
-
-    def strided(t):
-        return (None, 0) if t is None else (t.data_ptr(), _row_stride(t))
-
-    check(load().wq_rms_norm(*strided(x), *strided(residual), _ptr(weight), rows, n, eps, dt, *strided(residual_out),
-                             *strided(out), _ptr(codes), _ptr(scales), 0.0 if scale is None else scale,
-                             _stream(stream)), "wq_rms_norm")
+        if codes is None:
+            codes = torch.empty_like(x, dtype=torch.uint8, memory_format=torch.contiguous_format)
+            new.append(codes)
+        else:
+            _check(codes, "codes", shape, (torch.uint8, torch.float8_e4m3fn), dev)
+        if quant == "row":
+            if scales is None:
+                scales = torch.empty(rows, dtype=torch.float32, device=dev)
+                new.append(scales)
+            else:
+                _check(scales, "scales", (rows,), (torch.float32,), dev)
+    check(load().wq_rms_norm(x.data_ptr(), _row_stride(x), _ptr(residual), rs, _ptr(weight), rows, n, eps, dt,
+                             _ptr(residual_out), ros, _ptr(out), os_, _ptr(codes), _ptr(scales),
+                             0.0 if scale is None else scale, _stream(stream)), "wq_rms_norm")
     _keep_for(stream, *new)
     return RmsNormOut(out, residual_out, codes, scales)
 
