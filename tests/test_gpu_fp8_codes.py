@@ -82,6 +82,33 @@ def test_equals_the_quantising_call(M, bs):
             assert not bool(got[pad].any())
 
 
+@pytest.mark.parametrize("M,N", [(300, 256), (4300, 256), (2200, 512), (50001, 256)])
+def test_large_batch_shapes_equal_the_quantising_call(M, N):
+    """Each tile shape of the 128-row blocks (by the number of tiles), with one power-of-two scale a row."""
+    need_gpu()
+    E, K, topk, bs = 8, 128, 2, 128
+    g = torch.Generator().manual_seed(M)
+    w = torch.randint(0, 256, (E, 2 * N, K), generator=g, dtype=torch.uint8).numpy()
+    w[(w & 0x7F) >= 0x60] &= 0x8F
+    wp, sp = wq.pack_fp8(w, np.full((E, 2 * N), 2.0 ** -6, np.float32), interleave_gate_up=True)
+    wp, sp = torch.from_numpy(wp).cuda(), torch.from_numpy(sp).cuda()
+    codes = torch.randint(0, 256, (M, K), generator=g, dtype=torch.uint8)
+    codes[(codes & 0x7F) >= 0x70] &= 0x8F
+    value = torch.from_numpy(e4m3_values(codes.numpy())).cuda()
+    codes = codes.cuda()
+    ids = torch.argsort(torch.rand((M, E), generator=g), dim=1)[:, :topk].int().cuda()
+    cap = wq.moe_align_capacity(M, topk, E, bs)
+    st, ex, nt = wq.moe_align(ids, E, bs, cap)
+    say("shapes", M, N, cap)
+    got, ref = torch.zeros((2, cap, N), dtype=torch.uint8, device="cuda")
+    common = (M, topk, E, 2 * N, K, wp, sp, st, ex, nt, cap, bs)
+    wq.moe_fp8_codes_gemm(wq.WQ_STAGE_GATE_UP, codes, torch.full((M,), 0.125, device="cuda"), *common, got, out_scale=0.5)
+    work = torch.empty(M * K + 256, dtype=torch.uint8, device="cuda")
+    wq.moe_fp8_w8a8_gemm(wq.WQ_STAGE_GATE_UP, (value * 0.125).bfloat16(), *common, None, ref, work, 0.125, 0.5)
+    torch.cuda.synchronize()
+    assert bool(got.any()) and torch.equal(got, ref)
+
+
 @pytest.mark.parametrize("bs", [16, 128])
 def test_nan_rows_stay_their_own(bs):
     need_gpu()

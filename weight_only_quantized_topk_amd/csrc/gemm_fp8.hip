@@ -56,20 +56,22 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return (uint32_t)w;
 }
 
-// the scale of a pair's A row: its token's own (x codes that the caller
-// quantised row by row), or the tensor's
-template <int STAGE>
-__device__ __forceinline__ float a_row_scale(const Fp8GemmArgs& g, int pair, int T) {
-    if constexpr (STAGE != STAGE_DOWN) {
-        if (g.row_scales) return pair < T ? g.row_scales[pair / g.topk] : 0.0f;
-    }
-    return g.in_scale;
+// CODES (moe_fp8_codes_gemm: x arrives as codes): a pair's products are scaled by
+// its token's own scale where there are row scales, by the tensor's otherwise.
+// A template parameter, and fields for arguments: with the descriptor passed by
+// reference to a helper the 512 x 128 shape of the quantising call spilled
+// registers (gate/up of 1024 tokens, 8 experts of 4096 x 3584: 120 us).
+template <bool CODES>
+__device__ __forceinline__ float row_scale(const float* row_scales, int pair, int T, int topk, float in_scale) {
+    if constexpr (CODES) return row_scales ? (pair < T ? row_scales[pair / topk] : 0.0f) : in_scale;
+    else return in_scale;
 }
 
 // H codes: e4m3x4, and a NaN code for a NaN where the caller's codes may hold one
-__device__ __forceinline__ uint32_t h_codes(const Fp8GemmArgs& g, const float (&h)[4]) {
+template <bool CODES>
+__device__ __forceinline__ uint32_t h_codes(const float (&h)[4]) {
     uint32_t w = e4m3x4(h[0], h[1], h[2], h[3]);
-    if (g.x_codes) {
+    if constexpr (CODES) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) w |= h[i] != h[i] ? 0x7Fu << (8 * i) : 0u;
     }
@@ -112,7 +114,7 @@ void launch_fp8_quant(const uint16_t* x, int64_t rows, int k, bool bf16, float s
 // QX (GATE_UP of one token): the workgroup quantises the token's row into LDS
 // itself (the quantisation kernel's arithmetic, so the same codes) and takes
 // every B operand from there; all rows of the sorted order are that token's.
-template <int STAGE, int RMAX, int NP, int NW, int DEPTH, bool QX = false>
+template <int STAGE, int RMAX, int NP, int NW, int DEPTH, bool QX = false, bool CODES = false>
 __global__ __launch_bounds__(64 * NW) void fp8_decode_kernel(Fp8GemmArgs g) {
     constexpr int NT = (STAGE == STAGE_GATE_UP) ? 2 * NP : NP;  // 16-row weight tiles per workgroup
     static_assert(NW * NT * RMAX * 1024 <= 64 * 1024, "LDS reduction buffer");
@@ -221,7 +223,7 @@ __global__ __launch_bounds__(64 * NW) void fp8_decode_kernel(Fp8GemmArgs g) {
             const int r = item % R;
             const int p = (sb_first + s0 + r) * 16 + (lane & 15);
             const int pair = g.sorted[p];
-            const float a_scale = a_row_scale<STAGE>(g, pair, T);
+            const float rs = row_scale<CODES>(g.row_scales, pair, T, g.topk, g.in_scale);
             if constexpr (STAGE == STAGE_GATE_UP) {
                 const int tg = 2 * pp, tu = 2 * pp + 1;
                 f32x4 gv = red[0][tg][r][lane], uv = red[0][tu][r][lane];
@@ -235,11 +237,11 @@ __global__ __launch_bounds__(64 * NW) void fp8_decode_kernel(Fp8GemmArgs g) {
                 float h[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float gt = gv[i] * a_scale * se[(NT * unit + tg) * TILE_ROWS + rowq + i];
-                    const float up = uv[i] * a_scale * se[(NT * unit + tu) * TILE_ROWS + rowq + i];
+                    const float gt = gv[i] * rs * se[(NT * unit + tg) * TILE_ROWS + rowq + i];
+                    const float up = uv[i] * rs * se[(NT * unit + tu) * TILE_ROWS + rowq + i];
                     h[i] = pair < T ? __fdiv_rn(silu_f32(gt) * up, g.out_scale) : 0.0f;
                 }
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.out) + (size_t)p * N + hcol) = h_codes(g, h);
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.out) + (size_t)p * N + hcol) = h_codes<CODES>(h);
             } else {
                 if (pair < T) {
                     f32x4 o = red[0][pp][r][lane];
@@ -248,7 +250,7 @@ __global__ __launch_bounds__(64 * NW) void fp8_decode_kernel(Fp8GemmArgs g) {
                     const int row = (NT * unit + pp) * TILE_ROWS + rowq;
                     const float rw = (STAGE == STAGE_DOWN) ? g.topk_w[pair] : 1.0f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = o[i] * a_scale * se[row + i] * rw;
+                    for (int i = 0; i < 4; ++i) o[i] = o[i] * rs * se[row + i] * rw;
                     *reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + (size_t)pair * g.n_out + row) = o;
                 }
             }
@@ -308,6 +310,13 @@ static void launch_fp8_decode_cfg(const Fp8GemmArgs& g, hipStream_t s) {
     constexpr int NT = (STAGE == STAGE_GATE_UP) ? 2 * NP : NP;
     const int nsb = g.cap / 16;
     const dim3 grid(g.n_out / (TILE_ROWS * NT), std::min(nsb, 65535), (nsb + 65534) / 65535);
+    if constexpr (STAGE != STAGE_DOWN && !QX) {
+        if (g.x_codes) {
+            hipLaunchKernelGGL((fp8_decode_kernel<STAGE, RMAX, NP, NW, DEPTH, false, true>), grid, dim3(64 * NW), 0, s,
+                               g);
+            return;
+        }
+    }
     hipLaunchKernelGGL((fp8_decode_kernel<STAGE, RMAX, NP, NW, DEPTH, QX>), grid, dim3(64 * NW), QX ? g.k_in : 0, s,
                        g);
 }
@@ -379,7 +388,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t fp8_rsrc(const void* base) {
 __device__ __forceinline__ int fp8_lds_off(int row, int ch) { return row * FP8_ROWB + ((ch ^ ((row >> 1) & 7)) << 4); }
 __device__ __forceinline__ int fp8_slot(int piece) { return (piece >> 1) + 4 * (piece & 1); }
 
-template <int STAGE, int NW, int RT, int BM, int OCC>
+template <int STAGE, int NW, int RT, int BM, int OCC, bool CODES = false>
 __global__ __launch_bounds__(NW * 64, OCC) void fp8_prefill_kernel(Fp8GemmArgs g) {
     constexpr int NT = NW * 64;
     constexpr int BN = NW * RT * 16;
@@ -530,7 +539,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void fp8_prefill_kernel(Fp8GemmArgs g
     for (int j = 0; j < TJ; ++j) {
         const int p = row0 + 16 * j + brow;
         const int pair = g.sorted[p];
-        const float a_scale = a_row_scale<STAGE>(g, pair, T);
+        const float rs = row_scale<CODES>(g.row_scales, pair, T, g.topk, g.in_scale);
         if constexpr (STAGE == STAGE_GATE_UP) {
             const int N = g.n_out / 2;
 #pragma unroll
@@ -540,11 +549,11 @@ __global__ __launch_bounds__(NW * 64, OCC) void fp8_prefill_kernel(Fp8GemmArgs g
                 float h[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float gt = acc[2 * qq][j][r] * a_scale * se[gtile * TILE_ROWS + 4 * g4 + r];
-                    const float up = acc[2 * qq + 1][j][r] * a_scale * se[(gtile + 1) * TILE_ROWS + 4 * g4 + r];
+                    const float gt = acc[2 * qq][j][r] * rs * se[gtile * TILE_ROWS + 4 * g4 + r];
+                    const float up = acc[2 * qq + 1][j][r] * rs * se[(gtile + 1) * TILE_ROWS + 4 * g4 + r];
                     h[r] = (pair < T) ? __fdiv_rn(silu_f32(gt) * up, g.out_scale) : 0.0f;
                 }
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.out) + (size_t)p * N + hcol) = h_codes(g, h);
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.out) + (size_t)p * N + hcol) = h_codes<CODES>(h);
             }
         } else {
             if (pair < T) {
@@ -554,7 +563,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void fp8_prefill_kernel(Fp8GemmArgs g
                     const int n0 = (rt0 + t) * TILE_ROWS + 4 * g4;
                     f32x4 o;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) o[r] = acc[t][j][r] * a_scale * se[n0 + r] * rw;
+                    for (int r = 0; r < 4; ++r) o[r] = acc[t][j][r] * rs * se[n0 + r] * rw;
                     *reinterpret_cast<f32x4*>(yslab + (size_t)pair * g.n_out + n0) = o;
                 }
             }
@@ -562,10 +571,10 @@ __global__ __launch_bounds__(NW * 64, OCC) void fp8_prefill_kernel(Fp8GemmArgs g
     }
 }
 
-template <int STAGE, int NW, int RT, int BM, int OCC>
+template <int STAGE, int NW, int RT, int BM, int OCC, bool CODES = false>
 static void launch_fp8_prefill_cfg(const Fp8GemmArgs& g, int ksplit, hipStream_t s) {
     const dim3 grid(g.n_out / (NW * RT * 16), g.cap / BM, ksplit);
-    hipLaunchKernelGGL((fp8_prefill_kernel<STAGE, NW, RT, BM, OCC>), grid, dim3(NW * 64), 0, s, g);
+    hipLaunchKernelGGL((fp8_prefill_kernel<STAGE, NW, RT, BM, OCC, CODES>), grid, dim3(NW * 64), 0, s, g);
 }
 
 // shapes (weight rows x token rows, waves, workgroups per CU):
@@ -605,6 +614,26 @@ int fp8_down_split(int T, int E, int n_out, int k_in, int block_size) {
         if (t < 0.85 * best_t) best = ks, best_t = t;
     }
     return best;
+}
+
+// moe_fp8_codes_gemm, 128-row blocks: the 512 x 128 shape pays once its grid
+// fills the chip several times over; below that 256 x 128 (8 waves of 2 tiles),
+// and for the least tiles 128 x 128.  us by shape (512 / 256 / 128 rows) and
+// tiles of 512 rows, 8 experts, K = 4096: 56 tiles 68 / 43 / 37, 84 tiles 76 /
+// 49 / 52, 476 tiles 203 / 177 / 182, 560 tiles 208 / 189 / 203, 1120 tiles 336 /
+// 367 / 409, 3808 tiles 1070 / 1252 / 1376.
+template <int STAGE>
+static void launch_fp8_prefill_codes(const Fp8GemmArgs& g, hipStream_t s) {
+    if (g.block_size == 64) {
+        if (fp8_shape(g.n_out, 64) == F8_T256) launch_fp8_prefill_cfg<STAGE, 4, 4, 64, 2, true>(g, 1, s);
+        else launch_fp8_prefill_cfg<STAGE, 4, 2, 64, 2, true>(g, 1, s);
+        return;
+    }
+    const long T = (long)g.M * g.topk;
+    const long tiles = (T + std::min<long>(T, g.E) * 64 + 127) / 128 * g.n_out / 512;  // as fp8_down_split counts
+    if (g.n_out % 512 == 0 && tiles > 768) launch_fp8_prefill_cfg<STAGE, 8, 4, 128, 1, true>(g, 1, s);
+    else if (g.n_out % 256 == 0 && tiles > 64) launch_fp8_prefill_cfg<STAGE, 8, 2, 128, 1, true>(g, 1, s);
+    else launch_fp8_prefill_cfg<STAGE, 4, 2, 128, 2, true>(g, 1, s);
 }
 
 template <int STAGE>
@@ -776,7 +805,9 @@ void launch_fp8_down_combine(bool bf16, const Fp8GemmArgs& g, hipStream_t s) {
 int launch_gemm_fp8(int stage, const Fp8GemmArgs& g, hipStream_t s) {
     if (fp8_prefill_supported(g.n_out, g.k_in, g.block_size)) {
         const int ks = stage == STAGE_DOWN ? fp8_down_split(g.M * g.topk, g.E, g.n_out, g.k_in, g.block_size) : 1;
-        if (stage == STAGE_GATE_UP) launch_fp8_prefill_s<STAGE_GATE_UP>(g, 1, s);
+        if (g.x_codes && stage == STAGE_GATE_UP) launch_fp8_prefill_codes<STAGE_GATE_UP>(g, s);
+        else if (g.x_codes) launch_fp8_prefill_codes<STAGE_RAW>(g, s);
+        else if (stage == STAGE_GATE_UP) launch_fp8_prefill_s<STAGE_GATE_UP>(g, 1, s);
         else if (stage == STAGE_DOWN) launch_fp8_prefill_s<STAGE_DOWN>(g, ks, s);
         else launch_fp8_prefill_s<STAGE_RAW>(g, 1, s);
         return ks;
