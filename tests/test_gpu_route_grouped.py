@@ -62,7 +62,7 @@ def test_scores_and_groups(dt, scoring, biased):
                       topk_group=TG, group_score=score, renormalize=renorm, routed_scale=2.5 if renorm else 16.0)
 
 
-@pytest.mark.parametrize("M", [1, 2, 7, 15, 16, 17, 64, 300])
+@pytest.mark.parametrize("M", [1, 2, 7, 15, 16, 17, 31, 63, 64, 65, 300])
 @pytest.mark.parametrize("block", [16, 64, 256])
 def test_align(M, block):
     """The fused sort (one wave up to 64 pairs, a workgroup above) and the separate one."""
@@ -71,6 +71,8 @@ def test_align(M, block):
     check(logits_of(M, 256, "bf16", M), 8, bias_of(256, 1), block, scoring="sigmoid", n_group=8, topk_group=4,
           group_score="top2", routed_scale=2.5)
     check(logits_of(M, 8, "f16", M), 2, None, block)
+    check(logits_of(M, 64, "f32", M), 16, bias_of(64, 1), block, n_group=4, topk_group=3, group_score="top2")
+    check(logits_of(M, 96, "bf16", M), 4, bias_of(96, 1), block, scoring="sigmoid")
     check(logits_of(M, 1024, "f32", M), 16, bias_of(1024, 1), block, scoring="sigmoid")
 
 
@@ -135,6 +137,42 @@ def test_plain_softmax_is_moe_route():
             torch.cuda.synchronize()
             assert torch.equal(a[1], b[1])
             assert float(((a[0] - b[0]).abs() / a[0]).max()) <= 2.0 ** -23
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_large_batches(dt):
+    """Four tokens a wave, over group and expert counts (16-byte loads or not, lanes left over)."""
+    need_gpu()
+    for E, G, TG, k in ((1, 1, 1, 1), (8, 1, 1, 2), (9, 3, 2, 4), (60, 3, 2, 5), (64, 16, 5, 7), (96, 1, 1, 16), (160, 8, 3, 6),
+                        (256, 8, 4, 8), (256, 1, 1, 8), (250, 5, 2, 10), (272, 1, 1, 8), (512, 32, 7, 8), (1024, 4, 2, 16)):
+        lg = logits_of(2051, E, dt, E + G)
+        for scoring, biased, score, renorm in (("softmax", False, "max", True), ("softmax", True, "top2", False),
+                                               ("sigmoid", True, "max", True), ("sigmoid", False, "top2", True)):
+            if score == "top2" and G > 1 and E // G < 2:
+                continue
+            check(lg, k, bias_of(E, E) if biased else None, None, "large", scoring=scoring, n_group=G, topk_group=TG,
+                  group_score=score, renormalize=renorm)
+
+
+def test_large_batches_of_special_rows():
+    """Ties, masked experts, empty rows and NaN rows among the four tokens of a wave."""
+    need_gpu()
+    rng = np.random.default_rng(4)
+    lg = torch.from_numpy(rng.integers(-2, 3, size=(2050, 160)).astype(np.float32))
+    lg[5] = -np.inf
+    lg[6, 3:] = -np.inf
+    lg[9] = 3.0e38
+    for how in (dict(n_group=8, topk_group=3), dict(scoring="sigmoid", n_group=8, topk_group=3, group_score="top2")):
+        for b in (None, bias_of(160, 1)):
+            check(lg, 6, b, None, "special rows", **how)
+            bad = lg.clone()
+            bad[4] = np.nan
+            bad[7, ::3] = np.nan
+            ids = wq.moe_route_grouped(bad.cuda(), 6, bias=None if b is None else b.cuda(), **how)[1].cpu().numpy()
+            keep = np.delete(np.arange(2050), [4, 7])
+            ref = route(lg.double().numpy(), 6, bias=None if b is None else b.double().numpy(), **how)[1]
+            assert np.array_equal(ids[keep], ref[keep])
+            assert all(len(set(ids[m])) == 6 and 0 <= ids[m].min() and ids[m].max() < 160 for m in (4, 7))
 
 
 def test_large_batch_and_empty():

@@ -375,7 +375,7 @@ wq_status moe_route_grouped_align(const void* d_logits, int logits_dtype, int M,
         WQ_TRY(check_dev(d_expert_ids, "expert_ids", cur));
         WQ_TRY(check_dev(d_num_tokens_post_padded, "num_tokens_post_padded", cur));
         hipStream_t s = (hipStream_t)stream;
-        if (M > 0 && wq::route_grouped_fused(M, topk)) {
+        if (M > 0 && wq::route_grouped_fused(g)) {
             wq::launch_route_grouped_align(g, block_size, d_sorted_token_ids, d_expert_ids, d_num_tokens_post_padded,
                                            (int)capacity, s);
             return after_launch("moe_route_grouped_align");

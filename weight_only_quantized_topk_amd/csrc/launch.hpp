@@ -45,8 +45,8 @@ struct RouteGroupedArgs {
     float scale;              // routed weights are multiplied by it
 };
 void launch_route_grouped(const RouteGroupedArgs& g, hipStream_t s);
-// with the sort, in one kernel (M and M * topk within route_grouped_fused)
-bool route_grouped_fused(int M, int topk);
+// with the sort, in one kernel (small batches: where route_grouped_fused)
+bool route_grouped_fused(const RouteGroupedArgs& g);
 void launch_route_grouped_align(const RouteGroupedArgs& g, int BS, int32_t* sorted, int32_t* expert_ids,
                                 int32_t* ntpp, int cap, hipStream_t s);
 

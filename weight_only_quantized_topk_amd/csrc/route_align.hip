@@ -332,22 +332,22 @@ void launch_route_align(const float* logits, int M, int E, int topk, int renorma
 }
 
 // ---------------------------------------------------------------------------
-// moe_route_grouped: one wave per token (route_grouped.hpp), four tokens a
+// moe_route_grouped: 16 or 64 lanes per token (route_grouped.hpp), 256 lanes a
 // workgroup; with the sort for small batches in one workgroup, as
 // route_align_kernel: the pairs' experts stay in LDS, up to 64 pairs are sorted
 // by one wave, more by the whole workgroup.
 // ---------------------------------------------------------------------------
-template <int PL>
-__global__ __launch_bounds__(256) void route_grouped_kernel(RouteGroupedArgs g, int lpg, int per) {
-    const int m = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (m >= g.M) return;
-    route_token_grouped<PL>(g, m, threadIdx.x & 63, lpg, per, nullptr);
+template <int W, int PL>
+__global__ __launch_bounds__(256) void route_grouped_kernel(RouteGroupedArgs g, GroupedLayout y) {
+    const int m = blockIdx.x * (256 / W) + threadIdx.x / W;
+    const int r = threadIdx.x % W;
+    if (W == 64 && m >= g.M) return;  // a whole wave
+    route_token_grouped<W, PL>(g, y, min(m, g.M - 1), m < g.M, r, (threadIdx.x & 63) - r, nullptr);
 }
 
 template <int PL>
-__global__ __launch_bounds__(ALIGN_THREADS) void route_grouped_align_kernel(RouteGroupedArgs g, int lpg, int per,
-                                                                            int BS, int nbits,
-                                                                            int32_t* __restrict__ sorted,
+__global__ __launch_bounds__(ALIGN_THREADS) void route_grouped_align_kernel(RouteGroupedArgs g, GroupedLayout y, int BS,
+                                                                            int nbits, int32_t* __restrict__ sorted,
                                                                             int32_t* __restrict__ expert_ids,
                                                                             int32_t* __restrict__ ntpp, int cap) {
     extern __shared__ int smem[];
@@ -355,7 +355,7 @@ __global__ __launch_bounds__(ALIGN_THREADS) void route_grouped_align_kernel(Rout
     const int wave = threadIdx.x >> 6;
     const int T = g.M * g.topk;
     int* sids = smem;
-    if (wave < g.M) route_token_grouped<PL>(g, wave, lane, lpg, per, sids + wave * g.topk);
+    if (wave < g.M) route_token_grouped<64, PL>(g, y, wave, true, lane, 0, sids + wave * g.topk);
     __syncthreads();
     if (T <= ROUTE_ALIGN_WAVE_MAX) {
         if (wave == 0) align_pairs(sids, T, BS, cap, lane, sorted, expert_ids, ntpp);
@@ -371,33 +371,56 @@ static void with_per_lane(int per, F f) {
     else if (per <= 2) f(std::integral_constant<int, 2>{});
     else if (per <= 4) f(std::integral_constant<int, 4>{});
     else if (per <= 8) f(std::integral_constant<int, 8>{});
+    else if (per <= 12) f(std::integral_constant<int, 12>{});
     else if (per <= 16) f(std::integral_constant<int, 16>{});
     else f(std::integral_constant<int, 32>{});
 }
 
+// Lanes per token: 16 lanes and four tokens a wave take fewer instructions per
+// token, 64 lanes the shorter chain (a lane's exponentials in double and its
+// compares follow one another).  us with 16 / 64 lanes: 8 experts (1 per lane)
+// 512 tokens 3.0 / 3.2, 4096 tokens 3.2 / 4.3; 160 experts (12 per lane) 1024
+// tokens 7.5 / 5.4, 4096 tokens 7.7 / 8.2; 256 experts (16 per lane) 4096 tokens
+// 11.4 / 9.7, 8192 tokens 14.0 / 16.1
+static bool route_by_16(const RouteGroupedArgs& g, const GroupedLayout& few) {
+    return few.lpg > 0 && few.per <= 16 && g.M >= 400 * few.per;
+}
+
 void launch_route_grouped(const RouteGroupedArgs& g, hipStream_t s) {
-    const int lpg = grouped_lanes(g.groups), per = grouped_per_lane(g.E, g.groups);
-    with_per_lane(per, [&](auto P) {
-        hipLaunchKernelGGL(route_grouped_kernel<decltype(P)::value>, dim3((g.M + 3) / 4), dim3(256), 0, s, g, lpg, per);
+    const GroupedLayout few = grouped_layout(g.E, g.groups, 16);
+    if (route_by_16(g, few)) {
+        with_per_lane(few.per, [&](auto P) {
+            if constexpr (decltype(P)::value <= 16)
+                hipLaunchKernelGGL((route_grouped_kernel<16, decltype(P)::value>), dim3((g.M + 15) / 16), dim3(256), 0, s,
+                                   g, few);
+        });
+        return;
+    }
+    const GroupedLayout y = grouped_layout(g.E, g.groups, 64);
+    with_per_lane(y.per, [&](auto P) {
+        hipLaunchKernelGGL((route_grouped_kernel<64, decltype(P)::value>), dim3((g.M + 3) / 4), dim3(256), 0, s, g, y);
     });
 }
 
-bool route_grouped_fused(int M, int topk) { return route_align_fused(M, topk); }
+// with the sort in one workgroup, a wave per token: up to 16 tokens.  (Up to 64
+// tokens by 16 lanes each, in the one workgroup: 61 tokens, 96 experts 12.4 us;
+// two launches 8.6 us.)
+bool route_grouped_fused(const RouteGroupedArgs& g) { return route_align_fused(g.M, g.topk); }
 
 void launch_route_grouped_align(const RouteGroupedArgs& g, int BS, int32_t* sorted, int32_t* expert_ids,
                                 int32_t* ntpp, int cap, hipStream_t s) {
-    const int lpg = grouped_lanes(g.groups), per = grouped_per_lane(g.E, g.groups);
+    const GroupedLayout y = grouped_layout(g.E, g.groups, 64);
     const int T = g.M * g.topk;
     const bool one_wave = T <= ROUTE_ALIGN_WAVE_MAX;
-    const int threads = one_wave ? 64 * std::min(g.M, ALIGN_WAVES) : ALIGN_THREADS;
+    const int threads = one_wave ? 64 * g.M : ALIGN_THREADS;
     const size_t lds = sizeof(int) * ((size_t)T + (one_wave ? 0 : (size_t)g.E * ALIGN_WAVES));
-    with_per_lane(per, [&](auto P) {
+    with_per_lane(y.per, [&](auto P) {
         constexpr int PL = decltype(P)::value;
         if (lds > 65536)
             (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&route_grouped_align_kernel<PL>),
                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        hipLaunchKernelGGL(route_grouped_align_kernel<PL>, dim3(1), dim3(threads), lds, s, g, lpg, per, BS,
-                           id_bits(g.E), sorted, expert_ids, ntpp, cap);
+        hipLaunchKernelGGL(route_grouped_align_kernel<PL>, dim3(1), dim3(threads), lds, s, g, y, BS, id_bits(g.E), sorted,
+                           expert_ids, ntpp, cap);
     });
 }
 

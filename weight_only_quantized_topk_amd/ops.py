@@ -155,30 +155,31 @@ _GROUP_SCORE = {"max": WQ_GROUP_MAX, "top2": WQ_GROUP_TOP2}
 
 def _grouped_args(logits, topk, scoring, bias, n_group, topk_group, group_score, topk_weights, topk_ids):
     torch = _torch()
-    codes = {torch.float32: WQ_F32, torch.float16: WQ_F16, torch.bfloat16: WQ_BF16}
+    f32, dt = torch.float32, logits.dtype
+    code = WQ_F32 if dt == f32 else WQ_BF16 if dt == torch.bfloat16 else WQ_F16
     if logits.dim() != 2:
         raise ValueError("logits must be [M, E], got %s" % list(logits.shape))
     M, E = logits.shape
-    _int32(M=M, E=E, topk=topk, n_group=n_group, topk_group=topk_group)
-    _check(logits, "logits", (M, E), codes)
+    if topk < 1 or max(M, E, topk, abs(n_group), abs(topk_group)) > 0x7fffffff:
+        raise ValueError("topk must be >= 1 and sizes fit 32 bits: M %d E %d topk %d n_group %d topk_group %d"
+                         % (M, E, topk, n_group, topk_group))
+    _check(logits, "logits", (M, E), (f32, torch.float16, torch.bfloat16))
     if scoring not in _SCORING or group_score not in _GROUP_SCORE:
         raise ValueError("scoring %r not in %s or group_score %r not in %s"
                          % (scoring, list(_SCORING), group_score, list(_GROUP_SCORE)))
     dev = logits.device
     if bias is not None:
-        _check(bias, "bias", (E,), (torch.float32,), dev)
-    if topk < 1:
-        raise ValueError("topk must be >= 1, got %d" % topk)
+        _check(bias, "bias", (E,), (f32,), dev)
     new = []
     if topk_weights is None:
-        new.append(topk_weights := torch.empty((M, topk), dtype=torch.float32, device=dev))
+        new.append(topk_weights := torch.empty((M, topk), dtype=f32, device=dev))
     else:
-        _check(topk_weights, "topk_weights", (M, topk), (torch.float32,), dev)
+        _check(topk_weights, "topk_weights", (M, topk), (f32,), dev)
     if topk_ids is None:
-        new.append(topk_ids := torch.empty((M, topk), dtype=torch.int32, device=dev))
+        new.append(topk_ids := torch.empty_like(topk_weights, dtype=torch.int32))
     else:
         _check(topk_ids, "topk_ids", (M, topk), (torch.int32,), dev)
-    return M, E, codes[logits.dtype], topk_weights, topk_ids, new
+    return M, E, code, topk_weights, topk_ids, new
 
 
 def moe_route_grouped(logits, topk: int, scoring: str = "softmax", bias=None, n_group: int = 1, topk_group: int = 1,
@@ -214,17 +215,24 @@ def moe_route_grouped_align(logits, topk: int, block_size: int, scoring: str = "
     if block_size < 1:
         raise ValueError("block_size must be >= 1, got %d" % block_size)
     cap = moe_align_capacity(M, topk, E, block_size) if capacity is None else capacity
-    dev, i32 = logits.device, torch.int32
-    arrays = [(sorted_token_ids, "sorted_token_ids", cap), (expert_ids, "expert_ids", cap // block_size),
-              (num_tokens_post_padded, "num_tokens_post_padded", 1)]
-    for k, (t, name, n) in enumerate(arrays):
-        if t is None:
-            arrays[k] = torch.empty(max(n, 1), dtype=i32, device=dev)
-            new.append(arrays[k])
-        else:
-            if t.dim() != 1 or t.numel() < n:
+    dev, i32, blocks = logits.device, torch.int32, cap // block_size
+    if sorted_token_ids is None and expert_ids is None and num_tokens_post_padded is None:
+        # one allocation for the three, each at a multiple of 16 bytes
+        rows = -(-max(cap, 1) // 4) * 4
+        new.append(torch.empty(rows + 4 + max(blocks, 1), dtype=i32, device=dev))
+        arrays = torch.split_with_sizes(new[-1], (rows, 1, 3, max(blocks, 1)))
+        arrays = [arrays[0], arrays[3], arrays[1]]
+    else:
+        arrays = [(sorted_token_ids, "sorted_token_ids", cap), (expert_ids, "expert_ids", blocks),
+                  (num_tokens_post_padded, "num_tokens_post_padded", 1)]
+        for k, (t, name, n) in enumerate(arrays):
+            if t is None:
+                t = torch.empty(max(n, 1), dtype=i32, device=dev)
+                new.append(t)
+            elif t.dim() != 1 or t.numel() < n:
                 raise ValueError("%s must hold %d values, got %s" % (name, n, list(t.shape)))
-            _check(t, name, t.shape, (i32,), dev)
+            else:
+                _check(t, name, t.shape, (i32,), dev)
             arrays[k] = t
     check(load().moe_route_grouped_align(_ptr(logits), dt, M, E, topk, _SCORING[scoring], _ptr(bias), n_group,
                                          topk_group, _GROUP_SCORE[group_score], int(bool(renormalize)), routed_scale,
@@ -255,7 +263,8 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, quant: Optional[s
     if x.dim() != 2:
         raise ValueError("x must be [rows, n], got %s" % list(x.shape))
     rows, n = x.shape
-    _int32(rows=rows, n=n)
+    if rows > 0x7fffffff or n > 0x7fffffff:
+        raise ValueError("x is too large: %s" % list(x.shape))
     dev, same = x.device, (x.dtype,)
     shape = x.shape
     _check(x, "x", shape, same, row_stride=True)
