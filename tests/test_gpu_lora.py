@@ -161,6 +161,24 @@ def test_range_of_the_intermediate(kind):
         assert (np.abs(f64(got) - ref) <= lim).all()
 
 
+def test_offsets_beyond_32_bits():
+    """x, y and t of more than 2^31 bytes, y of more than 2^31 values: the last rows against the plain form."""
+    need_gpu()
+    M, K, N, R = 70030, 16384, 32768, 8
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    tail = case(77, K, N, R, 2, "one", torch.bfloat16, 9)
+    x[-77:], y[-77:] = tail[0], tail[5]
+    ids = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    ids[-77:] = tail[1]
+    ids[::1000] = 0
+    ref, lim = plain(tail[0], ids[-77:], *tail[2:5], tail[5], "bf16")
+    wq.dense_lora_gemm(x, ids, tail[2], tail[3], tail[4], y)
+    torch.cuda.synchronize()
+    assert (np.abs(f64(y[-77:]) - ref) <= lim).all()
+    assert not bool(y[:-77].any())
+
+
 def test_dense_with_adapters_is_the_two_calls():
     need_gpu()
     K, N = 512, 384
@@ -190,8 +208,8 @@ def test_dense_with_adapters_is_the_two_calls():
 def test_graph_stream_and_repeats():
     """Replays with new inputs, another stream, and the same bits every time; M = 0."""
     need_gpu()
-    for M in (24, 900):
-        x, i, a, b, s, y = case(M, 1024, 520, 24, 5, "rows", torch.bfloat16, 8)
+    for M, R in ((24, 24), (900, 24), (900, 64), (900, 200)):
+        x, i, a, b, s, y = case(M, 1024, 520, R, 5, "rows", torch.bfloat16, 8)
         ref = wq.dense_lora_gemm(x, i, a, b, s, y.clone())
         for _ in range(3):
             assert torch.equal(wq.dense_lora_gemm(x, i, a, b, s, y.clone()), ref)

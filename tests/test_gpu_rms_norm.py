@@ -121,6 +121,16 @@ def test_many_rows():
     for rows, n in ((70001, 64), (4099, 1024), (2050, 5120)):
         say("many rows", rows, n)
         check(*inputs(rows, n, torch.bfloat16, 1), "bf16", "row", what="%d x %d" % (rows, n))
+    # more workgroups than one dimension of a launch is given: 256 and 1024 threads a row
+    for rows, n in (((1 << 20) + 3, 520), (4 * (1 << 20) + 9, 8), ((1 << 20) + 5, 2049)):
+        say("many rows", rows, n)
+        x = torch.full((rows, n), 3.0, dtype=torch.bfloat16, device="cuda")
+        x[-1] = torch.arange(n, device="cuda") % 7
+        out = wq.rms_norm(x, quant=None).out
+        one = wq.rms_norm(x[-1:].clone()).out
+        torch.cuda.synchronize()
+        assert torch.equal(out[-1:], one) and bool((out[:-1] == 1).all())
+        del x, out
 
 
 @pytest.mark.parametrize("n", [512, 1001, 4096, 40000])

@@ -30,6 +30,13 @@ struct Max {  // fmaxf: a NaN does not win, so the scale of a row with one is th
     static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
 };
 
+// a launch holds at most 2^32 threads along x: workgroups beyond GRID_X go on along y
+constexpr int GRID_X = 1 << 20;
+__device__ __forceinline__ int64_t block_index() { return (int64_t)blockIdx.y * GRID_X + blockIdx.x; }
+dim3 row_grid(int64_t blocks) {
+    return dim3((unsigned)std::min<int64_t>(blocks, GRID_X), (unsigned)((blocks + GRID_X - 1) / GRID_X));
+}
+
 template <class OP, int CTRL>
 __device__ __forceinline__ float dpp_step(float v) {
     const int o = __builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, 0xF, 0xF, false);
@@ -118,7 +125,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_kernel(RmsNorm
     static_assert(RPB == 1 || TPR == 64, "rows that share a workgroup are one wave each: no barrier");
     __shared__ float buf[4][TPR / 64];
     const int tid = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    const int64_t row = block_index() * RPB + threadIdx.x / TPR;
     if (row >= g.rows) return;
     const uint16_t* x = g.x + row * g.x_stride;
     const uint16_t* r = g.r ? g.r + row * g.r_stride : nullptr;
@@ -228,7 +235,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_kernel(RmsNorm
 template <bool BF16>
 __global__ __launch_bounds__(1024) void rms_norm_long_kernel(RmsNormArgs g) {
     __shared__ float buf[4][16];
-    const int64_t row = blockIdx.x;
+    const int64_t row = block_index();
+    if (row >= g.rows) return;
     const uint16_t* x = g.x + row * g.x_stride;
     const uint16_t* r = g.r ? g.r + row * g.r_stride : nullptr;
     auto value = [&](int c) {
@@ -284,7 +292,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(RmsNormArgs g) {
 template <bool BF16, int VEC, int TPR, int VPT>
 void launch_cfg(const RmsNormArgs& g, hipStream_t s) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-    hipLaunchKernelGGL((rms_norm_kernel<BF16, VEC, TPR, VPT>), dim3((unsigned)((g.rows + RPB - 1) / RPB)),
+    hipLaunchKernelGGL((rms_norm_kernel<BF16, VEC, TPR, VPT>), row_grid(((int64_t)g.rows + RPB - 1) / RPB),
                        dim3(TPR < 256 ? 256 : TPR), 0, s, g);
 }
 
@@ -304,7 +312,7 @@ void launch_t(const RmsNormArgs& g, hipStream_t s) {
         if (g.n <= 2048) return launch_cfg<BF16, 1, 256, 8>(g, s);
         if (g.n <= 8192) return launch_cfg<BF16, 1, 1024, 8>(g, s);
     }
-    hipLaunchKernelGGL(rms_norm_long_kernel<BF16>, dim3((unsigned)g.rows), dim3(1024), 0, s, g);
+    hipLaunchKernelGGL(rms_norm_long_kernel<BF16>, row_grid(g.rows), dim3(1024), 0, s, g);
 }
 
 }  // namespace
