@@ -89,9 +89,12 @@ def check(M, K, N, R, L, ids, kind, seed=1, integers=False, pad=0, scaled=True):
         assert not bad.any(), "%s: %d off, worst %.3g" % (what, bad.sum(), (np.abs(f64(y) - ref) / lim).max())
 
 
+# small batches (lora.hip), then large ones (lora_wide.hip, by rows x (K + 2 N) and rank)
 SHAPES = [(1, 8, 8, 8, 1), (1, 4096, 4096, 16, 1), (3, 40, 72, 8, 2), (16, 512, 256, 16, 16), (17, 136, 264, 24, 5),
           (33, 1024, 520, 64, 40), (64, 256, 1032, 72, 3), (100, 64, 64, 128, 7), (203, 520, 328, 200, 4),
-          (511, 264, 200, 32, 9), (513, 264, 200, 32, 9), (700, 136, 1288, 64, 70), (1025, 72, 72, 136, 3)]
+          (511, 264, 200, 32, 9), (513, 264, 200, 32, 9), (700, 136, 1288, 64, 70), (1025, 72, 72, 136, 3),
+          (1100, 520, 1608, 40, 6), (2500, 1000, 6664, 16, 9), (3000, 4096, 4104, 24, 5), (700, 264, 3000, 128, 3),
+          (400, 264, 4000, 72, 3), (300, 520, 5000, 64, 40), (2600, 136, 6504, 32, 70)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
@@ -126,12 +129,12 @@ def test_no_scales_and_column_ranges():
     assert (np.abs(f64(wide[:, 264:520]) - ref) <= lim).all()
 
 
-@pytest.mark.parametrize("M", [40, 600])
+@pytest.mark.parametrize("M", [40, 600, 3001])
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
 def test_adapters_and_rows_are_apart(M, kind):
     """NaN and infinities in one adapter's weights, or one row's input, reach that adapter's rows, that row, only."""
     need_gpu()
-    x, i, a, b, s, y = case(M, 256, 264, 16, 6, "rows", DT[kind], 5)
+    x, i, a, b, s, y = case(M, 256, 264 if M < 3000 else 6000, 16 if M < 3000 else 56, 6, "rows", DT[kind], 5)
     ref = wq.dense_lora_gemm(x, i, a, b, s, y.clone())
     bad_a, bad_b, bad_x = a.clone(), b.clone(), x.clone()
     bad_a[2] = float("nan")
@@ -208,8 +211,8 @@ def test_dense_with_adapters_is_the_two_calls():
 def test_graph_stream_and_repeats():
     """Replays with new inputs, another stream, and the same bits every time; M = 0."""
     need_gpu()
-    for M, R in ((24, 24), (900, 24), (900, 64), (900, 200)):
-        x, i, a, b, s, y = case(M, 1024, 520, R, 5, "rows", torch.bfloat16, 8)
+    for M, N, R in ((24, 520, 24), (900, 520, 24), (900, 2056, 64), (2000, 8200, 24), (900, 520, 200)):
+        x, i, a, b, s, y = case(M, 1024, N, R, 5, "rows", torch.bfloat16, 8)
         ref = wq.dense_lora_gemm(x, i, a, b, s, y.clone())
         for _ in range(3):
             assert torch.equal(wq.dense_lora_gemm(x, i, a, b, s, y.clone()), ref)

@@ -15,7 +15,7 @@ def work(seed, M):
     def rnd(*shape):
         return torch.randn(*shape, generator=g).bfloat16().cuda()
 
-    K, N, R, L = 512, 384, 64, 4
+    K, N, R, L = 512, 384 if M < 100 else 2048, 64, 4
     x, r, w = rnd(M, K), rnd(M, K), rnd(K)
     a, b, y = rnd(L, R, K) * 0.05, rnd(L, N, R), rnd(M, N)
     ids = torch.randint(-1, L, (M,), generator=g).int().cuda()

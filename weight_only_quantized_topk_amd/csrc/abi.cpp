@@ -1117,7 +1117,7 @@ static const char* lora_sizes(int M, int K, int N, int R, int adapters) {
 
 size_t dense_lora_workspace_bytes(int M, int K, int N, int R, int adapters) {
     if (M == 0 || lora_sizes(M, K, N, R, adapters)) return 0;
-    return round256((size_t)wq::lora_k_slices(M, K, R) * M * R * sizeof(float));
+    return round256((size_t)wq::lora_k_slices(M, K, N, R) * M * R * sizeof(float));
 }
 
 wq_status dense_lora_gemm(const void* d_x, int64_t x_stride, int M, int K, int N, int R, int adapters,
@@ -1193,7 +1193,7 @@ wq_status dense_lora_gemm(const void* d_x, int64_t x_stride, int M, int K, int N
         g.N = N;
         g.R = R;
         g.adapters = adapters;
-        g.ks = wq::lora_k_slices(M, K, R);
+        g.ks = wq::lora_k_slices(M, K, N, R);
         wq::launch_lora(g, act_dtype == WQ_BF16, (hipStream_t)stream);
         return after_launch(who);
     } catch (...) {

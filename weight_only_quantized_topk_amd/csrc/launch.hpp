@@ -76,9 +76,9 @@ struct LoraArgs {
     float* t;                 // workspace: [ks, M, R]
     int64_t x_stride, y_stride;
     int M, K, N, R, adapters;
-    int ks;                   // lora_k_slices(M, K, R)
+    int ks;                   // lora_k_slices(M, K, N, R)
 };
-int lora_k_slices(int M, int K, int R);
+int lora_k_slices(int M, int K, int N, int R);
 void launch_lora(const LoraArgs& g, bool bf16, hipStream_t s);
 
 struct GemmArgs {

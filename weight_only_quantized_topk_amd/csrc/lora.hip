@@ -321,15 +321,15 @@ void launch_t(const LoraArgs& g, hipStream_t s) {
 
 // K slices of the first product: workgroups to fill the chip, at most 4 (the
 // second product adds them up), a step of 64 channels at least for each wave
-int lora_k_slices(int M, int K, int R) {
-    if (lora_wide(M, R)) return lora_wide_k_slices(M, K, R);
+int lora_k_slices(int M, int K, int N, int R) {
+    if (lora_wide(M, K, N, R)) return lora_wide_k_slices(M, K, R);
     const int rows = 16 * TS, ranks = 16 * rank_tiles(R);
     const int wgs = (M + rows - 1) / rows * ((R + ranks - 1) / ranks);
     return std::max(1, std::min(std::min(LORA_MAX_SLICES, 512 / std::max(1, wgs)), K / LORA_STEP / DOWN_WAVES));
 }
 
 void launch_lora(const LoraArgs& g, bool bf16, hipStream_t s) {
-    if (lora_wide(g.M, g.R)) return launch_lora_wide(g, bf16, s);
+    if (lora_wide(g.M, g.K, g.N, g.R)) return launch_lora_wide(g, bf16, s);
     if (bf16) launch_t<true>(g, s);
     else launch_t<false>(g, s);
 }

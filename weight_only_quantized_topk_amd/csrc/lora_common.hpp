@@ -91,7 +91,7 @@ constexpr int LORA_STEP = 64;       // channels of a step of the first product
 constexpr int LORA_MAX_SLICES = 4;  // K slices of t
 
 // large batches (lora_wide.hip)
-bool lora_wide(int M, int R);
+bool lora_wide(int M, int K, int N, int R);
 int lora_wide_k_slices(int M, int K, int R);
 void launch_lora_wide(const LoraArgs& g, bool bf16, hipStream_t s);
 

@@ -15,12 +15,6 @@ namespace wq {
 
 namespace {
 
-#ifndef OCC
-#define OCC 3
-#define PERMAX 8
-#define PERWG 1024
-#define KSWG 256
-#endif
 constexpr int DOWN_WAVES = 8;
 constexpr int UP_WAVES = 4;
 // a wave's lanes exchange values through LDS that no other wave touches: the
@@ -139,7 +133,7 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void lora_wide_down_kernel(LoraArg
 // slot p ^ (n / 8) of its row (of CP slots): 8 lanes of a read, rows 8 apart,
 // fall on different banks.  RC: chunks of 32 ranks.
 template <bool BF16, int RC>
-__global__ __launch_bounds__(64 * UP_WAVES, RC <= 2 ? OCC : 1) void lora_wide_up_kernel(LoraArgs g, int per, int ranges) {
+__global__ __launch_bounds__(64 * UP_WAVES, RC <= 2 ? 3 : 1) void lora_wide_up_kernel(LoraArgs g, int per, int ranges) {
     constexpr int CP = 4 * RC;                    // slots of a B row
     constexpr int STAGE = 128 * CP / (64 * UP_WAVES);  // pieces a thread moves per step
     constexpr int BUF = 128 * CP;
@@ -283,7 +277,7 @@ template <bool BF16, int RC>
 void launch_up(const LoraArgs& g, hipStream_t s) {
     const int tiles = (g.M + 63) / 64;
     const int blocks = (g.N + 127) / 128;
-    const int per = (int)std::max<int64_t>(1, std::min<int64_t>(PERMAX, (int64_t)blocks * tiles / PERWG));
+    const int per = (int)std::max<int64_t>(1, std::min<int64_t>(8, (int64_t)blocks * tiles / 1024));
     const int ranges = (blocks + per - 1) / per;
     const int side = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(64, g.adapters), 1024 / ((int64_t)tiles * ranges)));
     hipLaunchKernelGGL((lora_wide_up_kernel<BF16, RC>), dim3((unsigned)(tiles * ranges), side), dim3(64 * UP_WAVES), 0,
@@ -306,12 +300,20 @@ void launch_t(const LoraArgs& g, hipStream_t s) {
 
 }  // namespace
 
-bool lora_wide(int M, int R) { return M > 512 && R <= 128; }
+// Large batches by the elements of x and y that pass: through LDS the loads are
+// whole cache lines, at the price of a longer chain.  us here / in lora.hip, 8
+// adapters: rank 16, 4096 x 4096: 2048 rows 28.7 / 26.1, 4096 rows 36.1 / 40.5;
+// rank 16, 7168 x 20480: 1024 rows 36.7 / 41.4; rank 64, 5120 x 1536: 256 rows 19.5 /
+// 18.7, 512 rows 22.3 / 27.6; rank 64, 7168 x 20480: 100 rows 30.1 / 24.2, 256 rows
+// 26.3 / 33.7.
+bool lora_wide(int M, int K, int N, int R) {
+    return M >= 256 && R <= 128 && (int64_t)M * (K + 2 * (int64_t)N) > (R > 32 ? 3 << 20 : 32 << 20);
+}
 
 int lora_wide_k_slices(int M, int K, int R) {
     const int ranks = 16 * rank_tiles(R);
     const int wgs = (M + 16 * TS - 1) / (16 * TS) * ((R + ranks - 1) / ranks);
-    return std::max(1, std::min(std::min(LORA_MAX_SLICES, KSWG / std::max(1, wgs)), K / LORA_STEP / DOWN_WAVES));
+    return std::max(1, std::min(std::min(LORA_MAX_SLICES, 256 / std::max(1, wgs)), K / LORA_STEP / DOWN_WAVES));
 }
 
 void launch_lora_wide(const LoraArgs& g, bool bf16, hipStream_t s) {
