@@ -62,14 +62,13 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(LoraArgs g) {
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) load_x(d, d);
     }
-    const TileIds ids = tile_ids<16 * TS>(g, tile, lane);
+    const int ids = tile_ids<16 * TS>(g, tile, lane);
 
     bool first = true;
-    uint64_t left = ids.first;
-    for (int j = 0; left; ++j, left &= left - 1) {
+    uint64_t left = __ballot(ids >= 0), mine;
+    for (int j = 0; left; ++j) {
+        const int a = next_adapter(ids, left, mine);
         if (j % (int)gridDim.y != (int)blockIdx.y) continue;
-        const int a = __builtin_amdgcn_readlane(ids.id, __builtin_ctzll(left));
-        const uint64_t mine = __ballot(ids.id == a);
         const uint16_t* ar[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -184,14 +183,13 @@ __global__ __launch_bounds__(64 * UP_WAVES, RG == 1 ? 3 : 2) void lora_up_kernel
         if (gr == 0) back[tok] = f;
     }
 
-    const TileIds ids = tile_ids<TOKENS>(g, tile, lane);
+    const int ids = tile_ids<TOKENS>(g, tile, lane);
     __syncthreads();
 
-    uint64_t left = ids.first;
-    for (int j = 0; left; ++j, left &= left - 1) {
+    uint64_t left = __ballot(ids >= 0), mine;
+    for (int j = 0; left; ++j) {
+        const int a = next_adapter(ids, left, mine);
         if (j % (int)gridDim.z != (int)blockIdx.z) continue;
-        const int a = __builtin_amdgcn_readlane(ids.id, __builtin_ctzll(left));
-        const uint64_t mine = __ballot(ids.id == a);
         const uint16_t* bw = g.b + (size_t)a * g.N * g.R;
 
         u32x4 bv[RC][4];

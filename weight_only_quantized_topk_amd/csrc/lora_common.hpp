@@ -12,23 +12,20 @@ namespace wq {
 // lane-wise condition would run all the same)
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
 
-// The adapters of a tile of up to 64 tokens: lane i holds token i's (-1: none,
-// an id out of range counts as none), first marks each one's first token
-struct TileIds {
-    int id;
-    uint64_t first;
-};
+// The adapters of a tile of up to 64 tokens: lane i holds token i's (-1: none, an
+// id out of range counts as none).  A pass takes the adapter of the first token
+// that is left and all tokens that share it (`mine`).
 template <int TOKENS>
-__device__ __forceinline__ TileIds tile_ids(const LoraArgs& g, int tile, int lane) {
-    TileIds t;
+__device__ __forceinline__ int tile_ids(const LoraArgs& g, int tile, int lane) {
     const int m = tile * TOKENS + lane;
-    t.id = (lane < TOKENS && m < g.M) ? g.ids[m] : -1;
-    if (t.id < 0 || t.id >= g.adapters) t.id = -1;
-    bool seen = t.id < 0;
-#pragma unroll
-    for (int i = 0; i < TOKENS; ++i) seen = seen || (i < lane && __builtin_amdgcn_readlane(t.id, i) == t.id);
-    t.first = __ballot(!seen);
-    return t;
+    const int id = lane < TOKENS && m < g.M ? g.ids[m] : -1;
+    return id < g.adapters ? max(id, -1) : -1;
+}
+__device__ __forceinline__ int next_adapter(int ids, uint64_t& left, uint64_t& mine) {
+    const int a = __builtin_amdgcn_readlane(ids, __builtin_ctzll(left));
+    mine = __ballot(ids == a);
+    left &= ~mine;
+    return a;
 }
 
 // One token's t by 8 threads (neighbouring lanes, gr = 0 .. 7, ranks 64 w + 8

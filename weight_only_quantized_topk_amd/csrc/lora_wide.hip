@@ -48,12 +48,11 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void lora_wide_down_kernel(LoraArg
     const int s0 = (int)((int64_t)slice * steps / g.ks) + wave, s1 = (int)((int64_t)(slice + 1) * steps / g.ks);
     const int lrow = lane >> 3, piece = lane & 7;
 
-    const TileIds ids = tile_ids<16 * TS>(g, tile, lane);
-    uint64_t left = ids.first;
-    for (int j = 0; left; ++j, left &= left - 1) {
+    const int ids = tile_ids<16 * TS>(g, tile, lane);
+    uint64_t left = __ballot(ids >= 0), mine;
+    for (int j = 0; left; ++j) {
+        const int a = next_adapter(ids, left, mine);
         if (j % (int)gridDim.y != (int)blockIdx.y) continue;
-        const int a = __builtin_amdgcn_readlane(ids.id, __builtin_ctzll(left));
-        const uint64_t mine = __ballot(ids.id == a);
         const uint16_t* row[LOADS];  // rows past M or R: the last one (their results are dropped)
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
@@ -161,7 +160,7 @@ __global__ __launch_bounds__(64 * UP_WAVES, RC <= 2 ? 3 : 1) void lora_wide_up_k
             });
         if (gr == 0) back[tok] = f;
     }
-    const TileIds ids = tile_ids<64>(g, tile, lane);
+    const int ids = tile_ids<64>(g, tile, lane);
     __syncthreads();
     u32x4 thi[RC], tlo[RC];
 #pragma unroll
@@ -186,11 +185,10 @@ __global__ __launch_bounds__(64 * UP_WAVES, RC <= 2 ? 3 : 1) void lora_wide_up_k
         slot[i] = n < 128 ? n * CP + ((p - n * pieces) ^ ((n >> 3) & SWZ)) : -1;
     }
 
-    uint64_t left = ids.first;
-    for (int j = 0; left; ++j, left &= left - 1) {
+    uint64_t left = __ballot(ids >= 0), mine;
+    for (int j = 0; left; ++j) {
+        const int a = next_adapter(ids, left, mine);
         if (j % (int)gridDim.y != (int)blockIdx.y) continue;
-        const int a = __builtin_amdgcn_readlane(ids.id, __builtin_ctzll(left));
-        const uint64_t mine = __ballot(ids.id == a);
         const uint32_t mw = (uint32_t)(mine >> (16 * wave)) & 0xFFFFu;  // of this wave's tokens
         const uint16_t* bw = g.b + (size_t)a * g.N * g.R;
 
@@ -264,7 +262,7 @@ void launch_down(const LoraArgs& g, hipStream_t s) {
     const int tiles = (g.M + 16 * TS - 1) / (16 * TS);
     const int groups = (g.R + 16 * RT - 1) / (16 * RT);
     const int wgs = tiles * g.ks * groups;
-    const int side = std::max(1, std::min(std::min(16 * TS, g.adapters), 512 / wgs));
+    const int side = std::max(1, std::min(std::min(16 * TS, g.adapters), 256 / wgs));
     const size_t lds = sizeof(u32x4) * 8 * 16 * (TS + RT) * DOWN_WAVES;
     static_assert(16 * (TS + RT) * 8 >= TS * RT * 64, "the waves' sums fit where the operands were");
     if (lds > 65536)
