@@ -15,6 +15,10 @@
 // to at most 1 per token (fp16 has the range then) and split in two 16-bit
 // parts, hi + lo, which are both multiplied by the B rows (one register load of
 // 32 ranks serves two matrix instructions).
+//
+// Bound by the chain of dependent loads (ids, weights, t, y), not by bytes: 8
+// rows of 8 adapters, rank 16, 4096 x 4096 bf16, 4.5 + 4.9 us for 2.3 MB; 203 rows,
+// rank 24, 5120 x 1544 fp16, 8.8 + 4.3 us.  Large batches: lora_wide.hip.
 #include "lora_common.hpp"
 
 #include <algorithm>

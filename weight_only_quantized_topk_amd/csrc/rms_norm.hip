@@ -9,8 +9,12 @@
 // Everything between the loads and the stores is float32: s is not rounded
 // before it is squared, y is not rounded before it is quantised.  A row is
 // read once: its values stay in registers between the sum of squares, the
-// maximum and the store.  HBM bound for many rows, launch and reduction
-// latency for one.
+// maximum and the store, a wave per row up to 1024 values, else a workgroup of
+// as many threads as keep 8 or 16 values each (16 bytes an access).  HBM bound
+// for many rows: 8192 x 5120 bf16 with residual, 16-bit and coded outputs moves
+// 378 MB in 73.2 us, 5.16 TB/s, what a large copy reaches.  One row of 4096: 3.9
+// us, the latency of two loads and two reductions; 333 rows of 1001 (single
+// 2-byte accesses) 4.7 us.
 #include "common.hpp"
 #include "launch.hpp"
 
