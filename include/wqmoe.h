@@ -468,8 +468,9 @@ wq_status dense_w8a16_gemm(const void* d_x, int M, int K, int N, const void* d_w
  *     are padded with zeros in both; d_scales device float [adapters], NULL for ones
  *   d_workspace: dense_lora_workspace_bytes() bytes (every value read from it
  *     is written first, by the same call)
- * Limits: K, N, R multiples of 8; M, N <= 2^24, R <= 256, N * R <
- * 2^31, y's row stride <= 2^25.  y must not overlap any input or the workspace.  Calls sharing a workspace must be stream-ordered.
+ * Limits: K, N, R multiples of 8; M, K, N <= 2^24, R <= 256,
+ * N * R < 2^31, y's row stride <= 2^25.  y must not overlap any input or the
+ * workspace.  Calls sharing a workspace must be stream-ordered.
  */
 size_t dense_lora_workspace_bytes(int M, int K, int N, int R, int adapters);
 wq_status dense_lora_gemm(const void* d_x, int64_t x_stride, int M, int K, int N, int R, int adapters,

@@ -222,6 +222,7 @@ def lora_args(**k):
 @pytest.mark.parametrize("change,want", [
     (dict(dt=2), INV), (dict(M=-1), INV), (dict(K=0), INV), (dict(N=-8), INV), (dict(R=0), INV), (dict(L=0), INV),
     (dict(K=508), UNS), (dict(N=252), UNS), (dict(R=12), UNS), (dict(R=264), UNS), (dict(M=(1 << 24) + 1), UNS),
+    (dict(K=(1 << 24) + 8, xs=(1 << 24) + 8), UNS), (dict(ys=(1 << 25) + 8), UNS),
     (dict(xs=504), INV), (dict(ys=0), INV), (dict(xs=516), UNS), (dict(ys=260), UNS), (dict(wsb=64), INV),
     (dict(x=None), INV), (dict(ids=None), INV), (dict(a=None), INV), (dict(b=at(2)), INV), (dict(s=at(4)), INV),
     (dict(y=None), INV), (dict(ws=None), INV),
@@ -260,6 +261,25 @@ def test_lora_binding_refusals():
     for change in (dict(y=y.half()), dict(a=a.half()), dict(adapter_ids=ids.long()), dict(scales=s.to(bf))):
         with pytest.raises(TypeError):
             wq.dense_lora_gemm(**{**good, **change})
+
+
+def test_dense_refuses_bad_adapters_before_it_launches():
+    """The binding's checks of the adapters come before the projection: the error is theirs, not the device's."""
+    bf = torch.bfloat16
+    x, w, s = torch.zeros((4, 512), dtype=bf), torch.zeros(512 * 256, dtype=torch.uint8), torch.zeros(256, dtype=bf)
+    ids = torch.zeros(4, dtype=torch.int32)
+    a, b = torch.zeros((3, 16, 512), dtype=bf), torch.zeros((3, 256, 16), dtype=bf)
+    for bad, err in ((wq.Lora(ids[:3], a, b, None), ValueError), (wq.Lora(ids, a, b[:, :128], None), ValueError),
+                     (wq.Lora(ids.long(), a, b, None), TypeError), (wq.Lora(ids, a.half(), b.half(), None), TypeError),
+                     (wq.Lora(ids, a[:, :12], b[:, :, :12], None), ValueError),
+                     (wq.Lora(ids, a[:, :4].contiguous(), b[:, :, :4].contiguous(), None), ValueError)):
+        with pytest.raises(err):
+            wq.dense_w8a16_gemm(x, 256, w, s, lora=bad)
+    good = wq.Lora(ids, a, b, None)
+    with pytest.raises(ValueError):
+        wq.dense_w8a16_gemm(x, 256, w, s, out=torch.zeros((4, 512), dtype=bf)[:, :256], lora=good)
+    with pytest.raises(ValueError):
+        wq.dense_w8a16_gemm(x, 256, w, s, out=torch.zeros((4, 128), dtype=bf), lora=good)
 
 
 def test_pack_lora():

@@ -1110,7 +1110,7 @@ wq_status dense_w8a16_gemm(const void* d_x, int M, int K, int N, const void* d_w
 // ---------------------------------------------------------------------------
 static const char* lora_sizes(int M, int K, int N, int R, int adapters) {
     if (M < 0 || K <= 0 || N <= 0 || R <= 0 || adapters <= 0) return "sizes must be positive (M >= 0)";
-    if (M > MAX_PAIRS || N > (1 << 24) || R > 256) return "M or N > 2^24, or rank > 256";
+    if (M > MAX_PAIRS || K > (1 << 24) || N > (1 << 24) || R > 256) return "M, K or N > 2^24, or rank > 256";
     if (K % 8 || N % 8 || R % 8) return "K, N and the rank must be multiples of 8";
     return nullptr;
 }

@@ -13,7 +13,8 @@ from typing import NamedTuple, Optional, Tuple
 import numpy as np
 
 from . import _lib
-from ._lib import (WQ_BF16, WQ_F16, WQ_F32, WQ_GROUP_MAX, WQ_GROUP_TOP2, WQ_SCORE_SIGMOID, WQ_SCORE_SOFTMAX, WQ_PACK_INTERLEAVE_GATE_UP, WQ_STAGE_DOWN, WQ_STAGE_GATE_UP, WQ_STAGE_RAW,
+from ._lib import (WQ_BF16, WQ_F16, WQ_F32, WQ_GROUP_MAX, WQ_GROUP_TOP2, WQ_PACK_INTERLEAVE_GATE_UP,
+                   WQ_SCORE_SIGMOID, WQ_SCORE_SOFTMAX, WQ_STAGE_DOWN, WQ_STAGE_GATE_UP, WQ_STAGE_RAW,
                    WqMoeGemmDesc, check, load)
 
 __all__ = [
@@ -499,8 +500,8 @@ def pack_lora(adapters, act, device="cuda"):
     a = torch.zeros((len(adapters), R, K), dtype=act)
     b = torch.zeros((len(adapters), N, R), dtype=act)
     for i, (A, B, _) in enumerate(adapters):
-        a[i, :A.shape[0]] = A
-        b[i, :, :B.shape[1]] = B
+        a[i, :A.shape[0]] = A.detach()
+        b[i, :, :B.shape[1]] = B.detach()
     scales = torch.tensor([float(s) for _, _, s in adapters], dtype=torch.float32)
     return a.to(device), b.to(device), scales.to(device)
 
@@ -509,14 +510,10 @@ def dense_lora_workspace_bytes(M: int, K: int, N: int, R: int, adapters: int) ->
     return int(load().dense_lora_workspace_bytes(M, K, N, R, adapters))
 
 
-def dense_lora_gemm(x, adapter_ids, a, b, scales, y, workspace=None, stream=None):
-    """Adds the rows' own adapters to y in place: y[m] += scales[i] * (x[m] a[i]^T)
-    b[i]^T with i = adapter_ids[m] (rows with an id outside [0, adapters) stay as
-    they are).  x [M, K], y [M, N] bf16/fp16 (device; rows may be strided), a
-    [adapters, rank, K] and b [adapters, N, rank] in their type, scales
-    [adapters] float32 or None for ones.  Returns y."""
+def _lora_sizes(x, adapter_ids, a, b, scales, y):
+    """Checks the arguments of dense_lora_gemm -> (M, K, N, R, adapters, workspace bytes)."""
     torch = _torch()
-    dt = act_code(x.dtype)
+    act_code(x.dtype)
     if x.dim() != 2 or y.dim() != 2 or a.dim() != 3:
         raise ValueError("x must be [M, K], y [M, N], a [adapters, rank, K], got %s, %s, %s"
                          % (list(x.shape), list(y.shape), list(a.shape)))
@@ -530,14 +527,28 @@ def dense_lora_gemm(x, adapter_ids, a, b, scales, y, workspace=None, stream=None
     _check(adapter_ids, "adapter_ids", (M,), (torch.int32,), dev)
     if scales is not None:
         _check(scales, "scales", (L,), (torch.float32,), dev)
+    nbytes = dense_lora_workspace_bytes(M, K, N, R, L)
+    if M and not nbytes:
+        raise ValueError("unsupported adapters: M %d K %d N %d rank %d (multiples of 8, rank at most 256)" % (M, K, N, R))
+    return M, K, N, R, L, nbytes
+
+
+def dense_lora_gemm(x, adapter_ids, a, b, scales, y, workspace=None, stream=None):
+    """Adds the rows' own adapters to y in place: y[m] += scales[i] * (x[m] a[i]^T)
+    b[i]^T with i = adapter_ids[m] (rows with an id outside [0, adapters) stay as
+    they are).  x [M, K], y [M, N] bf16/fp16 (device; rows may be strided), a
+    [adapters, rank, K] and b [adapters, N, rank] in their type, scales
+    [adapters] float32 or None for ones.  Returns y."""
+    torch = _torch()
+    M, K, N, R, L, nbytes = _lora_sizes(x, adapter_ids, a, b, scales, y)
     new = []
     if workspace is None:
-        workspace = torch.empty(dense_lora_workspace_bytes(M, K, N, R, L), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
         new.append(workspace)
-    elif not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError("workspace must be contiguous on %s" % dev)
+    elif not workspace.is_contiguous() or workspace.device != x.device:
+        raise ValueError("workspace must be contiguous on %s" % x.device)
     check(load().dense_lora_gemm(_ptr(x), _row_stride(x), M, K, N, R, L, _ptr(adapter_ids), _ptr(a), _ptr(b),
-                                 _ptr(scales), _ptr(y), _row_stride(y), dt, _ptr(workspace),
+                                 _ptr(scales), _ptr(y), _row_stride(y), act_code(x.dtype), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _stream(stream)), "dense_lora_gemm")
     _keep_for(stream, *new)
     return y
@@ -548,13 +559,19 @@ def _dense(fn, x, N, w_packed, scales, extra, out, workspace, stream, act_order,
     M, K = x.shape
     if out is None:
         out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+    if lora is not None:  # before anything is launched
+        if not (x.is_contiguous() and out.is_contiguous()):
+            raise ValueError("x and out must be contiguous")
+        if out.shape != (M, N):
+            raise ValueError("out must be %s, got %s" % ([M, N], list(out.shape)))
+        _lora_sizes(x, *lora, out)
     if workspace is None:
         nb = dense_gemm_workspace_bytes(M, K, N, act_order)
         workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=x.device)
     check(fn(_ptr(x), M, K, N, _ptr(w_packed), _ptr(scales), *extra, _ptr(out), act_code(x.dtype), _ptr(workspace),
              workspace.numel(), _stream(stream)), fn.__name__)
     if lora is not None:
-        dense_lora_gemm(x, lora.adapter_ids, lora.a, lora.b, lora.scales, out, stream=stream)
+        dense_lora_gemm(x, *lora, out, stream=stream)
     return out
 
 
