@@ -74,12 +74,12 @@ def check(x, r, w, kind, quant, want_out=True, what="", eps=EPS, scale=0.03, **k
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
 @pytest.mark.parametrize("quant", [None, "row", "static"])
-@pytest.mark.parametrize("n", [1, 2, 7, 8, 64, 250, 512, 520, 1001, 1024, 1032, 2048, 2049, 4096, 4104, 7168, 8192,
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 64, 250, 512, 520, 1001, 1024, 1032, 2048, 2049, 4096, 4104, 5120, 7168, 8192,
                                8200, 9001, 16384, 16392, 40000])
 def test_widths(n, quant, kind):
     """Every width class (a wave, a workgroup, several vectors a thread, the long rows), aligned and not."""
     need_gpu()
-    for rows in (1, 5, 67):
+    for rows in (1, 5, 67) + ((300,) if n in (520, 1024, 4104, 5120, 8192) else ()):
         say("rms_norm", rows, n, quant, kind)
         check(*inputs(rows, n, DT[kind], n + rows), kind, quant, what="%d x %d" % (rows, n))
 

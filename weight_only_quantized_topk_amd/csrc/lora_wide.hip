@@ -142,7 +142,7 @@ __global__ __launch_bounds__(64 * UP_WAVES, RC <= 2 ? 3 : 1) void lora_wide_up_k
     constexpr int BUF = 128 * CP;
     constexpr int SWZ = CP < 8 ? CP - 1 : 7;
     __shared__ u32x4 buf[2 * BUF];
-    __shared__ float back[64];
+    __shared__ __attribute__((aligned(16))) float back[64];
     const int lane = threadIdx.x & 63;
     const int wave = wave_index();
     const int col = lane & 15, q = lane >> 4;
@@ -279,6 +279,8 @@ template <bool BF16, int RC>
 void launch_up(const LoraArgs& g, hipStream_t s) {
     const int tiles = (g.M + 63) / 64;
     const int blocks = (g.N + 127) / 128;
+    // steps of 128 outputs a workgroup takes, while 1024 workgroups are left: at most 8
+    // (4096 rows, rank 64, 7168 x 20480, both products: 16 146 us, 8 128, 4 128, 2 143)
     const int per = (int)std::max<int64_t>(1, std::min<int64_t>(8, (int64_t)blocks * tiles / 1024));
     const int ranges = (blocks + per - 1) / per;
     const int side = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(64, g.adapters), 1024 / ((int64_t)tiles * ranges)));
@@ -312,6 +314,8 @@ bool lora_wide(int M, int K, int N, int R) {
     return M >= 256 && R <= 128 && (int64_t)M * (K + 2 * (int64_t)N) > (R > 32 ? 3 << 20 : 32 << 20);
 }
 
+// K slices of the first product: a workgroup per CU (two measured the same, with
+// twice the slices to add up), a step at least for each wave
 int lora_wide_k_slices(int M, int K, int R) {
     const int ranks = 16 * rank_tiles(R);
     const int wgs = (M + 16 * TS - 1) / (16 * TS) * ((R + ranks - 1) / ranks);

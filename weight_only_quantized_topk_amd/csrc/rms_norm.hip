@@ -9,10 +9,9 @@
 // Everything between the loads and the stores is float32: s is not rounded
 // before it is squared, y is not rounded before it is quantised.  A row is
 // read once: its values stay in registers between the sum of squares, the
-// maximum and the store, a wave per row up to 1024 values, else a workgroup of
-// as many threads as keep 8 or 16 values each (16 bytes an access).  HBM bound
-// for many rows: 8192 x 5120 bf16 with residual, 16-bit and coded outputs moves
-// 378 MB in 73.2 us, 5.16 TB/s, what a large copy reaches.  One row of 4096: 3.9
+// maximum and the store, a wave or a workgroup per row, of as many threads
+// as keep 8 or 16 values each (16 bytes an access).  HBM bound for many rows: 8192 x 5120 bf16 with residual, 16-bit and coded outputs moves
+// 378 MB in 73.2 us, 5.16 TB/s, what a large copy reaches.  One row of 4096: 3.3
 // us, the latency of two loads and two reductions; 333 rows of 1001 (single
 // 2-byte accesses) 4.7 us.
 #include "common.hpp"
@@ -304,12 +303,21 @@ template <bool BF16>
 void launch_t(const RmsNormArgs& g, hipStream_t s) {
     const bool vec = g.n % 8 == 0 && g.x_stride % 8 == 0 && (!g.r || g.r_stride % 8 == 0) &&
                      (!g.r_out || g.ro_stride % 8 == 0) && (!g.out || g.out_stride % 8 == 0);
+    // Threads per row: one 16-byte access each is the shortest chain; up to a row
+    // per CU that decides, beyond it fewer threads per row keep more rows under way.
+    // us at 64 rows / 8192 rows (residual, 16-bit and coded outputs): n = 1024 by 256
+    // threads 3.4 / 16.9, by 64 of two accesses 4.0 / 14.0; n = 4096 by 512 3.7 / 56.7,
+    // by 256 of two 4.3 / 56.4; n = 5120 by 1024 4.0 / 82.7, by 512 of two 4.3 / 75.8, by
+    // 256 of four 5.2 / 77.9; n = 16384 by 1024 of two 5.8 / 114 (4096 rows), by 512 of
+    // four 6.8 / 121.
+    const bool few = g.rows <= 256;
     if (vec) {
         if (g.n <= 512) return launch_cfg<BF16, 8, 64, 1>(g, s);
-        if (g.n <= 1024) return launch_cfg<BF16, 8, 64, 2>(g, s);
+        if (g.n <= 1024 && !few) return launch_cfg<BF16, 8, 64, 2>(g, s);
         if (g.n <= 2048) return launch_cfg<BF16, 8, 256, 1>(g, s);
-        if (g.n <= 4096) return launch_cfg<BF16, 8, 256, 2>(g, s);
-        if (g.n <= 8192) return launch_cfg<BF16, 8, 512, 2>(g, s);
+        if (g.n <= 4096) return launch_cfg<BF16, 8, 512, 1>(g, s);
+        if (g.n <= 8192 && !few) return launch_cfg<BF16, 8, 512, 2>(g, s);
+        if (g.n <= 8192) return launch_cfg<BF16, 8, 1024, 1>(g, s);
         if (g.n <= 16384) return launch_cfg<BF16, 8, 1024, 2>(g, s);
     } else {
         if (g.n <= 512) return launch_cfg<BF16, 1, 64, 8>(g, s);
