@@ -82,7 +82,7 @@ def test_equals_the_quantising_call(M, bs):
             assert not bool(got[pad].any())
 
 
-@pytest.mark.parametrize("M,N", [(300, 256), (4300, 256), (2200, 512), (50001, 256)])
+@pytest.mark.parametrize("M,N", [(300, 256), (4300, 256), (2200, 512), (9001, 256), (2200, 1280), (50001, 256)])
 def test_large_batch_shapes_equal_the_quantising_call(M, N):
     """Each tile shape of the 128-row blocks (by the number of tiles), with one power-of-two scale a row."""
     need_gpu()
@@ -107,6 +107,44 @@ def test_large_batch_shapes_equal_the_quantising_call(M, N):
     wq.moe_fp8_w8a8_gemm(wq.WQ_STAGE_GATE_UP, (value * 0.125).bfloat16(), *common, None, ref, work, 0.125, 0.5)
     torch.cuda.synchronize()
     assert bool(got.any()) and torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("bs", [128, 256])
+@pytest.mark.parametrize("stage", [wq.WQ_STAGE_GATE_UP, wq.WQ_STAGE_RAW])
+def test_tiles_by_xcd_under_uneven_routing(stage, bs):
+    """The ordered 64-row tiles: an expert with nearly all rows, one with one, one with none, blocks of several tiles,
+    a buffer larger than needed, an odd number of K steps."""
+    need_gpu()
+    M, N, E, K, topk = 1500, 1280, 4, 384, 2
+    g = torch.Generator().manual_seed(bs)
+    w = torch.randint(0, 256, (E, 2 * N, K), generator=g, dtype=torch.uint8).numpy()
+    w[(w & 0x7F) >= 0x60] &= 0x8F
+    wp, sp = wq.pack_fp8(w, np.full((E, 2 * N), 2.0 ** -6, np.float32), interleave_gate_up=stage == wq.WQ_STAGE_GATE_UP)
+    wp, sp = torch.from_numpy(wp).cuda(), torch.from_numpy(sp).cuda()
+    codes = torch.randint(0, 256, (M, K), generator=g, dtype=torch.uint8)
+    codes[(codes & 0x7F) >= 0x70] &= 0x8F
+    value = torch.from_numpy(e4m3_values(codes.numpy())).cuda()
+    codes = codes.cuda()
+    ids = torch.tensor([2, 0], dtype=torch.int32).repeat(M, 1)
+    ids[700, 1] = 3
+    ids = ids.cuda()
+    cap = wq.moe_align_capacity(M, topk, E, bs) + 5 * bs
+    st, ex, nt = wq.moe_align(ids, E, bs, cap)
+    say("by xcd", stage, bs, cap)
+    if stage == wq.WQ_STAGE_GATE_UP:
+        got, ref = torch.full((2, cap, N), 0x55, dtype=torch.uint8, device="cuda")
+    else:
+        got, ref = torch.full((2, M * topk, 2 * N), 7.0, device="cuda")
+    common = (M, topk, E, 2 * N, K, wp, sp, st, ex, nt, cap, bs)
+    wq.moe_fp8_codes_gemm(stage, codes, None, *common, got, in_scale=0.125, out_scale=0.5)
+    work = torch.empty(wq.moe_fp8_gemm_workspace_bytes(stage, M, topk, E, 2 * N, K), dtype=torch.uint8, device="cuda")
+    wq.moe_fp8_w8a8_gemm(stage, (value * 0.125).bfloat16(), *common, None, ref, work, 0.125, 0.5)
+    torch.cuda.synchronize()
+    used = int(nt)
+    if stage == wq.WQ_STAGE_GATE_UP:
+        assert torch.equal(got[:used], ref[:used]) and bool((got[used:] == 0x55).all())
+    else:
+        assert torch.equal(got, ref)
 
 
 @pytest.mark.parametrize("bs", [16, 128])

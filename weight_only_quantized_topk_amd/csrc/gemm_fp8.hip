@@ -388,7 +388,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t fp8_rsrc(const void* base) {
 __device__ __forceinline__ int fp8_lds_off(int row, int ch) { return row * FP8_ROWB + ((ch ^ ((row >> 1) & 7)) << 4); }
 __device__ __forceinline__ int fp8_slot(int piece) { return (piece >> 1) + 4 * (piece & 1); }
 
-template <int STAGE, int NW, int RT, int BM, int OCC, bool CODES = false>
+// XCD: the workgroups of one XCD (linear number modulo 8) take neighbouring tiles,
+// the token tiles of a weight tile first, so that its weights are read into one L2.
+template <int STAGE, int NW, int RT, int BM, int OCC, bool CODES = false, bool XCD = false>
 __global__ __launch_bounds__(NW * 64, OCC) void fp8_prefill_kernel(Fp8GemmArgs g) {
     constexpr int NT = NW * 64;
     constexpr int BN = NW * RT * 16;
@@ -399,8 +401,16 @@ __global__ __launch_bounds__(NW * 64, OCC) void fp8_prefill_kernel(Fp8GemmArgs g
     __shared__ __attribute__((aligned(16))) uint8_t lds[2 * BUF];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int ntile = blockIdx.x, mtile = blockIdx.y;
+    int ntile = blockIdx.x, mtile = blockIdx.y;
     const int T = g.M * g.topk;
+    if constexpr (XCD) {
+        const int mt = min((*g.ntpp + BM - 1) / BM, (int)gridDim.y);
+        const int64_t total = (int64_t)mt * gridDim.x, l = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+        if (l >= total) return;
+        const int64_t q = (l & 7) * (total >> 3) + min(l & 7, total & 7) + (l >> 3);
+        ntile = (int)(q / mt);
+        mtile = (int)(q - (int64_t)ntile * mt);
+    }
     const int row0 = mtile * BM;
     if (row0 >= *g.ntpp) return;
     const int e = g.expert_ids[row0 / g.block_size];
@@ -571,10 +581,10 @@ __global__ __launch_bounds__(NW * 64, OCC) void fp8_prefill_kernel(Fp8GemmArgs g
     }
 }
 
-template <int STAGE, int NW, int RT, int BM, int OCC, bool CODES = false>
+template <int STAGE, int NW, int RT, int BM, int OCC, bool CODES = false, bool XCD = false>
 static void launch_fp8_prefill_cfg(const Fp8GemmArgs& g, int ksplit, hipStream_t s) {
     const dim3 grid(g.n_out / (NW * RT * 16), g.cap / BM, ksplit);
-    hipLaunchKernelGGL((fp8_prefill_kernel<STAGE, NW, RT, BM, OCC, CODES>), grid, dim3(NW * 64), 0, s, g);
+    hipLaunchKernelGGL((fp8_prefill_kernel<STAGE, NW, RT, BM, OCC, CODES, XCD>), grid, dim3(NW * 64), 0, s, g);
 }
 
 // shapes (weight rows x token rows, waves, workgroups per CU):
@@ -622,6 +632,12 @@ int fp8_down_split(int T, int E, int n_out, int k_in, int block_size) {
 // tiles of 512 rows, 8 experts, K = 4096: 56 tiles 68 / 43 / 37, 84 tiles 76 /
 // 49 / 52, 476 tiles 203 / 177 / 182, 560 tiles 208 / 189 / 203, 1120 tiles 336 /
 // 367 / 409, 3808 tiles 1070 / 1252 / 1376.
+// Between them, where the 256 x 128 tiles are more than a round of the CUs (one
+// workgroup each) and the experts have more than half a block of rows, 256 x 64 with
+// two workgroups per CU and the tiles ordered by XCD.  us, 256 x 128 / 256 x 64: 84
+// tiles 48 / 54; 140 tiles 80 / 65, 252 tiles 107 / 94, 440 tiles of 64 experts (K =
+// 2048, 96 rows each) 117 / 97, 476 tiles 173 / 172; 448 tiles with 64 rows an expert
+// 212 / 226; 140 tiles unordered: 93.
 template <int STAGE>
 static void launch_fp8_prefill_codes(const Fp8GemmArgs& g, hipStream_t s) {
     if (g.block_size == 64) {
@@ -632,6 +648,7 @@ static void launch_fp8_prefill_codes(const Fp8GemmArgs& g, hipStream_t s) {
     const long T = (long)g.M * g.topk;
     const long tiles = (T + std::min<long>(T, g.E) * 64 + 127) / 128 * g.n_out / 512;  // as fp8_down_split counts
     if (g.n_out % 512 == 0 && tiles > 768) launch_fp8_prefill_cfg<STAGE, 8, 4, 128, 1, true>(g, 1, s);
+    else if (g.n_out % 256 == 0 && tiles > 128 && T > 64L * g.E) launch_fp8_prefill_cfg<STAGE, 8, 2, 64, 2, true, true>(g, 1, s);
     else if (g.n_out % 256 == 0 && tiles > 64) launch_fp8_prefill_cfg<STAGE, 8, 2, 128, 1, true>(g, 1, s);
     else launch_fp8_prefill_cfg<STAGE, 4, 2, 128, 2, true>(g, 1, s);
 }
