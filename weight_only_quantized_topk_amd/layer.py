@@ -229,13 +229,20 @@ class MoERunner:
                 "capacity": self.cap}
 
 
+def _result(r, out, stream, keep):
+    """What a call on a runner of its own returns: out, and its other buffers if kept."""
+    import torch
+    aux = r.aux() if keep else {}
+    ops._keep_for(stream, out, *(t for t in aux.values() if isinstance(t, torch.Tensor)))
+    return (out, aux) if keep else out
+
+
 def fused_moe(x, logits, p: PackedMoE, topk: int, renormalize: bool = True, block_size: Optional[int] = None,
               stream=None, keep=False, router: Optional[Router] = None):
     """x [M, K] act, logits [M, E] float32 -> out [M, K] act.  With keep=True also
     returns a dict of the intermediate device buffers."""
-    r = MoERunner(p, x.shape[0], topk, renormalize, block_size, device=x.device, router=router)
-    out = r(x, logits, stream=stream)
-    return (out, r.aux()) if keep else out
+    r = ops._alloc(stream, MoERunner, p, x.shape[0], topk, renormalize, block_size, device=x.device, router=router)
+    return _result(r, r(x, logits, stream=stream), stream, keep)
 
 
 # ----------------------------------------------------------------------------
@@ -333,6 +340,6 @@ def fused_moe_fp8(x, logits, p: PackedFp8MoE, topk: int, renormalize: bool = Tru
                   block_size: Optional[int] = None, stream=None, keep=False, router: Optional[Router] = None):
     """x [M, K] act, or (codes, row scales or None) -> out [M, K] act with logits [M, E] float32 (FP8 W8A8 experts)."""
     first = x[0] if isinstance(x, tuple) else x
-    r = Fp8MoERunner(p, first.shape[0], topk, renormalize, block_size, device=first.device, router=router)
-    out = r(x, logits, stream=stream)
-    return (out, r.aux()) if keep else out
+    r = ops._alloc(stream, Fp8MoERunner, p, first.shape[0], topk, renormalize, block_size, device=first.device,
+                   router=router)
+    return _result(r, r(x, logits, stream=stream), stream, keep)

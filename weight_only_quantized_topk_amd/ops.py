@@ -84,17 +84,28 @@ def _row_stride(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _keep_for(stream, *tensors):
-    """Memory allocated here for a call on another stream than the current one
-    is not handed out again before that stream is done with it."""
-    if stream is None:
-        return
+def _alloc(stream, make, *args, **kw):
+    """make(*args, **kw): a buffer that a call on `stream` allocates, out of that
+    stream's memory.  A block of the current stream's may have been freed by a
+    call whose kernel, on that stream, still uses it; here it is handed out in
+    the order of the stream that the call's kernels run on."""
+    if stream is None or stream == _stream(None):
+        return make(*args, **kw)
     torch = _torch()
-    if stream != torch.cuda.current_stream().cuda_stream:
-        s = torch.cuda.ExternalStream(stream)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(s)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream)):
+        return make(*args, **kw)
+
+
+def _keep_for(stream, *tensors):
+    """Outputs allocated here for a call on another stream than the current one
+    are not handed out again before the current stream, on which the caller
+    reads them (once it waits for `stream`), is done with them."""
+    if stream is None or stream == _stream(None):
+        return
+    here = _torch().cuda.current_stream()
+    for t in tensors:
+        if t is not None:
+            t.record_stream(here)
 
 
 def _np_ptr(a: Optional[np.ndarray]):
@@ -108,12 +119,16 @@ def moe_route(logits, topk: int, renormalize: bool = True, topk_weights=None, to
     """logits [M, E] float32 (device) -> (topk_weights [M, topk] f32, topk_ids [M, topk] i32)."""
     torch = _torch()
     M, E = logits.shape
+    new = []
     if topk_weights is None:
-        topk_weights = torch.empty((M, topk), dtype=torch.float32, device=logits.device)
+        topk_weights = _alloc(stream, torch.empty, (M, topk), dtype=torch.float32, device=logits.device)
+        new.append(topk_weights)
     if topk_ids is None:
-        topk_ids = torch.empty((M, topk), dtype=torch.int32, device=logits.device)
+        topk_ids = _alloc(stream, torch.empty, (M, topk), dtype=torch.int32, device=logits.device)
+        new.append(topk_ids)
     check(load().moe_route(_ptr(logits), M, E, topk, int(bool(renormalize)), _ptr(topk_weights), _ptr(topk_ids),
                            _stream(stream)), "moe_route")
+    _keep_for(stream, *new)
     return topk_weights, topk_ids
 
 
@@ -138,15 +153,21 @@ def moe_align(topk_ids, E: int, block_size: int, capacity: Optional[int] = None,
     torch = _torch()
     M, topk = topk_ids.shape
     cap = moe_align_capacity(M, topk, E, block_size) if capacity is None else capacity
-    dev = topk_ids.device
+    new = []
+
+    def i32(n):
+        new.append(_alloc(stream, torch.empty, n, dtype=torch.int32, device=topk_ids.device))
+        return new[-1]
+
     if sorted_token_ids is None:
-        sorted_token_ids = torch.empty(max(cap, 1), dtype=torch.int32, device=dev)
+        sorted_token_ids = i32(max(cap, 1))
     if expert_ids is None:
-        expert_ids = torch.empty(max(cap // block_size, 1), dtype=torch.int32, device=dev)
+        expert_ids = i32(max(cap // block_size, 1))
     if num_tokens_post_padded is None:
-        num_tokens_post_padded = torch.empty(1, dtype=torch.int32, device=dev)
+        num_tokens_post_padded = i32(1)
     check(load().moe_align(_ptr(topk_ids), M, topk, E, block_size, _ptr(sorted_token_ids), _ptr(expert_ids),
                            _ptr(num_tokens_post_padded), cap, _stream(stream)), "moe_align")
+    _keep_for(stream, *new)
     return sorted_token_ids, expert_ids, num_tokens_post_padded
 
 
@@ -154,7 +175,7 @@ _SCORING = {"softmax": WQ_SCORE_SOFTMAX, "sigmoid": WQ_SCORE_SIGMOID}
 _GROUP_SCORE = {"max": WQ_GROUP_MAX, "top2": WQ_GROUP_TOP2}
 
 
-def _grouped_args(logits, topk, scoring, bias, n_group, topk_group, group_score, topk_weights, topk_ids):
+def _grouped_args(logits, topk, scoring, bias, n_group, topk_group, group_score, topk_weights, topk_ids, stream):
     torch = _torch()
     f32, dt = torch.float32, logits.dtype
     code = WQ_F32 if dt == f32 else WQ_BF16 if dt == torch.bfloat16 else WQ_F16
@@ -173,11 +194,11 @@ def _grouped_args(logits, topk, scoring, bias, n_group, topk_group, group_score,
         _check(bias, "bias", (E,), (f32,), dev)
     new = []
     if topk_weights is None:
-        new.append(topk_weights := torch.empty((M, topk), dtype=f32, device=dev))
+        new.append(topk_weights := _alloc(stream, torch.empty, (M, topk), dtype=f32, device=dev))
     else:
         _check(topk_weights, "topk_weights", (M, topk), (f32,), dev)
     if topk_ids is None:
-        new.append(topk_ids := torch.empty_like(topk_weights, dtype=torch.int32))
+        new.append(topk_ids := _alloc(stream, torch.empty_like, topk_weights, dtype=torch.int32))
     else:
         _check(topk_ids, "topk_ids", (M, topk), (torch.int32,), dev)
     return M, E, code, topk_weights, topk_ids, new
@@ -192,7 +213,7 @@ def moe_route_grouped(logits, topk: int, scoring: str = "softmax", bias=None, n_
     logits [M, E] float32 / fp16 / bf16 (device) -> (topk_weights [M, topk]
     f32, topk_ids [M, topk] i32)."""
     M, E, dt, topk_weights, topk_ids, new = _grouped_args(logits, topk, scoring, bias, n_group, topk_group,
-                                                          group_score, topk_weights, topk_ids)
+                                                          group_score, topk_weights, topk_ids, stream)
     check(load().moe_route_grouped(_ptr(logits), dt, M, E, topk, _SCORING[scoring], _ptr(bias), n_group, topk_group,
                                    _GROUP_SCORE[group_score], int(bool(renormalize)), routed_scale,
                                    _ptr(topk_weights), _ptr(topk_ids), _stream(stream)), "moe_route_grouped")
@@ -211,7 +232,7 @@ def moe_route_grouped_align(logits, topk: int, block_size: int, scoring: str = "
     not given are allocated, for the least capacity unless one is given."""
     torch = _torch()
     M, E, dt, topk_weights, topk_ids, new = _grouped_args(logits, topk, scoring, bias, n_group, topk_group,
-                                                          group_score, topk_weights, topk_ids)
+                                                          group_score, topk_weights, topk_ids, stream)
     _int32(block_size=block_size)
     if block_size < 1:
         raise ValueError("block_size must be >= 1, got %d" % block_size)
@@ -220,7 +241,7 @@ def moe_route_grouped_align(logits, topk: int, block_size: int, scoring: str = "
     if sorted_token_ids is None and expert_ids is None and num_tokens_post_padded is None:
         # one allocation for the three, each at a multiple of 16 bytes
         rows = -(-max(cap, 1) // 4) * 4
-        new.append(torch.empty(rows + 4 + max(blocks, 1), dtype=i32, device=dev))
+        new.append(_alloc(stream, torch.empty, rows + 4 + max(blocks, 1), dtype=i32, device=dev))
         arrays = torch.split_with_sizes(new[-1], (rows, 1, 3, max(blocks, 1)))
         arrays = [arrays[0], arrays[3], arrays[1]]
     else:
@@ -228,7 +249,7 @@ def moe_route_grouped_align(logits, topk: int, block_size: int, scoring: str = "
                   (num_tokens_post_padded, "num_tokens_post_padded", 1)]
         for k, (t, name, n) in enumerate(arrays):
             if t is None:
-                t = torch.empty(max(n, 1), dtype=i32, device=dev)
+                t = _alloc(stream, torch.empty, max(n, 1), dtype=i32, device=dev)
                 new.append(t)
             elif t.dim() != 1 or t.numel() < n:
                 raise ValueError("%s must hold %d values, got %s" % (name, n, list(t.shape)))
@@ -283,7 +304,7 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, quant: Optional[s
 
     def like_x(t, name):
         if t is None:
-            t = torch.empty_like(x, memory_format=torch.contiguous_format)
+            t = _alloc(stream, torch.empty_like, x, memory_format=torch.contiguous_format)
             new.append(t)
         else:
             _check(t, name, shape, same, dev, row_stride=True)
@@ -299,13 +320,13 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, quant: Optional[s
         os_ = _row_stride(out)
     if quant is not None:
         if codes is None:
-            codes = torch.empty_like(x, dtype=torch.uint8, memory_format=torch.contiguous_format)
+            codes = _alloc(stream, torch.empty_like, x, dtype=torch.uint8, memory_format=torch.contiguous_format)
             new.append(codes)
         else:
             _check(codes, "codes", shape, (torch.uint8, torch.float8_e4m3fn), dev)
         if quant == "row":
             if scales is None:
-                scales = torch.empty(rows, dtype=torch.float32, device=dev)
+                scales = _alloc(stream, torch.empty, rows, dtype=torch.float32, device=dev)
                 new.append(scales)
             else:
                 _check(scales, "scales", (rows,), (torch.float32,), dev)
@@ -454,10 +475,12 @@ def moe_fp8_codes_gemm(stage, codes, row_scales, M, topk, E, n_out, k_in, w_pack
 def _sparse24(fn, x, vals, meta, scales, N, out, group_size, stream):
     torch = _torch()
     M, K = x.shape
+    new = []
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        new.append(out := _alloc(stream, torch.empty, (M, N), dtype=torch.float16, device=x.device))
     check(fn(_ptr(x), M, K, N, _ptr(vals), _ptr(meta), _ptr(scales), group_size, _ptr(out), act_code(x.dtype),
              _stream(stream)), fn.__name__)
+    _keep_for(stream, *new)
     return out
 
 
@@ -541,24 +564,22 @@ def dense_lora_gemm(x, adapter_ids, a, b, scales, y, workspace=None, stream=None
     [adapters] float32 or None for ones.  Returns y."""
     torch = _torch()
     M, K, N, R, L, nbytes = _lora_sizes(x, adapter_ids, a, b, scales, y)
-    new = []
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-        new.append(workspace)
+        workspace = _alloc(stream, torch.empty, nbytes, dtype=torch.uint8, device=x.device)
     elif not workspace.is_contiguous() or workspace.device != x.device:
         raise ValueError("workspace must be contiguous on %s" % x.device)
     check(load().dense_lora_gemm(_ptr(x), _row_stride(x), M, K, N, R, L, _ptr(adapter_ids), _ptr(a), _ptr(b),
                                  _ptr(scales), _ptr(y), _row_stride(y), act_code(x.dtype), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _stream(stream)), "dense_lora_gemm")
-    _keep_for(stream, *new)
     return y
 
 
 def _dense(fn, x, N, w_packed, scales, extra, out, workspace, stream, act_order, lora):
     torch = _torch()
     M, K = x.shape
+    new = []
     if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        new.append(out := _alloc(stream, torch.empty, (M, N), dtype=x.dtype, device=x.device))
     if lora is not None:  # before anything is launched
         if not (x.is_contiguous() and out.is_contiguous()):
             raise ValueError("x and out must be contiguous")
@@ -567,11 +588,12 @@ def _dense(fn, x, N, w_packed, scales, extra, out, workspace, stream, act_order,
         _lora_sizes(x, *lora, out)
     if workspace is None:
         nb = dense_gemm_workspace_bytes(M, K, N, act_order)
-        workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=x.device)
+        workspace = _alloc(stream, torch.empty, max(nb, 1), dtype=torch.uint8, device=x.device)
     check(fn(_ptr(x), M, K, N, _ptr(w_packed), _ptr(scales), *extra, _ptr(out), act_code(x.dtype), _ptr(workspace),
              workspace.numel(), _stream(stream)), fn.__name__)
     if lora is not None:
         dense_lora_gemm(x, *lora, out, stream=stream)
+    _keep_for(stream, *new)
     return out
 
 
@@ -597,15 +619,17 @@ def quantize_w8(w, q=None, scales=None, stream=None):
     torch = _torch()
     if w.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError("quantize_w8 takes bf16 or fp16 weights, got %s" % w.dtype)
-    w = w.contiguous()
+    w = _alloc(stream, w.contiguous)  # (a copy runs on the stream, before the kernel)
     k = w.shape[-1]
     rows = w.numel() // k if k else 0
+    new = []
     if q is None:
-        q = torch.empty(w.shape, dtype=torch.int8, device=w.device)
+        new.append(q := _alloc(stream, torch.empty, w.shape, dtype=torch.int8, device=w.device))
     if scales is None:
-        scales = torch.empty(w.shape[:-1], dtype=w.dtype, device=w.device)
+        new.append(scales := _alloc(stream, torch.empty, w.shape[:-1], dtype=w.dtype, device=w.device))
     check(load().wq_quantize_w8(_ptr(w), rows, k, act_code(w.dtype), _ptr(q), _ptr(scales), _stream(stream)),
           "wq_quantize_w8")
+    _keep_for(stream, *new)
     return q, scales
 
 
