@@ -294,3 +294,28 @@ def test_pack_lora():
                 [(torch.randn(3, 64), torch.randn(32, 3), 1.0), (torch.randn(3, 65), torch.randn(32, 3), 1.0)]):
         with pytest.raises(ValueError):
             wq.pack_lora(bad, torch.bfloat16, device="cpu")
+
+
+def test_codes_gemm_binding_refuses_short_or_foreign_arrays():
+    """What the kernels read beside the rows: too few values, another type, no contiguous layout."""
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    E, n_out, k_in, cap, bs = 8, 256, 256, 128, 16
+    good = dict(w_packed=torch.zeros(E * n_out * k_in, dtype=u8), scales=torch.zeros((E, n_out)),
+                sorted_token_ids=torch.zeros(cap, dtype=i32), expert_ids=torch.zeros(cap // bs, dtype=i32),
+                num_tokens_post_padded=torch.zeros(1, dtype=i32))
+
+    def call(**change):
+        wq.moe_fp8_codes_gemm(wq.WQ_STAGE_GATE_UP, torch.zeros((4, k_in), dtype=u8), torch.ones(4), 4, 2, E, n_out, k_in,
+                              capacity=cap, block_size=bs, out=torch.zeros((cap, n_out // 2), dtype=u8),
+                              stream=0, **{**good, **change})
+
+    for name, t in good.items():
+        flat = t.reshape(-1)
+        with pytest.raises(ValueError, match=name):
+            call(**{name: flat[:-1]})
+        with pytest.raises(ValueError, match=name):
+            call(**{name: torch.cat([flat, flat])[::2] if len(flat) > 1 else flat[:0]})
+        with pytest.raises(TypeError, match=name):
+            call(**{name: t.to(torch.int64)})
+    with pytest.raises(wq.WqError):  # as it should be, it goes on to the library, which refuses host memory
+        call()
