@@ -160,9 +160,13 @@ wq_status moe_route_align(const float* d_logits, int M, int E, int topk, int ren
  * Scores, sums and quotients are double, weights are rounded once to float.
  *   d_logits        device [M, E], logits_dtype WQ_F32, WQ_F16 or WQ_BF16.
  *                   -inf is a score of 0; a row whose scores are all 0, or
- *                   whose slots' are, gets weights of 0.  With a NaN or +inf
- *                   logit the weights of that row are unspecified (its ids
- *                   still name topk different experts).
+ *                   whose slots' are, gets weights of 0.  A NaN is the last
+ *                   in the choice (its c and value are); under sigmoid scores
+ *                   its weight is a NaN, with renormalize those of all the
+ *                   row's slots if it is among them.  Under softmax the
+ *                   weights of a row with a NaN or +inf are unspecified, and
+ *                   with a bias its choice is (its ids still name topk
+ *                   different experts).
  *   d_bias          device float [E] or NULL; -inf keeps an expert to the last
  *   d_topk_weights  device float [M, topk] (out)
  *   d_topk_ids      device int32 [M, topk] (out)

@@ -214,3 +214,36 @@ def test_graph_and_stream():
         torch.cuda.synchronize()
         for x, y in zip(held, wq.moe_route_grouped_align(live, 6, 16, **how)):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("M", [7, 5003])  # 64 and 16 lanes a token
+@pytest.mark.parametrize("biased", [False, True])
+def test_nan_under_sigmoid_scores(M, biased):
+    """A NaN logit ranks below every number, also where its bias is the largest, and is not hidden in the weights."""
+    need_gpu()
+    E, k = 16, 5
+    lg, b = logits_of(M, E, "f32", 21), bias_of(E, 3)
+    lg[0] = np.nan
+    lg[1, 2:14] = np.nan  # four numbers are left
+    lg[2, ::2] = np.nan
+    lg[3, 6] = np.nan
+    b[6] = 3.0
+    order = torch.sigmoid(lg.double()) + b.double() if biased else lg.double()
+    for renorm in (True, False):
+        say("nan, sigmoid", M, biased, renorm)
+        w, ids = wq.moe_route_grouped(lg.cuda(), k, scoring="sigmoid", bias=b.cuda() if biased else None, renormalize=renorm)
+        w, ids = w.cpu().double(), ids.cpu()
+        for m in range(7):
+            nan = torch.isnan(lg[m])
+            rank = sorted(range(E), key=lambda e: (bool(nan[e]), 0.0 if nan[e] else -float(order[m, e].float() if biased else order[m, e]), e))
+            assert ids[m].tolist() == rank[:k], m
+            s = torch.sigmoid(lg[m].double())[ids[m].long()]
+            ref = s / s.sum() if renorm else s
+            assert torch.equal(torch.isnan(w[m]), torch.isnan(ref)), m
+            num = ~torch.isnan(ref)
+            assert bool(((w[m] - ref).abs()[num] <= 2.0 ** -23 * ref[num]).all()), m
+    # groups by their two best numbers: group 1 holds the largest number and NaN otherwise, so it has no second
+    lg[4] = torch.arange(16.0) / 16
+    lg[4, 4:8] = torch.tensor([9.0, np.nan, np.nan, np.nan])
+    ids = wq.moe_route_grouped(lg.cuda(), 4, scoring="sigmoid", n_group=4, topk_group=2, group_score="top2")[1].cpu()
+    assert ids[4].tolist() == [15, 14, 13, 12]

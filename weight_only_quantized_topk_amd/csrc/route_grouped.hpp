@@ -10,8 +10,9 @@
 //   slots = the topk best experts of the open groups
 //   w_j = scale * s_j, over the slots' sum of s when renormalised; a sum of
 //         zero gives weights of zero
-// Equal values: the lower group, the lower expert.  A NaN ranks below every
-// number, so the slots always name topk different experts.
+// Equal values: the lower group, the lower expert.  A NaN (c_e of a NaN logit,
+// all of a row's under softmax) ranks below every number, so the slots always
+// name topk different experts.
 //
 // Layout: W lanes take a token (64, or 16 and four tokens a wave).  The groups,
 // padded to a power of two, share them evenly (LPG lanes each) and a lane holds
@@ -87,12 +88,12 @@ __device__ __forceinline__ double token_sum(double v) {
 
 // 1 / d for d >= 1 by the hardware's estimate and two Newton steps (the last
 // bit may differ from the rounded quotient, far below the float that is
-// compared); 0 for an infinite d
+// compared); 0 for an infinite d (the steps would give a NaN), a NaN for a NaN
 __device__ __forceinline__ double inverse(double d) {
     double r = __builtin_amdgcn_rcp(d);
     r = fma(r, fma(-d, r, 1.0), r);
     r = fma(r, fma(-d, r, 1.0), r);
-    return d < __builtin_inf() ? r : 0.0;
+    return d == __builtin_inf() ? 0.0 : r;
 }
 
 // the score of a logit but for the softmax's sum: exp(l - ref), or 1 / (1 +
