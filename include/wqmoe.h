@@ -203,8 +203,9 @@ wq_status moe_route_grouped_align(const void* d_logits, int logits_dtype, int M,
  *     d_scales   a scale per row, written: c = max(max|y| / 448, 2^-100); the
  *                code is that of y * (1 / c)
  *     otherwise  static_scale: the code is that of y / static_scale
- * s is not rounded before the norm.  Any one of residual_out, out and codes
- * may be the only output.  Rows of bf16 values beyond float32's square range
+ * s is not rounded before the norm.  A row's bits depend on its values, on n and
+ * on whether n and the strides are multiples of 8, not on the number of rows.
+ * Any one of residual_out, out and codes may be the only output.  Rows of bf16 values beyond float32's square range
  * are scaled down first; a row with an infinity or a NaN gives what the
  * formulas do (NaN codes are 0x7F or 0xFF, the row scale skips NaNs).
  *   d_x, d_residual, d_residual_out, d_out: [rows, n] act dtype, row strides in

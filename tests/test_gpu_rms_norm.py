@@ -184,6 +184,24 @@ def test_rows_do_not_depend_on_the_batch():
     assert torch.equal(all_.scales[11:12], one.scales)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [520, 1001, 1024, 2048, 4104, 5120, 8192, 16384])
+def test_rows_do_not_depend_on_the_number_of_rows(n, kind):
+    """The launch shape goes by the rows (up to 256, more) at some widths; a row's bits do not, also where its squares
+    pass float32's range."""
+    need_gpu()
+    x, r, w = inputs(300, n, DT[kind], 6)
+    if kind == "bf16":
+        x[17] = x[17] * 1e25
+    all_ = wq.rms_norm(x, w, EPS, residual=r, quant="row")
+    for at, rows in ((0, 1), (17, 1), (0, 256), (40, 257)):
+        say("rows", n, kind, at, rows)
+        part = wq.rms_norm(x[at:at + rows].clone(), w, EPS, residual=r[at:at + rows].clone(), quant="row")
+        torch.cuda.synchronize()
+        for a, b in zip(all_, part):
+            assert torch.equal(a[at:at + rows], b)
+
+
 def test_empty_graph_and_stream():
     need_gpu()
     e = wq.rms_norm(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), quant="row")

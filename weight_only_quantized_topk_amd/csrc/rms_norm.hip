@@ -121,12 +121,47 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[VEC]) {
 constexpr float SUM_MAX = 3.0e38f;
 constexpr float DOWN = 0x1p-96f;
 
+// The row's sum of squares, in an order that the launch shape does not change
+// (the shape goes by the number of rows, a row's bits must not): each vector of 8
+// by itself, the 64 consecutive vectors of a wave, then these sums in ascending
+// order, whether one wave holds several of them or several waves one each.
+// Single values: one chain a thread, in shapes that go by the width only.
+template <int VEC, int TPR, int VPT>
+__device__ __forceinline__ float row_squares(const float (&v)[VPT][VEC], float* buf) {
+    constexpr int SUMS = VEC == 1 ? 1 : VPT;
+    float p[SUMS];
+#pragma unroll
+    for (int k = 0; k < SUMS; ++k) p[k] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) p[i % SUMS] = fmaf(v[i][j], v[i][j], p[i % SUMS]);
+#pragma unroll
+    for (int k = 0; k < SUMS; ++k) p[k] = wave_all<Add>(p[k]);
+    float total;
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int k = 0; k < SUMS; ++k) buf[k * (TPR / 64) + (threadIdx.x >> 6)] = p[k];
+        }
+        __syncthreads();
+        total = buf[0];
+#pragma unroll
+        for (int k = 1; k < SUMS * (TPR / 64); ++k) total += buf[k];
+    } else {
+        total = p[0];
+#pragma unroll
+        for (int k = 1; k < SUMS; ++k) total += p[k];
+    }
+    return total;
+}
+
 // A row in registers: TPR threads, VPT vectors of VEC values each.
 template <bool BF16, int VEC, int TPR, int VPT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_kernel(RmsNormArgs g) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     static_assert(RPB == 1 || TPR == 64, "rows that share a workgroup are one wave each: no barrier");
-    __shared__ float buf[4][TPR / 64];
+    __shared__ float buf[4][VPT * (TPR / 64)];
     const int tid = threadIdx.x % TPR;
     const int64_t row = block_index() * RPB + threadIdx.x / TPR;
     if (row >= g.rows) return;
@@ -164,12 +199,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_kernel(RmsNorm
     }
     if (!g.out && !g.codes) return;
 
-    float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-    ss = row_all<Add, TPR>(ss, buf[0]);
+    float ss = row_squares<VEC, TPR, VPT>(v, buf[0]);
     float eps = g.eps;
     if (!(ss <= SUM_MAX)) {  // the same for the whole row
         float am = 0.0f;
@@ -179,15 +209,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_kernel(RmsNorm
             for (int j = 0; j < VEC; ++j) am = fmaxf(am, fabsf(v[i][j]));
         am = row_all<Max, TPR>(am, buf[1]);
         if (am < __builtin_inff()) {  // finite (or a NaN beside finite values, which keeps the sum a NaN)
-            ss = 0.0f;
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    v[i][j] *= DOWN;
-                    ss = fmaf(v[i][j], v[i][j], ss);
-                }
-            ss = row_all<Add, TPR>(ss, buf[2]);
+                for (int j = 0; j < VEC; ++j) v[i][j] *= DOWN;
+            ss = row_squares<VEC, TPR, VPT>(v, buf[2]);
             eps = 0.0f;  // nothing beside such a sum
         }
     }
