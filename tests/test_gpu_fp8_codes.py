@@ -242,3 +242,93 @@ def test_layers_with_a_router():
         import oracle
         ref = oracle.moe_layer_from_weights(wts, x.float().cpu().numpy(), w.astype(np.float32), ids)["out"]
         assert_close_fp(out.float().cpu().numpy(), ref, "router layer M=%d" % M)
+
+
+def of_size(M, N, E, topk, K, bs, stage, seed):
+    """Codes, row scales 2^-2 .. 2^-4 by token, random routing -> (run on codes, quantising run at one scale, token of each row)."""
+    g = torch.Generator().manual_seed(seed)
+    w = torch.randint(0, 256, (E, 2 * N, K), generator=g, dtype=torch.uint8).numpy()
+    w[(w & 0x7F) >= 0x60] &= 0x8F
+    ws = (2.0 ** torch.randint(-7, -4, (E, 2 * N), generator=g).float()).numpy()
+    wp, sp = wq.pack_fp8(w, ws, interleave_gate_up=stage == wq.WQ_STAGE_GATE_UP)
+    wp, sp = torch.from_numpy(wp).cuda(), torch.from_numpy(sp).cuda()
+    codes = torch.randint(0, 256, (M, K), generator=g, dtype=torch.uint8)
+    codes[(codes & 0x7F) >= 0x70] &= 0x8F
+    value = torch.from_numpy(e4m3_values(codes.numpy())).cuda()
+    codes = codes.cuda()
+    ids = torch.argsort(torch.rand((M, E), generator=g), dim=1)[:, :topk].int().cuda()
+    cap = wq.moe_align_capacity(M, topk, E, bs)
+    st, ex, nt = wq.moe_align(ids, E, bs, cap)
+    gate_up = stage == wq.WQ_STAGE_GATE_UP
+    token = st[:int(nt)].long() // topk if gate_up else torch.arange(M * topk, device="cuda") // topk
+    rows = 2.0 ** -(2 + torch.arange(M, device="cuda") % 3).float()
+
+    def out():
+        return (torch.zeros((cap, N), dtype=torch.uint8, device="cuda") if gate_up
+                else torch.zeros((M * topk, 2 * N), device="cuda"))
+
+    common = (M, topk, E, 2 * N, K, wp, sp, st, ex, nt, cap, bs)
+
+    def on_codes():
+        got = wq.moe_fp8_codes_gemm(stage, codes, rows, *common, out(), out_scale=0.5)
+        return got[:len(token)]
+
+    def quantising(scale):
+        work = torch.empty(wq.moe_fp8_gemm_workspace_bytes(stage, M, topk, E, 2 * N, K), dtype=torch.uint8, device="cuda")
+        got = out()
+        wq.moe_fp8_w8a8_gemm(stage, (value * scale).bfloat16(), *common, None, got, work, scale, 0.5)
+        return got[:len(token)]
+
+    plain = dict(w=w, ws=ws, x=value, ids=ids.cpu().numpy())
+    return on_codes, quantising, token, plain
+
+
+def compare_row_scales(on_codes, quantising, token, M):
+    got = on_codes()
+    torch.cuda.synchronize()
+    assert bool(got.any())
+    for k in range(3):
+        ref = quantising(2.0 ** -(2 + k))
+        torch.cuda.synchronize()
+        of = (token < M) & (token % 3 == k)
+        assert bool(of.any()) and torch.equal(got[of], ref[of]), k
+    pad = token >= M
+    assert not bool(got[pad].any())
+    return got
+
+
+@pytest.mark.parametrize("stage", [wq.WQ_STAGE_GATE_UP, wq.WQ_STAGE_RAW])
+@pytest.mark.parametrize("M,N", [(300, 256), (4300, 256), (9001, 256), (9001, 384), (50001, 256), (40001, 384), (700, 192)])
+def test_row_scales_in_each_tile_shape(M, N, stage):
+    """128-row blocks: 128 x 128, 256 x 128, 256 x 64 by XCD and 512 x 128 tiles (and widths that only one of them
+    takes), every token with a scale that its neighbours do not have."""
+    need_gpu()
+    say("row scales", M, N, stage)
+    made = of_size(M, N, 8, 2, 384, 128, stage, M + N)
+    compare_row_scales(*made[:3], M)
+
+
+@pytest.mark.parametrize("stage", [wq.WQ_STAGE_GATE_UP, wq.WQ_STAGE_RAW])
+@pytest.mark.parametrize("bs", [16, 64, 128])
+@pytest.mark.parametrize("M,E,topk,N", [(3, 64, 6, 128), (100, 64, 6, 128), (200, 160, 6, 128), (333, 256, 8, 64), (1500, 64, 6, 512)])
+def test_many_experts(M, E, topk, N, bs, stage):
+    """64 experts and more: the small-batch kernel's shape for them, 64- and 128-row blocks with most of them part empty;
+    RAW also against float64 on some rows.  There each of the 3 products of 128 channels is off by at most 2^-9 of the
+    largest value it adds (the matrix instruction drops bits 2^-11 below it in 4 groups, as test_gpu_fp8.py bounds it):
+    a term, or the sum so far, which the 3 products' own sums bound in any order; the sums and the two scalings add 5
+    roundings of float32."""
+    need_gpu()
+    say("many experts", M, E, topk, N, bs, stage)
+    K = 384
+    on_codes, quantising, token, plain = of_size(M, N, E, topk, K, bs, stage, M + E + bs)
+    got = compare_row_scales(on_codes, quantising, token, M)
+    if stage == wq.WQ_STAGE_RAW:
+        x = plain["x"].double().cpu().numpy()
+        for pair in range(0, M * topk, max(1, M * topk // 50)):
+            m, e = pair // topk, plain["ids"][pair // topk, pair % topk]
+            terms = e4m3_values(plain["w"][e]) * x[m]  # [2N, K]
+            scale = plain["ws"][e] * 2.0 ** -(2 + m % 3)
+            ref = terms.sum(1) * scale
+            largest = np.maximum(np.abs(terms).max(1), np.abs(terms.reshape(2 * N, 3, 128).sum(2)).sum(1))
+            off = (3 * 2.0 ** -9 * largest + 5 * 2.0 ** -24 * np.abs(terms).sum(1)) * scale
+            assert (np.abs(got[pair].double().cpu().numpy() - ref) <= off).all(), pair
