@@ -38,6 +38,11 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 // 32 channels), both E4M3 (format 0), block scales 2^0 (E8M0 127).  The
 // channel order inside a lane's 32 bytes is the same for A and B, so the sum
 // runs over all 128 channels whatever order the instruction pairs them in.
+// D is float32, but the instruction drops low bits of products far below the
+// largest value it adds (beyond 2^11 times smaller, at most 2^-11 of the largest
+// in each group of 32 channels): a sum is right to about 1e-4 of its terms, and
+// 0.1 % of the H codes, those next to a border, are the neighbouring code.  The
+// exact way, 16-bit products, has half the rate and twice the bytes in LDS.
 __device__ __forceinline__ f32x4 mfma_e4m3(const u32x8& a, const u32x8& b, f32x4 c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, a), __builtin_bit_cast(i32x8, b),
                                                             c, 0, 0, 0, 127, 0, 127);
@@ -633,11 +638,21 @@ int fp8_down_split(int T, int E, int n_out, int k_in, int block_size) {
 // 49 / 52, 476 tiles 203 / 177 / 182, 560 tiles 208 / 189 / 203, 1120 tiles 336 /
 // 367 / 409, 3808 tiles 1070 / 1252 / 1376.
 // Between them, where the 256 x 128 tiles are more than a round of the CUs (one
-// workgroup each) and the experts have more than half a block of rows, 256 x 64 with
-// two workgroups per CU and the tiles ordered by XCD.  us, 256 x 128 / 256 x 64: 84
-// tiles 48 / 54; 140 tiles 80 / 65, 252 tiles 107 / 94, 440 tiles of 64 experts (K =
-// 2048, 96 rows each) 117 / 97, 476 tiles 173 / 172; 448 tiles with 64 rows an expert
-// 212 / 226; 140 tiles unordered: 93.
+// workgroup each), 256 x 64 with two workgroups per CU and the tiles ordered by XCD:
+// from 160 rows an expert; with a short reduction, where 256 x 128 waits longest
+// between tiles, from 64.  (Up to 128 rows an expert is one block, whose two 64-row
+// tiles read its weights twice where 256 x 128 reads them once.)  It has no upper end where
+// the width is no multiple of 512.  us, 256 x 128 / 256 x 64, experts x K x width:
+//   8 x 4096 x 3584: 140 tiles 76 / 57, 357 128 / 114, 581 202 / 168, 756 239 / 217
+//   8 x 2048 x 2816: 198 tiles 61 / 45, 726 174 / 133, 1430 318 / 245
+//   rows an expert                70         120        180        240 / 300
+//   64 x 2048 x 2816          114 /  99  126 / 108  164 / 152  193 / 159
+//   160 x 2048 x 2816         249 / 221  274 / 251  372 / 368  461 / 384
+//   64 x 4096 x 2816          168 / 167  207 / 205  283 / 268  448 / 350
+//   64 x 7168 x 2816          256 / 298  312 / 352  452 / 439  707 / 567
+//   160 x 5120 x 2816         441 / 536  552 / 599  796 / 790  938 / 836
+//   16 x 6144 x 14336         283 / 310  294 / 331 (then more than 768 tiles)
+// 140 tiles of the first unordered: 93 (256 x 128: 80).
 template <int STAGE>
 static void launch_fp8_prefill_codes(const Fp8GemmArgs& g, hipStream_t s) {
     if (g.block_size == 64) {
@@ -648,7 +663,8 @@ static void launch_fp8_prefill_codes(const Fp8GemmArgs& g, hipStream_t s) {
     const long T = (long)g.M * g.topk;
     const long tiles = (T + std::min<long>(T, g.E) * 64 + 127) / 128 * g.n_out / 512;  // as fp8_down_split counts
     if (g.n_out % 512 == 0 && tiles > 768) launch_fp8_prefill_cfg<STAGE, 8, 4, 128, 1, true>(g, 1, s);
-    else if (g.n_out % 256 == 0 && tiles > 128 && T > 64L * g.E) launch_fp8_prefill_cfg<STAGE, 8, 2, 64, 2, true, true>(g, 1, s);
+    else if (g.n_out % 256 == 0 && tiles > 128 && T > (g.k_in <= 2048 ? 64L : 160L) * g.E)
+        launch_fp8_prefill_cfg<STAGE, 8, 2, 64, 2, true, true>(g, 1, s);
     else if (g.n_out % 256 == 0 && tiles > 64) launch_fp8_prefill_cfg<STAGE, 8, 2, 128, 1, true>(g, 1, s);
     else launch_fp8_prefill_cfg<STAGE, 4, 2, 128, 2, true>(g, 1, s);
 }
