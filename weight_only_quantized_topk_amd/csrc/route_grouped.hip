@@ -56,12 +56,17 @@ static void with_per_lane(int per, F f) {
 
 // Lanes per token: 16 lanes and four tokens a wave take fewer instructions per
 // token, 64 lanes the shorter chain (a lane's exponentials in double and its
-// compares follow one another).  us with 16 / 64 lanes: 8 experts (1 per lane)
-// 512 tokens 3.0 / 3.2, 4096 tokens 3.2 / 4.3; 160 experts (12 per lane) 1024
-// tokens 7.5 / 5.4, 4096 tokens 7.7 / 8.2; 256 experts (16 per lane) 4096 tokens
-// 11.4 / 9.7, 8192 tokens 14.0 / 16.1
+// compares follow one another): 16 lanes pay from 400 tokens per expert of a lane where
+// every expert has its exponential, from 200 where the slots alone have one.  us with
+// 16 / 64 lanes, sigmoid with a bias and groups' two best | renormalised softmax:
+//   96 experts (8 per lane)   3000 tokens  5.7 /  4.7,  3600  5.7 /  5.3 | 1200  3.5 / 3.6,  1800  3.5 / 3.7
+//   128 experts (8 per lane)  2720 tokens  7.3 /  6.5,  3200  7.3 /  7.4 | 1600  5.0 / 5.1,  3200  5.1 / 6.7
+//   160 experts (12 per lane) 4096 tokens  8.3 /  8.3,  5000  9.4 /  9.7 | 2000  5.2 / 4.8,  3000  5.2 / 5.6
+//   256 experts (16 per lane) 5440 tokens 12.8 / 12.0,  8000 13.0 / 14.8 | 3200  6.5 / 7.1,  5440  7.3 / 9.2
+//   8 experts (1 per lane)     200 tokens  2.7 /  2.9                    |  200  2.5 / 2.8
 static bool route_by_16(const RouteGroupedArgs& g, const GroupedLayout& few) {
-    return few.lpg > 0 && few.per <= 16 && g.M >= 400 * few.per;
+    const bool slots_only = !g.bias && !(g.top2 && g.groups > 1) && (g.sigmoid || g.renormalize);
+    return few.lpg > 0 && few.per <= 16 && g.M >= (slots_only ? 200 : 400) * few.per;
 }
 
 void launch_route_grouped(const RouteGroupedArgs& g, hipStream_t s) {
