@@ -236,3 +236,15 @@ def test_graph_stream_and_repeats():
     wq.dense_lora_gemm(e, torch.empty(0, dtype=torch.int32, device="cuda"),
                        torch.zeros((1, 8, 64), dtype=torch.bfloat16, device="cuda"),
                        torch.zeros((1, 64, 8), dtype=torch.bfloat16, device="cuda"), None, e.clone())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("ids", ["rows", "prompts", "one"])
+@pytest.mark.parametrize("shape", [(300, 1000, 5008, 24, 9), (517, 520, 3208, 32, 7), (263, 4096, 4104, 24, 33),
+                                   (1001, 1032, 1056, 32, 40), (290, 136, 6504, 24, 1)])
+def test_ranks_17_to_32_in_large_batches(shape, ids, kind):
+    """From 3 Mi elements of x and y on they take the large-batch kernels."""
+    need_gpu()
+    check(*shape, ids, kind)
+    if shape[1] <= 1024:
+        check(*shape, ids, kind, integers=True, pad=8)

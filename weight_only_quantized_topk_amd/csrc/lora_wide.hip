@@ -306,12 +306,20 @@ void launch_t(const LoraArgs& g, hipStream_t s) {
 
 // Large batches by the elements of x and y that pass: through LDS the loads are
 // whole cache lines, at the price of a longer chain.  us here / in lora.hip, 8
-// adapters: rank 16, 4096 x 4096: 2048 rows 28.7 / 26.1, 4096 rows 36.1 / 40.5;
-// rank 16, 7168 x 20480: 1024 rows 36.7 / 41.4; rank 64, 5120 x 1536: 256 rows 19.5 /
-// 18.7, 512 rows 22.3 / 27.6; rank 64, 7168 x 20480: 100 rows 30.1 / 24.2, 256 rows
-// 26.3 / 33.7.
+// adapters in 11 prompts | in random order:
+//   rank 8    4096 x 4096   2048 rows 22.9 / 21.0 | 45 / 53,  2730 rows 28.3 / 27.9 | 62 / 71,  4096 rows 29.7 / 34.0
+//   rank 16   4096 x 4096   2048 rows 23.1 / 22.7 | 47 / 58,  2730 rows 28.9 / 30.7 | 63 / 79
+//             7168 x 20480   348 rows 20.6 / 24.1 | 31 / 40,   697 rows 28.0 / 32.6 | 53 / 68
+//   rank 24   4096 x 4096    341 rows 15.0 / 15.1 | 20 / 23,  1365 rows 21.0 / 21.2 | 44 / 56
+//             7168 x 20480   261 rows 20.2 / 24.1 | 31 / 38,   5120 x 1536   512 rows 14.2 / 17.2 | 19 / 25
+//   rank 32   4096 x 4096    341 rows 15.0 / 16.0 | 20 / 25,   5120 x 1536  2048 rows 21.6 / 26.7 | 45 / 83
+//   rank 40   4096 x 4096    341 rows 20.5 / 18.2 | 28 / 29,   5120 x 1536   384 rows 16.0 / 20.6 | 23 / 30
+//   rank 64   4096 x 4096    341 rows 20.7 / 21.0 | 28 / 39,   5120 x 1536   384 rows 16.4 / 22.8 | 23 / 37
+//   rank 128  4096 x 4096    341 rows 28.4 / 31.0 | 44 / 67,   5120 x 1536   384 rows 26.3 / 32.9 | 43 / 74
+// rank 64, 7168 x 20480, 100 rows: 30.1 / 24.2.  32 adapters in random order: rank 24
+// 103 / 89 (4096 x 4096, 1365 rows) to 106 / 135 (5120 x 1536, 2048 rows), rank 128 101 / 154.
 bool lora_wide(int M, int K, int N, int R) {
-    return M >= 256 && R <= 128 && (int64_t)M * (K + 2 * (int64_t)N) > (R > 32 ? 3 << 20 : 32 << 20);
+    return M >= 256 && R <= 128 && (int64_t)M * (K + 2 * (int64_t)N) > (R > 16 ? 3 << 20 : 32 << 20);
 }
 
 // K slices of the first product: a workgroup per CU (two measured the same, with
