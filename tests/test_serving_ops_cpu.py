@@ -319,3 +319,16 @@ def test_codes_gemm_binding_refuses_short_or_foreign_arrays():
             call(**{name: t.to(torch.int64)})
     with pytest.raises(wq.WqError):  # as it should be, it goes on to the library, which refuses host memory
         call()
+
+
+def test_a_router_and_renormalize():
+    """renormalize=False is not overruled without a word by a router that renormalises."""
+    import types
+    p = types.SimpleNamespace(act=torch.bfloat16, act_code=BF, k_perm1=None, bits=8, E=8, K=256, N=128)
+    for runner in (wq.MoERunner, wq.Fp8MoERunner):
+        with pytest.raises(ValueError, match="renormalize"):
+            runner(p, 4, 2, renormalize=False, device="cpu", router=wq.Router())
+        for mine, its in ((True, True), (True, False), (False, False)):
+            r = runner(p, 4, 2, renormalize=mine, device="cpu", router=wq.Router(renormalize=its))
+            assert r.router.renormalize == its
+        assert runner(p, 4, 2, renormalize=False, device="cpu").renormalize is False

@@ -35,6 +35,12 @@ class Router:
     routed_scale: float = 1.0
 
 
+def _check_renormalize(renormalize, router):
+    """With a router the weights are renormalised as it says; a call that says otherwise is refused."""
+    if router is not None and not renormalize and router.renormalize:
+        raise ValueError("renormalize=False with a router that renormalises: give it renormalize=False")
+
+
 def _route_align(r, logits, stream):
     """The routing arrays of a runner's batch (its buffers), by its router."""
     if r.router is None:
@@ -124,11 +130,13 @@ class MoERunner:
     """The hot path for one batch shape with every buffer allocated up front, so
     a call allocates nothing.  marks: optional 3 events recorded on the stream
     after alignment, after GATE_UP and after DOWN (stage timing).  router: the
-    scores, bias and groups to route with (renormalize is then the router's)."""
+    scores, bias and groups to route with (its renormalize holds then; renormalize=False
+    beside a router that renormalises is refused)."""
 
     def __init__(self, p: PackedMoE, M: int, topk: int, renormalize: bool = True, block_size: Optional[int] = None,
                  device="cuda", router: Optional[Router] = None):
         import torch
+        _check_renormalize(renormalize, router)
         self.p, self.M, self.topk, self.renormalize, self.router = p, M, topk, renormalize, router
         self.bs = choose_block_size(M, topk, p.E, p.bits) if block_size is None else block_size
         self.cap = ops.moe_align_capacity(M, topk, p.E, self.bs)
@@ -291,6 +299,7 @@ class Fp8MoERunner:
     def __init__(self, p: PackedFp8MoE, M: int, topk: int, renormalize: bool = True,
                  block_size: Optional[int] = None, device="cuda", router: Optional[Router] = None):
         import torch
+        _check_renormalize(renormalize, router)
         self.p, self.M, self.topk, self.renormalize, self.router = p, M, topk, renormalize, router
         self.bs = choose_block_size(M, topk, p.E, 8) if block_size is None else block_size
         self.cap = ops.moe_align_capacity(M, topk, p.E, self.bs)
