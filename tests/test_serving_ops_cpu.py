@@ -332,3 +332,22 @@ def test_a_router_and_renormalize():
             r = runner(p, 4, 2, renormalize=mine, device="cpu", router=wq.Router(renormalize=its))
             assert r.router.renormalize == its
         assert runner(p, 4, 2, renormalize=False, device="cpu").renormalize is False
+
+
+def test_adapters_the_library_would_refuse_stop_the_projection():
+    """Unaligned arrays and too large ones, which dense_lora_gemm refuses, are found before the projection is launched."""
+    bf = torch.bfloat16
+    x, w, s = torch.zeros((4, 512), dtype=bf), torch.zeros(512 * 256, dtype=torch.uint8), torch.zeros(256, dtype=bf)
+    ids, one, work = torch.zeros(5, dtype=torch.int32), torch.ones(4), torch.zeros(1 << 20, dtype=torch.uint8)
+    a, b = torch.zeros((3, 16, 512), dtype=bf), torch.zeros((3, 256, 16), dtype=bf)
+    for bad, name in ((wq.Lora(ids[1:], a, b, None), "adapter_ids"), (wq.Lora(ids[:4], a, b, one[1:]), "scales"),
+                      (wq.Lora(ids[:4], torch.zeros(3 * 16 * 512 + 1, dtype=bf)[1:].view(3, 16, 512), b, None), "a is")):
+        with pytest.raises(ValueError, match=name):
+            wq.dense_w8a16_gemm(x, 256, w, s, lora=bad, out=torch.zeros((4, 256), dtype=bf), workspace=work, stream=0)
+        with pytest.raises(ValueError, match=name):
+            wq.dense_lora_gemm(x, *bad, torch.zeros((4, 256), dtype=bf), stream=0)
+    with pytest.raises(wq.WqError):  # as they should be, the call goes on to the library, which refuses host memory
+        wq.dense_w8a16_gemm(x, 256, w, s, lora=wq.Lora(ids[:4], a, b, one[:3]), out=torch.zeros((4, 256), dtype=bf),
+                            workspace=work, stream=0)
+    assert wq.dense_lora_workspace_bytes(4, 512, 1 << 24, 128, 1) == 0
+    assert status("dense_lora_gemm", *lora_args(N=1 << 24, R=128, ys=1 << 24))[0] == UNS

@@ -1112,6 +1112,7 @@ static const char* lora_sizes(int M, int K, int N, int R, int adapters) {
     if (M < 0 || K <= 0 || N <= 0 || R <= 0 || adapters <= 0) return "sizes must be positive (M >= 0)";
     if (M > MAX_PAIRS || K > (1 << 24) || N > (1 << 24) || R > 256) return "M, K or N > 2^24, or rank > 256";
     if (K % 8 || N % 8 || R % 8) return "K, N and the rank must be multiples of 8";
+    if ((int64_t)N * R > INT32_MAX) return "N * rank >= 2^31";
     return nullptr;
 }
 
@@ -1139,7 +1140,6 @@ wq_status dense_lora_gemm(const void* d_x, int64_t x_stride, int M, int K, int N
                    (long long)y_stride, N);
         WQ_REQUIRE(y_stride <= (1 << 25), WQ_ERR_UNSUPPORTED, "%s: y row stride %lld > 2^25", who,
                    (long long)y_stride);
-        WQ_REQUIRE((int64_t)N * R <= INT32_MAX, WQ_ERR_UNSUPPORTED, "%s: N * rank >= 2^31", who);
         WQ_REQUIRE(x_stride % 8 == 0 && y_stride % 8 == 0, WQ_ERR_UNSUPPORTED,
                    "%s: row strides must be multiples of 8 (%lld, %lld)", who, (long long)x_stride,
                    (long long)y_stride);

@@ -570,7 +570,11 @@ def _lora_sizes(x, adapter_ids, a, b, scales, y):
         _check(scales, "scales", (L,), (torch.float32,), dev)
     nbytes = dense_lora_workspace_bytes(M, K, N, R, L)
     if M and not nbytes:
-        raise ValueError("unsupported adapters: M %d K %d N %d rank %d (multiples of 8, rank at most 256)" % (M, K, N, R))
+        raise ValueError("unsupported adapters: M %d K %d N %d rank %d (multiples of 8, rank at most 256, N * rank < 2^31)"
+                         % (M, K, N, R))
+    for t, name in ((x, "x"), (y, "y"), (adapter_ids, "adapter_ids"), (a, "a"), (b, "b"), (scales, "scales")):
+        if M and t is not None and t.data_ptr() % 16:
+            raise ValueError("%s is not 16-byte aligned" % name)
     return M, K, N, R, L, nbytes
 
 
@@ -580,12 +584,18 @@ def dense_lora_gemm(x, adapter_ids, a, b, scales, y, workspace=None, stream=None
     they are).  x [M, K], y [M, N] bf16/fp16 (device; rows may be strided), a
     [adapters, rank, K] and b [adapters, N, rank] in their type, scales
     [adapters] float32 or None for ones.  Returns y."""
+    sizes = _lora_sizes(x, adapter_ids, a, b, scales, y)
+    if workspace is not None and (not workspace.is_contiguous() or workspace.device != x.device):
+        raise ValueError("workspace must be contiguous on %s" % x.device)
+    return _lora_call(sizes, x, adapter_ids, a, b, scales, y, workspace, stream)
+
+
+def _lora_call(sizes, x, adapter_ids, a, b, scales, y, workspace, stream):
+    """dense_lora_gemm of arguments that _lora_sizes has passed."""
     torch = _torch()
-    M, K, N, R, L, nbytes = _lora_sizes(x, adapter_ids, a, b, scales, y)
+    M, K, N, R, L, nbytes = sizes
     if workspace is None:
         workspace = _alloc(stream, torch.empty, nbytes, dtype=torch.uint8, device=x.device)
-    elif not workspace.is_contiguous() or workspace.device != x.device:
-        raise ValueError("workspace must be contiguous on %s" % x.device)
     check(load().dense_lora_gemm(_ptr(x), _row_stride(x), M, K, N, R, L, _ptr(adapter_ids), _ptr(a), _ptr(b),
                                  _ptr(scales), _ptr(y), _row_stride(y), act_code(x.dtype), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _stream(stream)), "dense_lora_gemm")
@@ -603,14 +613,14 @@ def _dense(fn, x, N, w_packed, scales, extra, out, workspace, stream, act_order,
             raise ValueError("x and out must be contiguous")
         if out.shape != (M, N):
             raise ValueError("out must be %s, got %s" % ([M, N], list(out.shape)))
-        _lora_sizes(x, *lora, out)
+        sizes = _lora_sizes(x, *lora, out)
     if workspace is None:
         nb = dense_gemm_workspace_bytes(M, K, N, act_order)
         workspace = _alloc(stream, torch.empty, max(nb, 1), dtype=torch.uint8, device=x.device)
     check(fn(_ptr(x), M, K, N, _ptr(w_packed), _ptr(scales), *extra, _ptr(out), act_code(x.dtype), _ptr(workspace),
              workspace.numel(), _stream(stream)), fn.__name__)
     if lora is not None:
-        dense_lora_gemm(x, *lora, out, stream=stream)
+        _lora_call(sizes, x, *lora, out, None, stream)
     _keep_for(stream, *new)
     return out
 
