@@ -391,7 +391,9 @@ wq_status moe_fp8_w8a8_gemm(const wq_moe_gemm_desc* d, float in_scale, float out
  *   g, u = row scale * scale[row] * (x codes . weight codes); the rest as
  *   moe_fp8_w8a8_gemm, d_workspace unused.  A NaN code in a token's row gives
  *   NaN codes in its H rows, and in no other.
- * Errors: those of moe_fp8_w8a8_gemm; WQ_ERR_INVALID for the DOWN stage.
+ * Errors: those of moe_fp8_w8a8_gemm; WQ_ERR_INVALID for the DOWN stage;
+ * WQ_ERR_UNSUPPORTED for more than 65535 blocks of 64 or 128 rows on the
+ * large-batch kernel.
  */
 wq_status moe_fp8_codes_gemm(const wq_moe_gemm_desc* d, const float* d_row_scales, float in_scale, float out_scale,
                              void* stream);

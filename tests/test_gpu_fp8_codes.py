@@ -332,3 +332,28 @@ def test_many_experts(M, E, topk, N, bs, stage):
             largest = np.maximum(np.abs(terms).max(1), np.abs(terms.reshape(2 * N, 3, 128).sum(2)).sum(1))
             off = (3 * 2.0 ** -9 * largest + 5 * 2.0 ** -24 * np.abs(terms).sum(1)) * scale
             assert (np.abs(got[pair].double().cpu().numpy() - ref) <= off).all(), pair
+
+
+def test_more_64_row_tiles_than_a_grid_dimension_takes():
+    """Beyond 65535 tiles of 64 rows the 128-row tiles go on."""
+    need_gpu()
+    M, N, E, K, topk, bs = 2_100_001, 128, 8, 128, 2, 128
+    w = torch.randint(0, 256, (E, 2 * N, K), generator=torch.Generator().manual_seed(1), dtype=torch.uint8).numpy()
+    w[(w & 0x7F) >= 0x60] &= 0x8F
+    wp, sp = wq.pack_fp8(w, np.full((E, 2 * N), 2.0 ** -6, np.float32), interleave_gate_up=True)
+    wp, sp = torch.from_numpy(wp).cuda(), torch.from_numpy(sp).cuda()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    codes = torch.randint(0, 0x70, (M, K), generator=g, dtype=torch.uint8, device="cuda")
+    ids = torch.argsort(torch.rand((M, E), generator=g, device="cuda"), dim=1)[:, :topk].int().contiguous()
+    cap = wq.moe_align_capacity(M, topk, E, bs)
+    assert cap // 64 > 65535 >= cap // 128
+    st, ex, nt = wq.moe_align(ids, E, bs, cap)
+    say("many tiles", M, cap)
+    got, ref = torch.zeros((2, cap, N), dtype=torch.uint8, device="cuda")
+    common = (M, topk, E, 2 * N, K, wp, sp, st, ex, nt, cap, bs)
+    wq.moe_fp8_codes_gemm(wq.WQ_STAGE_GATE_UP, codes, torch.full((M,), 0.125, device="cuda"), *common, got, out_scale=0.5)
+    x = codes.view(torch.float8_e4m3fn).bfloat16() * 0.125
+    work = torch.empty(M * K + 256, dtype=torch.uint8, device="cuda")
+    wq.moe_fp8_w8a8_gemm(wq.WQ_STAGE_GATE_UP, x, *common, None, ref, work, 0.125, 0.5)
+    torch.cuda.synchronize()
+    assert bool(got[-cap // 4:].any()) and torch.equal(got, ref)

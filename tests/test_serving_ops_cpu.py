@@ -351,3 +351,15 @@ def test_adapters_the_library_would_refuse_stop_the_projection():
                             workspace=work, stream=0)
     assert wq.dense_lora_workspace_bytes(4, 512, 1 << 24, 128, 1) == 0
     assert status("dense_lora_gemm", *lora_args(N=1 << 24, R=128, ys=1 << 24))[0] == UNS
+
+
+def test_codes_gemm_row_limit():
+    """More token tiles than a grid dimension takes are refused before any device work."""
+    for bs, tile in ((64, 64), (128, 128), (256, 128)):
+        M = 65535 * tile // 2 + 1
+        cap = wq.moe_align_capacity(M, 2, 8, bs)
+        how = dict(M=M, capacity=cap, block_size=bs, k_in=128)
+        assert status("moe_fp8_codes_gemm", codes_desc(**how), at(), 1.0, 1.0, None)[0] == UNS
+    how = dict(M=65535 * 32 - 1000, k_in=128, block_size=64)
+    how["capacity"] = wq.moe_align_capacity(how["M"], 2, 8, 64)
+    assert status("moe_fp8_codes_gemm", codes_desc(**how), at(), 1.0, 1.0, None)[0] in (wq.WQ_ERR_DEVICE, wq.WQ_ERR_HIP)

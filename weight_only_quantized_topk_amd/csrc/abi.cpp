@@ -807,6 +807,9 @@ static wq_status fp8_gemm(const wq_moe_gemm_desc* d, float in_scale, float out_s
     const size_t a_rows = stage == WQ_STAGE_DOWN ? d->capacity : (size_t)d->M;
     WQ_REQUIRE(!large || a_rows * (size_t)d->k_in <= (size_t)0xffffffffu, WQ_ERR_UNSUPPORTED,
                "%s: activations of %zu rows x %d codes exceed 4 GiB (large-batch kernel)", who, a_rows, d->k_in);
+    // its token tiles lie along grid y
+    WQ_REQUIRE(!codes || !large || d->capacity / (d->block_size == 64 ? 64 : 128) <= 65535, WQ_ERR_UNSUPPORTED,
+               "%s: capacity %zu exceeds 65535 token tiles", who, d->capacity);
     if (d->M == 0) return ok();
     WQ_TRY(check_ptr(d->d_a, "a"));
     WQ_TRY(check_ptr(d->d_w_packed, "w_packed"));

@@ -663,7 +663,8 @@ static void launch_fp8_prefill_codes(const Fp8GemmArgs& g, hipStream_t s) {
     const long T = (long)g.M * g.topk;
     const long tiles = (T + std::min<long>(T, g.E) * 64 + 127) / 128 * g.n_out / 512;  // as fp8_down_split counts
     if (g.n_out % 512 == 0 && tiles > 768) launch_fp8_prefill_cfg<STAGE, 8, 4, 128, 1, true>(g, 1, s);
-    else if (g.n_out % 256 == 0 && tiles > 128 && T > (g.k_in <= 2048 ? 64L : 160L) * g.E)
+    else if (g.n_out % 256 == 0 && tiles > 128 && T > (g.k_in <= 2048 ? 64L : 160L) * g.E &&
+             g.cap / 64 <= 65535)  // (token tiles lie along grid y)
         launch_fp8_prefill_cfg<STAGE, 8, 2, 64, 2, true, true>(g, 1, s);
     else if (g.n_out % 256 == 0 && tiles > 64) launch_fp8_prefill_cfg<STAGE, 8, 2, 128, 1, true>(g, 1, s);
     else launch_fp8_prefill_cfg<STAGE, 4, 2, 128, 2, true>(g, 1, s);
