@@ -463,8 +463,10 @@ wq_status dense_w8a16_gemm(const void* d_x, int M, int K, int N, const void* d_w
  * projection (dense_w4a16_gemm, dense_w8a16_gemm or any other), in place:
  *   y[m, n] += scales[a] * sum_r B_a[n, r] (sum_k A_a[r, k] x[m, k]),
  *   a = adapter_ids[m]; rows whose id is outside [0, adapters) stay as they are
- * Both sums are fp32, the inner one (the intermediate of R values per row) is
- * not rounded to 16 bits; y is rounded once more.  Each row takes its own
+ * Both sums are fp32; the inner one (the intermediate of R values per row) goes
+ * into the outer as two 16-bit parts, right to 2^-16 of each value in bf16, to
+ * 2^-22 of it and 2^-24 of the row's largest in fp16; y is rounded once more.
+ * Its last bit may differ with M (the K sum is split by it).  Each row takes its own
  * adapter's values only: infinities or NaN in another adapter or row do not
  * reach it.  Rows of one adapter next to each other (a prompt) share one read
  * of its weights; no order is asked for.
@@ -473,8 +475,8 @@ wq_status dense_w8a16_gemm(const void* d_x, int M, int K, int N, const void* d_w
  *   d_adapter_ids device int32 [M]
  *   d_a [adapters, R, K], d_b [adapters, N, R] act dtype: adapters of lower rank
  *     are padded with zeros in both; d_scales device float [adapters], NULL for ones
- *   d_workspace: dense_lora_workspace_bytes() bytes (every value read from it
- *     is written first, by the same call)
+ *   d_workspace: dense_lora_workspace_bytes() bytes, for these sizes (fewer rows
+ *     may take more: their K sum is split further); what it holds does not matter
  * Limits: K, N, R multiples of 8; M, K, N <= 2^24, R <= 256,
  * N * R < 2^31, y's row stride <= 2^25.  y must not overlap any input or the
  * workspace.  Calls sharing a workspace must be stream-ordered.

@@ -248,3 +248,17 @@ def test_ranks_17_to_32_in_large_batches(shape, ids, kind):
     check(*shape, ids, kind)
     if shape[1] <= 1024:
         check(*shape, ids, kind, integers=True, pad=8)
+
+
+@pytest.mark.parametrize("shape", [(40, 512, 264, 24, 5), (700, 136, 1288, 64, 9)])
+def test_what_the_workspace_held_does_not_matter(shape):
+    """NaN in it beforehand: rows without an adapter have no intermediate, the others' is written first."""
+    need_gpu()
+    M, K, N, R, L = shape
+    x, i, a, b, s, y = case(M, K, N, R, L, "rows", torch.bfloat16, 4)
+    i[::3] = -1
+    ref = wq.dense_lora_gemm(x, i, a, b, s, y.clone())
+    ws = torch.full((wq.dense_lora_workspace_bytes(M, K, N, R, L),), 0xFF, dtype=torch.uint8, device="cuda")
+    got = wq.dense_lora_gemm(x, i, a, b, s, y.clone(), workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(got, ref) and bool(torch.isfinite(got).all()) and torch.equal(got[::3], y[::3])
