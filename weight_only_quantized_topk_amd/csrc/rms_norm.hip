@@ -10,10 +10,12 @@
 // before it is squared, y is not rounded before it is quantised.  A row is
 // read once: its values stay in registers between the sum of squares, the
 // maximum and the store, a wave or a workgroup per row, of as many threads
-// as keep 8 or 16 values each (16 bytes an access).  HBM bound for many rows: 8192 x 5120 bf16 with residual, 16-bit and coded outputs moves
-// 378 MB in 73.2 us, 5.16 TB/s, what a large copy reaches.  One row of 4096: 3.3
-// us, the latency of two loads and two reductions; 333 rows of 1001 (single
-// 2-byte accesses) 4.7 us.
+// as keep 8 or 16 values each (16 bytes an access).  HBM bound for many rows: 8192
+// x 5120 bf16 with residual, 16-bit and coded outputs moves 378 MB in 73.5 us, 5.14
+// TB/s, what a large copy reaches.  One row of 4096: 2.8 us, the latency of two loads
+// and two reductions; 333 rows of 1001 (single 2-byte accesses) 4.9 us, 8192 of 5121 195.
+// Above 16384 values a row is read again for each step, by 2-byte accesses: 4096 rows
+// of 20480 520 us.
 #include "common.hpp"
 #include "launch.hpp"
 
