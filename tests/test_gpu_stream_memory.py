@@ -102,3 +102,45 @@ def test_dense_with_adapters_and_a_layer():
         assert stream_of(got[1][0]) == stream_of(got[1][1]) == side.cuda_stream
         for g, w in zip(got, want):
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_default_stream_by_its_handle():
+    """stream=0 with another stream current."""
+    need_gpu()
+    d = inputs(3, 65)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in run(d)]
+    torch.cuda.synchronize()
+    d = inputs(3, 65)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = run(d, 0)
+        torch.cuda.synchronize()
+        assert all(stream_of(t) == 0 for t in got)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_stream_forked_in_a_capture():
+    """Calls on a second stream of a captured graph, replayed with new inputs, eager work between."""
+    need_gpu()
+    d = inputs(4, 200)
+    y0, x0 = d["y"].clone(), d["x"].clone()
+    side = torch.cuda.Stream()
+    run(d)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        two = wq.rms_norm(d["r"], quant="row")
+        held = run(d, side.cuda_stream)
+        here.wait_stream(side)
+    for k in range(4):
+        d["x"].copy_(torch.roll(x0, k, 0))
+        d["y"].copy_(y0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got, got2 = [t.clone() for t in held], [t.clone() for t in two if t is not None]
+        d["y"].copy_(y0)
+        assert all(torch.equal(a, b) for a, b in zip(got, run(d)))
+        assert all(torch.equal(a, b) for a, b in zip(got2, [t for t in wq.rms_norm(d["r"], quant="row") if t is not None]))

@@ -48,9 +48,15 @@ def on(s):
         Book.current = was
 
 
+def external(handle):
+    """As torch's: for handle 0 (the default stream) it makes some other stream."""
+    return Stream(handle or 999)
+
+
 class FakeTorch:
     empty, empty_like = staticmethod(make(torch.empty)), staticmethod(make(torch.empty_like))
-    cuda = types.SimpleNamespace(stream=on, ExternalStream=Stream, current_stream=lambda: Stream(Book.current))
+    cuda = types.SimpleNamespace(stream=on, ExternalStream=external, default_stream=lambda: Stream(0),
+                                 current_stream=lambda: Stream(Book.current))
     _C = types.SimpleNamespace(_cuda_getDevice=lambda: 0, _cuda_getCurrentRawStream=lambda d: Book.current)
 
     def __getattr__(self, name):
@@ -115,6 +121,14 @@ def test_memory_of_the_calls_stream(calls, name):
         if t.data_ptr() in Book.made:
             assert (t.data_ptr(), HERE) in Book.kept
     assert all(s == HERE for _, s in Book.kept)
+
+
+@pytest.mark.parametrize("name", JOBS)
+def test_memory_of_the_default_stream(calls, name):
+    """Handle 0, with another stream current."""
+    JOBS[name](0)
+    assert Book.made and set(Book.made.values()) == {0}
+    assert all(a[-1] == 0 for _, a in calls)
 
 
 @pytest.mark.parametrize("name", JOBS)

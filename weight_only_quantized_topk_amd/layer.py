@@ -128,7 +128,8 @@ def choose_block_size(M: int, topk: int, E: int, bits: int = 8) -> int:
 
 class MoERunner:
     """The hot path for one batch shape with every buffer allocated up front, so
-    a call allocates nothing.  marks: optional 3 events recorded on the stream
+    a call allocates nothing (on the stream current then: a first call on another
+    one waits for it, as for any tensor).  marks: optional 3 events recorded on the stream
     after alignment, after GATE_UP and after DOWN (stage timing).  router: the
     scores, bias and groups to route with (its renormalize holds then; renormalize=False
     beside a router that renormalises is refused)."""

@@ -102,7 +102,8 @@ def _alloc(stream, make, *args, **kw):
     if stream is None or stream == _stream(None):
         return make(*args, **kw)
     torch = _torch()
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream)):
+    # (ExternalStream makes a new stream of handle 0, the default stream's)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()):
         return make(*args, **kw)
 
 
