@@ -158,6 +158,8 @@ wq_status moe_route_align(const float* d_logits, int M, int E, int topk, int ren
  *   weights: routed_scale * s_j, and with renormalize over the sum of the
  *     slots' s (the bias is not in them).
  * Scores, sums and quotients are double, weights are rounded once to float.
+ * The order of the softmax's sum goes by M: a row's c or weight can differ with
+ * its batch only where the double value lies on the border of two floats.
  *   d_logits        device [M, E], logits_dtype WQ_F32, WQ_F16 or WQ_BF16.
  *                   -inf is a score of 0; a row whose scores are all 0, or
  *                   whose slots' are, gets weights of 0.  A NaN is the last

@@ -128,11 +128,12 @@ def choose_block_size(M: int, topk: int, E: int, bits: int = 8) -> int:
 
 class MoERunner:
     """The hot path for one batch shape with every buffer allocated up front, so
-    a call allocates nothing (on the stream current then: a first call on another
-    one waits for it, as for any tensor).  marks: optional 3 events recorded on the stream
-    after alignment, after GATE_UP and after DOWN (stage timing).  router: the
-    scores, bias and groups to route with (its renormalize holds then; renormalize=False
-    beside a router that renormalises is refused)."""
+    a call allocates nothing (in the memory of the stream current then: a program
+    that calls it on another one orders that stream behind it, as for any tensor).
+    marks: optional 3 events recorded on the stream after alignment, after GATE_UP
+    and after DOWN (stage timing).  router: the scores, bias and groups to route
+    with (its renormalize holds then; renormalize=False beside a router that
+    renormalises is refused)."""
 
     def __init__(self, p: PackedMoE, M: int, topk: int, renormalize: bool = True, block_size: Optional[int] = None,
                  device="cuda", router: Optional[Router] = None):

@@ -4,6 +4,11 @@ Every function here only marshals arguments: torch tensors supply device
 memory and the current HIP stream, numpy arrays supply host memory for the
 offline packers.  All computation happens in the library's kernels (or, for
 the packers, in its host code).  The names follow include/wqmoe.h.
+
+stream: the raw handle of the HIP stream to run on (0: the default stream);
+None is torch's current one.  Nothing waits: inputs have to be ready on that
+stream, and a reader on another one waits for it.  Buffers that a call allocates
+are of that stream's memory.
 """
 from __future__ import annotations
 
