@@ -77,14 +77,14 @@ def _check(t, name: str, shape, dtypes, device=None, row_stride: bool = False):
                              % (name, " in its rows" if row_stride else "", list(t.stride())))
 
 
-def _holds(t, name: str, n: int, dtypes, device):
-    """A tensor argument of any shape is contiguous, has one of the types and at least n values."""
-    if t.numel() >= n and t.dtype in dtypes and t.is_contiguous() and t.device == device:
+def _holds(t, name: str, n: int, dtypes):
+    """A tensor argument of any shape is contiguous, has one of the types and at
+    least n values (its device the library checks)."""
+    if t.numel() >= n and t.dtype in dtypes and t.is_contiguous():
         return
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
-    raise ValueError("%s must hold %d values, contiguous on %s; got %s, strides %s, on %s"
-                     % (name, n, device, list(t.shape), list(t.stride()), t.device))
+    raise ValueError("%s must hold %d values, contiguous; got %s, strides %s" % (name, n, list(t.shape), list(t.stride())))
 
 
 def _int32(**sizes):
@@ -472,7 +472,7 @@ def moe_fp8_codes_gemm(stage, codes, row_scales, M, topk, E, n_out, k_in, w_pack
     n_out]) stage of moe_fp8_w8a8_gemm on E4M3 codes [M, k_in] (rms_norm's),
     with row_scales [M] float32 or, for None, in_scale for every row.  w_packed
     (E * n_out * k_in codes), scales (E * n_out float32) and the routing arrays
-    of moe_align are checked for their size, type and device."""
+    of moe_align are checked for their size and type."""
     torch = _torch()
     _int32(M=M, topk=topk, E=E, n_out=n_out, k_in=k_in, block_size=block_size)
     f8 = (torch.uint8, torch.float8_e4m3fn)
@@ -484,11 +484,11 @@ def moe_fp8_codes_gemm(stage, codes, row_scales, M, topk, E, n_out, k_in, w_pack
     elif stage == WQ_STAGE_RAW:
         _check(out, "out", (M * topk, n_out), (torch.float32,), codes.device)
     i32 = (torch.int32,)
-    _holds(w_packed, "w_packed", E * n_out * k_in, f8, codes.device)
-    _holds(scales, "scales", E * n_out, (torch.float32,), codes.device)
-    _holds(sorted_token_ids, "sorted_token_ids", capacity, i32, codes.device)
-    _holds(expert_ids, "expert_ids", capacity // block_size if block_size > 0 else 0, i32, codes.device)
-    _holds(num_tokens_post_padded, "num_tokens_post_padded", 1, i32, codes.device)
+    _holds(w_packed, "w_packed", E * n_out * k_in, f8)
+    _holds(scales, "scales", E * n_out, (torch.float32,))
+    _holds(sorted_token_ids, "sorted_token_ids", capacity, i32)
+    _holds(expert_ids, "expert_ids", capacity // block_size if block_size > 0 else 0, i32)
+    _holds(num_tokens_post_padded, "num_tokens_post_padded", 1, i32)
     d = _desc(stage, codes, M, topk, E, n_out, k_in, w_packed, scales, -1, None, sorted_token_ids, expert_ids,
               num_tokens_post_padded, capacity, block_size, None, out, None, WQ_BF16)
     check(load().moe_fp8_codes_gemm(C.byref(d), _ptr(row_scales), in_scale, out_scale, _stream(stream)),
