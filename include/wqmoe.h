@@ -19,6 +19,9 @@
  *   moe_route_grouped_align  the same with the token sort (one kernel for small batches)
  *   wq_rms_norm           residual addition + RMS norm, 16-bit and/or E4M3 output with scales
  *   dense_lora_gemm       low-rank adapters of many requests beside a dense projection
+ *   wq_kv_cache_write     new tokens' keys and values into a paged cache, 16-bit or E4M3
+ *   wq_kv_cache_read      rows of the cache back as 16-bit values
+ *   wq_paged_attention    attention of one new token a sequence over the cache
  * Beside them: dense_w4a16_gemm / dense_w8a16_gemm (one quantized weight
  * matrix, the same kernels with one expert) and wq_quantize_w8 (the int8
  * weights and scales from a 16-bit checkpoint on the device, at load time).
@@ -68,6 +71,7 @@ typedef int wq_status;
 #define WQ_F16 0
 #define WQ_BF16 1
 #define WQ_F32 2 /* router logits only */
+#define WQ_E4M3 3 /* key-value caches only */
 
 /* Stages of the grouped GEMM (moe_w4a16_gemm / moe_w8a16_gemm). */
 #define WQ_STAGE_GATE_UP 0 /* H = silu(A W_gate^T) * (A W_up^T), rows in sorted order       */
@@ -488,6 +492,90 @@ wq_status dense_lora_gemm(const void* d_x, int64_t x_stride, int M, int K, int N
                           const int32_t* d_adapter_ids, const void* d_a, const void* d_b, const float* d_scales,
                           void* d_y, int64_t y_stride, int act_dtype, void* d_workspace, size_t workspace_bytes,
                           void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Paged key-value cache and attention of one token over it                  */
+/* ------------------------------------------------------------------------ */
+/*
+ * The cache: pages of page_size tokens, the rows (one token, one head) of a
+ * head in a page next to each other.
+ *   d_k, d_v    device [pages, kv_heads, page_size, head_dim]: act dtype
+ *               values, or E4M3 codes (dtype WQ_E4M3)
+ *   d_k_scales, d_v_scales  device float [pages, kv_heads, page_size], a scale
+ *               for each row of codes; both NULL: k_scale and v_scale are those
+ *               of every row (finite, > 0)
+ * Limits: page_size a multiple of 16, at most 4096; head_dim a multiple of 16,
+ * at most 256; pages * page_size < 2^31; kv_heads <= 65535.  A 16-bit cache is
+ * of the call's act dtype.
+ */
+typedef struct wq_kv_cache {
+    size_t struct_size;          /* = sizeof(wq_kv_cache) */
+    void* d_k;
+    void* d_v;
+    float* d_k_scales;
+    float* d_v_scales;
+    float k_scale, v_scale;
+    int dtype;                   /* WQ_F16, WQ_BF16 or WQ_E4M3 */
+    int pages, kv_heads, page_size, head_dim;
+} wq_kv_cache;
+
+/*
+ * wq_kv_cache_write: token t's rows into slot d_slots[t] = page * page_size +
+ * position; a slot outside [0, pages * page_size) (-1, a padding token) writes
+ * nothing, and the rest of the cache stays as it was.  Codes as wq_rms_norm's:
+ *   row scales  c = max(max|v| / 448, 2^-100), written; code of v * (1 / c)
+ *   k_scale ..  code of v / k_scale (v / v_scale for the values)
+ * clamped to +-448, ties to even; a NaN's code is one, the row scale skips it.
+ * The slots of a call differ: of two tokens with one slot either's values may
+ * be kept, not all of the same one.
+ * wq_kv_cache_read: the rows of d_slots[t] back, code * scale rounded once to
+ * the act dtype; zeros for a slot outside the cache.  A slot may be read twice.
+ *   d_k, d_v [T, kv_heads, head_dim] act dtype, row strides in elements (>=
+ *     kv_heads * head_dim, multiples of 8: column ranges of one projection's output)
+ *   d_slots device int64 [T]
+ * The cache must not overlap the rows or slots, nor the arrays written one
+ * another.  Limits: T <= 2^24.  T = 0 launches nothing.
+ */
+wq_status wq_kv_cache_write(const wq_kv_cache* c, const void* d_k, int64_t k_stride, const void* d_v,
+                            int64_t v_stride, const int64_t* d_slots, int T, int act_dtype, void* stream);
+wq_status wq_kv_cache_read(const wq_kv_cache* c, const int64_t* d_slots, int T, void* d_k, int64_t k_stride,
+                           void* d_v, int64_t v_stride, int act_dtype, void* stream);
+
+/*
+ * wq_paged_attention: one query token of each of B sequences over its tokens
+ * [max(0, len - window), len) in the cache (window 0: all), len =
+ * d_lengths[b].  Query head h reads kv head h / (heads / kv_heads):
+ *   s_t = scale * q . k_t;  out = sum_t exp(s_t) v_t / sum_t exp(s_t);
+ *   lse = log sum_t exp(s_t)
+ * Scores and sums are float32, the weights of the values two 16-bit parts
+ * (right to 2^-16 in bf16 and over E4M3 values, 2^-22 in fp16); out is rounded once.
+ *   d_q, d_out [B, heads, head_dim] act dtype, row strides in elements (>=
+ *     heads * head_dim, multiples of 8)
+ *   d_block_table device int32 [B, table_width]: the page of each page_size
+ *     tokens; entries past a sequence's end are not read.  An entry outside
+ *     [0, pages) holds no tokens
+ *   d_lengths device int32 [B]; below 0 is 0, above table_width * page_size
+ *     that.  A sequence without tokens (a padding row) gives zeros and an lse
+ *     of -inf, as one whose weights are all 0 does
+ *   d_lse device float [B, heads] or NULL
+ *   d_workspace: wq_paged_attention_workspace_bytes() bytes; 0 (NULL allowed)
+ *     where no sequence can be long enough to be split.  What it holds does not matter
+ * Rows of the cache outside a sequence do not reach its output, whatever they
+ * hold.  A NaN in its own keys or query is one in the heads that read it, and
+ * an infinite or NaN value an infinity or NaN in its channel.  The split of a sequence
+ * goes by all of the batch's lengths: its last bits may differ with the batch,
+ * and are the same for the same call.
+ * Limits: heads a multiple of kv_heads; B, heads <= 65535; table_width *
+ * page_size <= 2^30; table_width * (page_size / 16)^2 < 2^32; B * table_width *
+ * page_size < 2^35.  out, lse and the workspace must not overlap anything else
+ * (rows of out may lie in the gaps of q's).  B = 0 launches nothing.
+ */
+size_t wq_paged_attention_workspace_bytes(int B, int heads, int kv_heads, int head_dim, int page_size, int table_width,
+                                          int window);
+wq_status wq_paged_attention(const wq_kv_cache* c, const void* d_q, int64_t q_stride, int B, int heads,
+                             const int32_t* d_block_table, int table_width, const int32_t* d_lengths, float scale,
+                             int window, void* d_out, int64_t out_stride, float* d_lse, int act_dtype,
+                             void* d_workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* ExpertsInt8 quantization at load time                                     */

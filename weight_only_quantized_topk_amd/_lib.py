@@ -10,7 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libwqmoe.so")
 
 WQ_OK, WQ_ERR_INVALID, WQ_ERR_UNSUPPORTED, WQ_ERR_DEVICE, WQ_ERR_HIP = 0, 1, 2, 3, 4
-WQ_F16, WQ_BF16, WQ_F32 = 0, 1, 2
+WQ_F16, WQ_BF16, WQ_F32, WQ_E4M3 = 0, 1, 2, 3
 WQ_SCORE_SOFTMAX, WQ_SCORE_SIGMOID = 0, 1
 WQ_GROUP_MAX, WQ_GROUP_TOP2 = 0, 1
 WQ_STAGE_GATE_UP, WQ_STAGE_DOWN, WQ_STAGE_RAW = 0, 1, 2
@@ -25,6 +25,7 @@ EXPORTS = (
     "sparse24_w4a16_gemm", "sparse24_w8a16_gemm", "wq_quantize_w8",
     "dense_gemm_workspace_bytes", "dense_w4a16_gemm", "dense_w8a16_gemm",
     "dense_lora_workspace_bytes", "dense_lora_gemm",
+    "wq_kv_cache_write", "wq_kv_cache_read", "wq_paged_attention_workspace_bytes", "wq_paged_attention",
     "wq_pack_w4_bytes", "wq_pack_w8_bytes", "wq_pack_w4", "wq_pack_w8",
     "wq_pack_sparse24_vals_bytes", "wq_pack_sparse24_meta_bytes", "wq_pack_sparse24",
     "moe_fp8_gemm_workspace_bytes", "moe_fp8_w8a8_gemm", "moe_fp8_codes_gemm", "wq_pack_fp8_bytes", "wq_pack_fp8",
@@ -51,6 +52,17 @@ class WqMoeGemmDesc(C.Structure):
         ("d_out", C.c_void_p),
         ("d_workspace", C.c_void_p),
         ("workspace_bytes", C.c_size_t),
+    ]
+
+
+class WqKvCache(C.Structure):
+    _fields_ = [
+        ("struct_size", C.c_size_t),
+        ("d_k", C.c_void_p), ("d_v", C.c_void_p),
+        ("d_k_scales", C.c_void_p), ("d_v_scales", C.c_void_p),
+        ("k_scale", C.c_float), ("v_scale", C.c_float),
+        ("dtype", C.c_int),
+        ("pages", C.c_int), ("kv_heads", C.c_int), ("page_size", C.c_int), ("head_dim", C.c_int),
     ]
 
 
@@ -108,6 +120,12 @@ def load():
     L.dense_lora_workspace_bytes.argtypes = [i, i, i, i, i]
     L.dense_lora_workspace_bytes.restype = sz
     L.dense_lora_gemm.argtypes = [p, i64, i, i, i, i, i, p, p, p, p, p, i64, i, p, sz, p]
+    kvc = C.POINTER(WqKvCache)
+    L.wq_kv_cache_write.argtypes = [kvc, p, i64, p, i64, p, i, i, p]
+    L.wq_kv_cache_read.argtypes = [kvc, p, i, p, i64, p, i64, i, p]
+    L.wq_paged_attention_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+    L.wq_paged_attention_workspace_bytes.restype = sz
+    L.wq_paged_attention.argtypes = [kvc, p, i64, i, i, p, i, p, f, i, p, i64, p, i, p, sz, p]
     L.wq_pack_w4_bytes.argtypes = [i, i, i]
     L.wq_pack_w4_bytes.restype = sz
     L.wq_pack_w8_bytes.argtypes = [i, i, i]
@@ -130,7 +148,8 @@ def load():
               "moe_route_grouped_align", "wq_rms_norm", "moe_w4a16_gemm", "moe_w8a16_gemm",
               "moe_w8a16_gemm_noalloc", "sparse24_w4a16_gemm",
               "sparse24_w8a16_gemm",
-              "wq_quantize_w8", "dense_w4a16_gemm", "dense_w8a16_gemm", "dense_lora_gemm", "wq_pack_w4",
+              "wq_quantize_w8", "dense_w4a16_gemm", "dense_w8a16_gemm", "dense_lora_gemm", "wq_kv_cache_write",
+              "wq_kv_cache_read", "wq_paged_attention", "wq_pack_w4",
               "wq_pack_w8", "wq_pack_sparse24", "moe_fp8_w8a8_gemm", "moe_fp8_codes_gemm", "wq_pack_fp8"):
         getattr(L, fn).restype = i
     _lib = L

@@ -22,6 +22,7 @@
 #include <vector>
 
 #include "../../include/wqmoe.h"
+#include "kv_common.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -1201,6 +1202,278 @@ wq_status dense_lora_gemm(const void* d_x, int64_t x_stride, int M, int K, int N
         return after_launch(who);
     } catch (...) {
         return fail(WQ_ERR_HIP, "dense_lora_gemm: unexpected exception");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// paged key-value cache
+// ---------------------------------------------------------------------------
+namespace {
+struct Span8 {  // a contiguous array
+    const void* p;
+    int64_t bytes;
+    const char* name;
+};
+
+struct KvCacheView {
+    int mode;
+    Span8 arrays[4];  // k, v, k_scales, v_scales (the last two NULL without row scales)
+};
+
+// the descriptor's checks that need no device
+wq_status kv_cache_args(const wq_kv_cache* c, int act_dtype, KvCacheView* out, const char* who) {
+    WQ_REQUIRE(c != nullptr, WQ_ERR_INVALID, "%s: cache is NULL", who);
+    WQ_REQUIRE(c->struct_size == sizeof(wq_kv_cache), WQ_ERR_INVALID, "%s: cache struct_size %zu, expected %zu", who,
+               c->struct_size, sizeof(wq_kv_cache));
+    WQ_REQUIRE(act_dtype == WQ_F16 || act_dtype == WQ_BF16, WQ_ERR_INVALID, "%s: bad act dtype", who);
+    WQ_REQUIRE(c->dtype == WQ_E4M3 || c->dtype == act_dtype, WQ_ERR_INVALID,
+               "%s: cache dtype %d: the act dtype or WQ_E4M3", who, c->dtype);
+    WQ_REQUIRE(c->pages >= 1 && c->kv_heads >= 1 && c->page_size >= 1 && c->head_dim >= 1, WQ_ERR_INVALID,
+               "%s: bad cache sizes: pages %d kv_heads %d page_size %d head_dim %d", who, c->pages, c->kv_heads,
+               c->page_size, c->head_dim);
+    WQ_REQUIRE(c->page_size % wq::KV_TOKENS == 0 && c->page_size <= 4096, WQ_ERR_UNSUPPORTED,
+               "%s: page_size %d: a multiple of 16, at most 4096", who, c->page_size);
+    WQ_REQUIRE(c->head_dim % 16 == 0 && c->head_dim <= wq::KV_MAX_DIM, WQ_ERR_UNSUPPORTED,
+               "%s: head_dim %d: a multiple of 16, at most 256", who, c->head_dim);
+    WQ_REQUIRE((int64_t)c->pages * c->page_size <= INT32_MAX && c->kv_heads <= 65535, WQ_ERR_UNSUPPORTED,
+               "%s: pages * page_size >= 2^31, or more than 65535 kv_heads", who);
+    const bool e4m3 = c->dtype == WQ_E4M3, rows = e4m3 && (c->d_k_scales || c->d_v_scales);
+    WQ_REQUIRE(e4m3 || (!c->d_k_scales && !c->d_v_scales), WQ_ERR_INVALID, "%s: scales of a 16-bit cache", who);
+    WQ_REQUIRE(!rows || (c->d_k_scales && c->d_v_scales), WQ_ERR_INVALID,
+               "%s: row scales for the keys and the values, or for neither", who);
+    WQ_REQUIRE(!e4m3 || rows || (std::isfinite(c->k_scale) && c->k_scale > 0.0f && std::isfinite(c->v_scale) &&
+                                 c->v_scale > 0.0f),
+               WQ_ERR_INVALID, "%s: k_scale and v_scale must be finite and > 0", who);
+    const int64_t n = (int64_t)c->pages * c->page_size * c->kv_heads;  // rows: < 2^47
+    const int64_t bytes = n * c->head_dim * (e4m3 ? 1 : 2);
+    out->mode = !e4m3 ? wq::KV_16 : rows ? wq::KV_E4M3_ROW : wq::KV_E4M3_STATIC;
+    out->arrays[0] = {c->d_k, bytes, "cache k"};
+    out->arrays[1] = {c->d_v, bytes, "cache v"};
+    out->arrays[2] = {rows ? c->d_k_scales : nullptr, n * 4, "cache k_scales"};
+    out->arrays[3] = {rows ? c->d_v_scales : nullptr, n * 4, "cache v_scales"};
+    for (int i = 0; i < (rows ? 4 : 2); ++i) WQ_TRY(check_ptr(out->arrays[i].p, out->arrays[i].name));
+    return WQ_OK;
+}
+
+bool spans_overlap(const Span8& a, const Span8& b) {
+    return a.p && b.p && rows_overlap(a.p, 0, a.bytes, b.p, 0, b.bytes, 1);
+}
+
+// no array of a shares memory with one of b
+wq_status apart(const Span8* a, int na, const Span8* b, int nb, const char* who) {
+    for (int i = 0; i < na; ++i)
+        for (int j = 0; j < nb; ++j)
+            WQ_REQUIRE(!spans_overlap(a[i], b[j]), WQ_ERR_INVALID, "%s: %s overlaps %s", who, a[i].name, b[j].name);
+    return WQ_OK;
+}
+
+wq_status kv_rows(const wq_kv_cache* c, void* d_k, int64_t k_stride, void* d_v, int64_t v_stride,
+                  const int64_t* d_slots, int T, int act_dtype, bool write, void* stream, const char* who) {
+    KvCacheView view;
+    WQ_REQUIRE(T >= 0, WQ_ERR_INVALID, "%s: T = %d", who, T);
+    WQ_REQUIRE(T <= MAX_PAIRS, WQ_ERR_UNSUPPORTED, "%s: T = %d > 2^24", who, T);
+    WQ_TRY(kv_cache_args(c, act_dtype, &view, who));
+    if (T == 0) return ok();  // (empty arrays may have no address)
+    const int64_t n = (int64_t)c->kv_heads * c->head_dim, most = INT64_MAX / 4 / T;
+    WQ_REQUIRE(k_stride >= n && k_stride <= most && v_stride >= n && v_stride <= most, WQ_ERR_INVALID,
+               "%s: row strides %lld, %lld (rows of %lld)", who, (long long)k_stride, (long long)v_stride,
+               (long long)n);
+    WQ_REQUIRE(k_stride % 8 == 0 && v_stride % 8 == 0, WQ_ERR_UNSUPPORTED, "%s: row strides must be multiples of 8", who);
+    WQ_TRY(check_ptr(d_k, "k"));
+    WQ_TRY(check_ptr(d_v, "v"));
+    WQ_TRY(check_ptr(d_slots, "slots"));
+    const Span8 rows[3] = {{d_k, ((int64_t)(T - 1) * k_stride + n) * 2, "k"},
+                           {d_v, ((int64_t)(T - 1) * v_stride + n) * 2, "v"},
+                           {d_slots, (int64_t)T * 8, "slots"}};
+    WQ_TRY(apart(view.arrays, 4, rows, 3, who));
+    if (write) {
+        for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < i; ++j)
+                WQ_REQUIRE(!spans_overlap(view.arrays[i], view.arrays[j]), WQ_ERR_INVALID, "%s: %s overlaps %s", who,
+                           view.arrays[i].name, view.arrays[j].name);
+    } else {  // (the rows of k and v may lie in each other's gaps)
+        WQ_REQUIRE(!rows_overlap(d_k, k_stride * 2, n * 2, d_v, v_stride * 2, n * 2, T), WQ_ERR_INVALID,
+                   "%s: k overlaps v", who);
+        WQ_REQUIRE(!spans_overlap(rows[0], rows[2]) && !spans_overlap(rows[1], rows[2]), WQ_ERR_INVALID,
+                   "%s: k or v overlaps slots", who);
+    }
+    int cur = -1;
+    WQ_TRY(current_device(&cur));
+    for (const Span8& a : view.arrays)
+        if (a.p) WQ_TRY(check_dev(a.p, a.name, cur));
+    for (const Span8& a : rows) WQ_TRY(check_dev(a.p, a.name, cur));
+    wq::KvRowsArgs g{};
+    g.k = static_cast<uint8_t*>(c->d_k);
+    g.v = static_cast<uint8_t*>(c->d_v);
+    g.ks = c->d_k_scales;
+    g.vs = c->d_v_scales;
+    g.k_scale = c->k_scale;
+    g.v_scale = c->v_scale;
+    g.k16 = static_cast<uint16_t*>(d_k);
+    g.v16 = static_cast<uint16_t*>(d_v);
+    g.slots = d_slots;
+    g.k_stride = k_stride;
+    g.v_stride = v_stride;
+    g.T = T;
+    g.pages = c->pages;
+    g.kv_heads = c->kv_heads;
+    g.page_size = c->page_size;
+    g.D = c->head_dim;
+    g.mode = view.mode;
+    wq::launch_kv_rows(g, write, act_dtype == WQ_BF16, (hipStream_t)stream);
+    return after_launch(who);
+}
+}  // namespace
+
+wq_status wq_kv_cache_write(const wq_kv_cache* c, const void* d_k, int64_t k_stride, const void* d_v,
+                            int64_t v_stride, const int64_t* d_slots, int T, int act_dtype, void* stream) {
+    try {
+        return kv_rows(c, const_cast<void*>(d_k), k_stride, const_cast<void*>(d_v), v_stride, d_slots, T, act_dtype,
+                       true, stream, "wq_kv_cache_write");
+    } catch (...) {
+        return fail(WQ_ERR_HIP, "wq_kv_cache_write: unexpected exception");
+    }
+}
+
+wq_status wq_kv_cache_read(const wq_kv_cache* c, const int64_t* d_slots, int T, void* d_k, int64_t k_stride,
+                           void* d_v, int64_t v_stride, int act_dtype, void* stream) {
+    try {
+        return kv_rows(c, d_k, k_stride, d_v, v_stride, d_slots, T, act_dtype, false, stream, "wq_kv_cache_read");
+    } catch (...) {
+        return fail(WQ_ERR_HIP, "wq_kv_cache_read: unexpected exception");
+    }
+}
+
+// ---------------------------------------------------------------------------
+static const char* attn_sizes(int B, int heads, int kv_heads, int head_dim, int page_size, int table_width, int window) {
+    if (B < 0 || heads <= 0 || kv_heads <= 0 || head_dim <= 0 || page_size <= 0 || table_width <= 0 || window < 0)
+        return "sizes must be positive (B, window >= 0)";
+    if (heads % kv_heads) return "heads must be a multiple of kv_heads";
+    return nullptr;
+}
+static const char* attn_limits(int B, int heads, int kv_heads, int page_size, int table_width) {
+    const int64_t tokens = (int64_t)table_width * page_size, tiles = tokens / 32 + 2, p16 = page_size / 16;
+    if (B > 65535) return "more than 65535 sequences";
+    if (heads > 65535) return "more than 65535 heads";
+    if (tokens > (1 << 30)) return "table_width * page_size > 2^30";
+    // a token's page from its index by one multiplication, exact below this
+    if ((int64_t)table_width * p16 * p16 >= ((int64_t)1 << 32)) return "table_width * (page_size / 16)^2 >= 2^32";
+    if (tiles * B > INT32_MAX / 2) return "sequences * table_width * page_size >= 2^35";
+    return nullptr;
+}
+struct AttnLayout {
+    int splits;
+    size_t off_ml, off_at, total;
+};
+static AttnLayout attn_layout(int B, int heads, int kv_heads, int head_dim, int page_size, int table_width, int window) {
+    int64_t most = (int64_t)table_width * page_size;
+    if (window > 0) most = std::min<int64_t>(most, (int64_t)window + wq::KV_TOKENS - 1);  // it begins anywhere in 16
+    AttnLayout L{};
+    L.splits = wq::paged_attn_splits(B, heads, kv_heads, most);
+    if (L.splits == 0) return L;
+    const size_t n = (size_t)(B + L.splits) * heads;
+    L.off_ml = round256(n * head_dim * sizeof(float));
+    L.off_at = L.off_ml + round256(n * 2 * sizeof(float));
+    L.total = L.off_at + round256((size_t)B * 2 * sizeof(int32_t));
+    return L;
+}
+
+size_t wq_paged_attention_workspace_bytes(int B, int heads, int kv_heads, int head_dim, int page_size, int table_width,
+                                          int window) {
+    if (B == 0 || attn_sizes(B, heads, kv_heads, head_dim, page_size, table_width, window) ||
+        attn_limits(B, heads, kv_heads, page_size, table_width))
+        return 0;
+    return attn_layout(B, heads, kv_heads, head_dim, page_size, table_width, window).total;
+}
+
+wq_status wq_paged_attention(const wq_kv_cache* c, const void* d_q, int64_t q_stride, int B, int heads,
+                             const int32_t* d_block_table, int table_width, const int32_t* d_lengths, float scale,
+                             int window, void* d_out, int64_t out_stride, float* d_lse, int act_dtype,
+                             void* d_workspace, size_t workspace_bytes, void* stream) {
+    try {
+        const char* who = "wq_paged_attention";
+        KvCacheView view;
+        WQ_TRY(kv_cache_args(c, act_dtype, &view, who));
+        const char* bad = attn_sizes(B, heads, c->kv_heads, c->head_dim, c->page_size, table_width, window);
+        WQ_REQUIRE(!bad, WQ_ERR_INVALID, "%s: %s", who, bad);
+        bad = attn_limits(B, heads, c->kv_heads, c->page_size, table_width);
+        WQ_REQUIRE(!bad, WQ_ERR_UNSUPPORTED, "%s: %s", who, bad);
+        WQ_REQUIRE(std::isfinite(scale), WQ_ERR_INVALID, "%s: scale must be finite", who);
+        const AttnLayout L =
+            attn_layout(B, heads, c->kv_heads, c->head_dim, c->page_size, table_width, window);
+        if (B == 0) return ok();  // (empty arrays may have no address)
+        WQ_REQUIRE(workspace_bytes >= L.total, WQ_ERR_INVALID, "%s: workspace %zu < required %zu", who,
+                   workspace_bytes, L.total);
+        const int64_t n = (int64_t)heads * c->head_dim, most = INT64_MAX / 4 / B;
+        WQ_REQUIRE(q_stride >= n && q_stride <= most && out_stride >= n && out_stride <= most, WQ_ERR_INVALID,
+                   "%s: row strides %lld, %lld (rows of %lld)", who, (long long)q_stride, (long long)out_stride,
+                   (long long)n);
+        WQ_REQUIRE(q_stride % 8 == 0 && out_stride % 8 == 0, WQ_ERR_UNSUPPORTED,
+                   "%s: row strides must be multiples of 8", who);
+        const Span8 in[3] = {{d_q, ((int64_t)(B - 1) * q_stride + n) * 2, "q"},
+                             {d_block_table, (int64_t)B * table_width * 4, "block_table"},
+                             {d_lengths, (int64_t)B * 4, "lengths"}};
+        const Span8 out[3] = {{d_out, ((int64_t)(B - 1) * out_stride + n) * 2, "out"},
+                              {d_lse, (int64_t)B * heads * 4, "lse"},
+                              {L.total ? d_workspace : nullptr, (int64_t)L.total, "workspace"}};
+        for (const Span8& a : in) WQ_TRY(check_ptr(a.p, a.name));
+        WQ_TRY(check_ptr(d_out, "out"));
+        if (d_lse) WQ_TRY(check_ptr(d_lse, "lse"));
+        if (L.total) WQ_TRY(check_ptr(d_workspace, "workspace"));
+        // rows of out may lie between q's (two column ranges of one array)
+        WQ_REQUIRE(!rows_overlap(d_q, q_stride * 2, n * 2, d_out, out_stride * 2, n * 2, B), WQ_ERR_INVALID,
+                   "%s: out overlaps q", who);
+        for (int o = 0; o < 3; ++o) {
+            for (int i = o == 0 ? 1 : 0; i < 3; ++i)
+                WQ_REQUIRE(!spans_overlap(out[o], in[i]), WQ_ERR_INVALID, "%s: %s overlaps %s", who, out[o].name,
+                           in[i].name);
+            for (int i = 0; i < o; ++i)
+                WQ_REQUIRE(!spans_overlap(out[o], out[i]), WQ_ERR_INVALID, "%s: %s overlaps %s", who, out[o].name,
+                           out[i].name);
+        }
+        WQ_TRY(apart(out, 3, view.arrays, 4, who));
+        int cur = -1;
+        WQ_TRY(current_device(&cur));
+        for (const Span8& a : view.arrays)
+            if (a.p) WQ_TRY(check_dev(a.p, a.name, cur));
+        for (const Span8& a : in) WQ_TRY(check_dev(a.p, a.name, cur));
+        for (const Span8& a : out)
+            if (a.p) WQ_TRY(check_dev(a.p, a.name, cur));
+        const bool fixed = view.mode == wq::KV_E4M3_STATIC;
+        uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+        wq::PagedAttnArgs g{};
+        g.k = static_cast<const uint8_t*>(c->d_k);
+        g.v = static_cast<const uint8_t*>(c->d_v);
+        g.ks = c->d_k_scales;
+        g.vs = c->d_v_scales;
+        g.q = static_cast<const uint16_t*>(d_q);
+        g.table = d_block_table;
+        g.lengths = d_lengths;
+        g.out = static_cast<uint16_t*>(d_out);
+        g.lse = d_lse;
+        if (L.splits) {
+            g.part_o = reinterpret_cast<float*>(ws);
+            g.part_ml = reinterpret_cast<float*>(ws + L.off_ml);
+            g.part_at = reinterpret_cast<int32_t*>(ws + L.off_at);
+        }
+        g.q_stride = q_stride;
+        g.out_stride = out_stride;
+        g.qk_scale = (float)((double)scale * (fixed ? (double)c->k_scale : 1.0) * 1.4426950408889634);
+        g.v_scale = fixed ? c->v_scale : 1.0f;
+        g.B = B;
+        g.heads = heads;
+        g.kv_heads = c->kv_heads;
+        g.D = c->head_dim;
+        g.pages = c->pages;
+        g.page_size = c->page_size;
+        g.width = table_width;
+        g.window = window;
+        g.mode = view.mode;
+        g.splits = L.splits;
+        wq::launch_paged_attention(g, act_dtype == WQ_BF16, (hipStream_t)stream);
+        return after_launch(who);
+    } catch (...) {
+        return fail(WQ_ERR_HIP, "wq_paged_attention: unexpected exception");
     }
 }
 

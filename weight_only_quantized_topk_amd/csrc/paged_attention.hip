@@ -1,0 +1,508 @@
+// paged_attention.hip -- attention of one new token a sequence over a paged
+// key-value cache.
+//
+//   s_t = scale * q . k_t,  p_t = exp(s_t - max s),  out = sum p_t v_t / sum p_t,
+//   lse = max s + log sum p_t
+//
+// over the sequence's tokens (the last `window` of them), for each query head
+// with the keys and values of its group's head; k_t, v_t 16-bit rows or E4M3
+// codes times their row's scale.  A row of the cache takes part in 2 products
+// of 2 operations a value for each of the group's G heads, so at most 2 G
+// operations a byte (4 G for codes): HBM bound.
+//
+// The cache is read once, straight to registers.  A wave takes tiles of 32
+// tokens; the group's heads (up to 16 at a time) are the 16 columns of
+// v_mfma_f32_16x16x32:
+//   S^T [token, head] = K Q^T: lane l holds 8 channels of token l % 16 as they lie
+//       in memory, the A operand;
+//   O^T [channel, head] += V^T P^T: S^T comes out with head l % 16 and tokens
+//       4 (l / 16) + i of each half in lane l, and as the order of the tokens in
+//       a product is free, that is the B operand as it stands.  Lane l loads
+//       VEC channels from VEC (l % 16) of the same 8 tokens, and the A operand of
+//       channel e of each is 4 byte permutations of its own registers.
+// No value crosses lanes but the running maximum, and nothing goes through LDS
+// until the waves' results are joined.  P is 16-bit in two parts (value, and
+// what that rounding left out), each multiplied by the same V operand: right to 2^-16
+// (bf16) or 2^-22 (fp16) of itself; with one part its rounding alone would be as
+// large as the output's.  Under E4M3 values P carries the row's scale, in bf16 for its range.
+// Scores, statistics and sums are float32.  The maximum is raised only
+// when a score passes it by 2^8, so p is up to 2^8 and the accumulators are
+// seldom rescaled.
+//
+// Split over the length: every workgroup reads the batch's lengths and finds
+// from them alone the same cut: the batch's tiles over the grid's pieces, at least
+// min_tiles a piece, equal pieces within a sequence, so one long sequence among short ones is
+// shared out.  The first pieces of all sequences are numbered in order; a
+// sequence in one piece is written at once, the pieces of others as (O, max, sum) in float32 to the
+// workspace, joined in ascending order by a second kernel.  No atomics: the same inputs
+// and grid give the same bits.
+#include "common.hpp"
+#include "kv_common.hpp"
+#include "launch.hpp"
+
+#include <algorithm>
+
+namespace wq {
+
+namespace {
+
+constexpr int TILE = 32;           // tokens of a wave's step
+constexpr float M_NONE = -3.4028234e38f;  // the running maximum before any score
+constexpr float M_SLACK = 8.0f;    // scores may pass it by this much (exponents of 2)
+constexpr float LN2 = 0.693147180559945309f;
+
+// the sequence's tokens [lo, len) and its tiles of 32, the first beginning at
+// lo rounded down to half a tile
+struct Span {
+    int lo, len, begin, tiles;
+};
+__device__ __forceinline__ Span span_of(const PagedAttnArgs& g, int len) {
+    Span s;
+    const int64_t most = (int64_t)g.width * g.page_size;
+    s.len = (int)min((int64_t)max(len, 0), most);
+    s.lo = g.window > 0 ? max(0, s.len - g.window) : 0;
+    s.begin = s.lo & ~(KV_TOKENS - 1);
+    s.tiles = (int)(((int64_t)s.len - s.begin + TILE - 1) / TILE);
+    return s;
+}
+
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ int dpp_add(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROW_MASK, 0xF, false);
+}
+// inclusive sums over the lanes of a wave: within rows of 16 lanes, then the
+// rows' last lanes onto the rows behind
+__device__ __forceinline__ int wave_scan(int v) {
+    v = dpp_add<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    v = dpp_add<0x118, 0xF>(v);
+    v = dpp_add<0x142, 0xA>(v);  // row_bcast 15
+    v = dpp_add<0x143, 0xC>(v);  // row_bcast 31
+    return v;
+}
+
+// piece x of the batch: sequence b, its piece `at` of n (n = 0: x is past the last)
+struct Piece {
+    int b, at, n;
+};
+__device__ __forceinline__ Piece piece_of(const PagedAttnArgs& g, int x) {
+    if (g.splits == 0) return Piece{x, 0, 1};
+    const int lane = threadIdx.x & 63;
+    const int each = (g.B + 63) / 64;  // consecutive sequences of a lane
+    const int b0 = lane * each, b1 = min(b0 + each, g.B);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += span_of(g, g.lengths[b]).tiles;
+    const int total = __builtin_amdgcn_readlane(wave_scan(sum), 63);
+    // sum over the batch of max(1, ceil(tiles / cut)) <= total / cut + B <= splits + B
+    const int cut = max(g.min_tiles, (total + g.splits - 1) / g.splits);
+    sum = 0;
+    for (int b = b0; b < b1; ++b) sum += max(1, (span_of(g, g.lengths[b]).tiles + cut - 1) / cut);
+    const int upto = wave_scan(sum);
+    const uint64_t past = __ballot(upto > x);
+    if (past == 0) return Piece{0, 0, 0};
+    const int owner = __ffsll((unsigned long long)past) - 1;
+    int at = x - (__builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(sum, owner));
+    for (int b = owner * each; b < min((owner + 1) * each, g.B); ++b) {
+        const int n = max(1, (span_of(g, g.lengths[b]).tiles + cut - 1) / cut);
+        if (at < n) return Piece{b, at, n};
+        at -= n;
+    }
+    return Piece{0, 0, 0};  // (not reached: the owner's pieces hold x)
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t codes2(uint32_t w, bool hi) {
+    // (the half has to be a constant)
+    if constexpr (BF16) {
+        const bf16x2 r = hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
+                            : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
+        return __builtin_bit_cast(uint32_t, r);
+    } else {
+        const f16x2 r = hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true)
+                           : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
+        return __builtin_bit_cast(uint32_t, r);
+    }
+}
+
+template <int N>
+struct Dwords {
+    uint32_t d[N];
+};
+template <int BYTES>
+__device__ __forceinline__ Dwords<BYTES / 4> load_bytes(const uint8_t* p) {
+    Dwords<BYTES / 4> r;
+    if constexpr (BYTES == 4) {
+        r.d[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (BYTES == 8) {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+        r.d[0] = v[0];
+        r.d[1] = v[1];
+    } else {
+#pragma unroll
+        for (int i = 0; i < BYTES / 16; ++i) {
+            const u32x4 v = ldg128(p + 16 * i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r.d[4 * i + j] = v[j];
+        }
+    }
+    return r;
+}
+
+// a pair of floats as 16-bit values and what their rounding left out
+template <bool BF16>
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = f32_to_act2<BF16>(a, b);
+    lo = f32_to_act2<BF16>(a - act_to_f32<BF16>((uint16_t)hi), b - act_to_f32<BF16>((uint16_t)(hi >> 16)));
+}
+
+// DM: head_dim rounded up to 64, 128 or 256 (FULL: it is DM)
+template <bool BF16, int MODE, int DM, bool FULL, int NW>
+__global__ __launch_bounds__(NW * 64) void paged_attention_kernel(PagedAttnArgs g) {
+    constexpr bool F8 = MODE != KV_16;
+    constexpr bool ROW = MODE == KV_E4M3_ROW;
+    constexpr bool PBF = BF16 || F8;              // P's type: E4M3 values and scales go as bf16
+    constexpr int ELT = F8 ? 1 : 2;
+    constexpr int KD = F8 ? 64 : 32;              // channels of one 16-byte K load of the 4 lane groups
+    constexpr int KL = DM / KD;                   // such loads a token row
+    constexpr int VEC = DM / 16;                  // V channels of a lane
+    constexpr int VD = VEC * ELT / 4;             // their dwords
+    extern __shared__ __attribute__((aligned(16))) float lds[];
+
+    const int D = FULL ? DM : g.D;
+    const int lane = threadIdx.x & 63, r = lane & 15, q4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Piece pc = piece_of(g, blockIdx.x);
+    const int b = __builtin_amdgcn_readfirstlane(pc.b), at = __builtin_amdgcn_readfirstlane(pc.at);
+    const int pieces = __builtin_amdgcn_readfirstlane(pc.n);
+    if (pieces == 0) return;
+    const Span sp = span_of(g, g.lengths[b]);
+    const int t0 = (int)((int64_t)sp.tiles * at / pieces), t1 = (int)((int64_t)sp.tiles * (at + 1) / pieces);
+    const int group = g.heads / g.kv_heads;
+    const int htiles = (group + 15) / 16;
+    const int kvh = blockIdx.y / htiles, h0 = (blockIdx.y - kvh * htiles) * 16;
+    const int nh = min(16, group - h0);           // heads of this workgroup
+    const int head0 = kvh * group + h0;
+    const uint32_t page16 = (uint32_t)g.page_size / KV_TOKENS;
+    const uint64_t magic = ((uint64_t)1 << 32) / page16 + ((((uint64_t)1 << 32) % page16) ? 1 : 0);
+
+    // half a tile: 16 tokens, in one page; those past the sequence read its last
+    struct Half {
+        int64_t rows;  // (page, head)'s first row in the cache + the position in the page
+        bool good;
+    };
+    const int last16 = (sp.len - 1) / KV_TOKENS;  // (not used of an empty sequence)
+    const int32_t* table = g.table + (int64_t)b * g.width;
+    auto half_at = [&](int tok) {
+        const uint32_t u = (uint32_t)min(tok / KV_TOKENS, last16);
+        const uint32_t col = (uint32_t)(((uint64_t)u * magic) >> 32);  // u / page16: the host checks the range
+        const int page = table[col];
+        Half h;
+        h.good = page >= 0 && page < g.pages;     // a bad page holds no tokens
+        h.rows = ((int64_t)(h.good ? page : 0) * g.kv_heads + kvh) * g.page_size + (u - col * page16) * KV_TOKENS;
+        return h;
+    };
+
+    // Q, the B operand of every K step: head r, the channels in K's order
+    u32x4 qv[DM / 32];
+#pragma unroll
+    for (int c = 0; c < DM / 32; ++c) {
+        const int ch = F8 ? 64 * (c / 2) + 16 * q4 + 8 * (c % 2) : 32 * c + 8 * q4;
+        qv[c] = u32x4{0, 0, 0, 0};
+        if (r < nh && ch < D) qv[c] = ldg128(g.q + (int64_t)b * g.q_stride + (int64_t)(head0 + r) * D + ch);
+    }
+
+    u32x4 kv[2][KL];
+    Dwords<VD> vv[8];
+    f32x4 ksv[2], vsv[2];
+    auto kload = [&](const Half (&h)[2]) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint8_t* p = g.k + h[s].rows * (D * ELT);
+#pragma unroll
+            for (int c = 0; c < KL; ++c) {
+                if (!FULL) kv[s][c] = u32x4{0, 0, 0, 0};
+                if (FULL || KD * c + (16 / ELT) * q4 < D) kv[s][c] = ldg128(p + r * (D * ELT) + (KD * c) * ELT + 16 * q4);
+            }
+            if constexpr (ROW) ksv[s] = *reinterpret_cast<const f32x4*>(g.ks + h[s].rows + 4 * q4);
+        }
+    };
+    auto vload = [&](const Half (&h)[2]) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint8_t* p = g.v + h[s].rows * (D * ELT);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (!FULL)
+#pragma unroll
+                    for (int i = 0; i < VD; ++i) vv[4 * s + j].d[i] = 0;
+                if (FULL || r * VEC < D)
+                    vv[4 * s + j] = load_bytes<VEC * ELT>(p + (4 * q4 + j) * (D * ELT) + r * (VEC * ELT));
+            }
+            if constexpr (ROW) vsv[s] = *reinterpret_cast<const f32x4*>(g.vs + h[s].rows + 4 * q4);
+        }
+    };
+
+    f32x4 acc[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = M_NONE, l = 0.0f;  // head r's running maximum (the same in its 4 lanes); the lane's own sum
+
+    int t = t0 + wave;
+    if (t < t1) {
+        Half cur[2], nxt[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) cur[s] = half_at(sp.begin + TILE * t + 16 * s);
+        kload(cur);
+        vload(cur);
+        for (; t < t1; t += NW) {
+            const int tok = sp.begin + TILE * t;
+            const int tn = min(t + NW, t1 - 1);  // past the end: a tile again, from the cache, unused
+#pragma unroll
+            for (int s = 0; s < 2; ++s) nxt[s] = half_at(sp.begin + TILE * tn + 16 * s);
+
+            f32x4 sc[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                sc[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < KL; ++c) {
+                    if constexpr (F8) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t w0 = kv[s][c][2 * half], w1 = kv[s][c][2 * half + 1];
+                            const u32x4 a = {codes2<BF16>(w0, false), codes2<BF16>(w0, true), codes2<BF16>(w1, false),
+                                             codes2<BF16>(w1, true)};
+                            sc[s] = mfma16x16x32<BF16>(a, qv[2 * c + half], sc[s]);
+                        }
+                    } else {
+                        sc[s] = mfma16x16x32<BF16>(kv[s][c], qv[c], sc[s]);
+                    }
+                }
+                if constexpr (ROW) sc[s] *= ksv[s];
+            }
+            kload(nxt);
+
+            // scores in exponents of 2; tokens outside the span or in a bad page have none
+            const bool edge = tok < sp.lo || tok + TILE > sp.len || !cur[0].good || !cur[1].good;
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = sc[j / 4][j % 4] * g.qk_scale;
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int k = tok + 16 * (j / 4) + 4 * q4 + j % 4;
+                    const bool live = k >= sp.lo && k < sp.len && cur[j / 4].good;
+                    x[j] = live ? x[j] : -INFINITY;
+                    // what lies there may be anything, and 0 * NaN is one
+#pragma unroll
+                    for (int i = 0; i < VD; ++i) vv[j].d[i] = live ? vv[j].d[i] : 0;
+                    if constexpr (ROW) vsv[j / 4][j % 4] = live ? vsv[j / 4][j % 4] : 0.0f;
+                }
+            }
+            float top = x[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
+            if (__any(top > m + M_SLACK)) {
+                top = fmaxf(top, m);
+                top = fmaxf(top, __shfl_xor(top, 16, 64));
+                top = fmaxf(top, __shfl_xor(top, 32, 64));
+                const float f = __builtin_amdgcn_exp2f(m - top);
+                m = top;
+                l *= f;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) acc[e] *= f;
+            }
+            u32x4 phi, plo;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = __builtin_amdgcn_exp2f(x[j] - m);
+                l += x[j];
+                if constexpr (ROW) x[j] *= vsv[j / 4][j % 4];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t hi, lo;
+                split2<PBF>(x[2 * j], x[2 * j + 1], hi, lo);
+                phi[j] = hi;
+                plo[j] = lo;
+            }
+            // channel e of each lane's VEC: tokens 2 j and 2 j + 1 side by side
+            if constexpr (F8) {
+#pragma unroll
+                for (int w = 0; w < VEC / 2; ++w) {  // channels 2 w and 2 w + 1: bytes of dword w / 2
+                    u32x4 a0, a1;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t lo = vv[2 * j].d[w / 2], hi = vv[2 * j + 1].d[w / 2];
+                        const uint32_t pair = __builtin_amdgcn_perm(hi, lo, w % 2 ? 0x07030602u : 0x05010400u);
+                        a0[j] = codes2<PBF>(pair, false);
+                        a1[j] = codes2<PBF>(pair, true);
+                    }
+                    acc[2 * w] = mfma16x16x32<PBF>(a0, phi, acc[2 * w]);
+                    acc[2 * w + 1] = mfma16x16x32<PBF>(a1, phi, acc[2 * w + 1]);
+                    acc[2 * w] = mfma16x16x32<PBF>(a0, plo, acc[2 * w]);
+                    acc[2 * w + 1] = mfma16x16x32<PBF>(a1, plo, acc[2 * w + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    u32x4 a;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t lo = vv[2 * j].d[e / 2], hi = vv[2 * j + 1].d[e / 2];
+                        a[j] = __builtin_amdgcn_perm(hi, lo, e % 2 ? 0x07060302u : 0x05040100u);
+                    }
+                    acc[e] = mfma16x16x32<PBF>(a, phi, acc[e]);
+                    acc[e] = mfma16x16x32<PBF>(a, plo, acc[e]);
+                }
+            }
+            vload(nxt);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) cur[s] = nxt[s];
+        }
+    }
+
+    // join the waves: lane l holds channels [4 VEC q4, +4 VEC) of head r
+    constexpr int LD = DM + 4;
+    float* lm = lds;                   // [NW][16]
+    float* ll = lds + NW * 16;         // [NW][16]
+    float* lo = lds + 2 * NW * 16;     // [NW][nh][LD]
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (q4 == 0) {
+        lm[wave * 16 + r] = m;
+        ll[wave * 16 + r] = l;
+    }
+    if (r < nh) {
+        float* o = lo + (wave * nh + r) * LD + 4 * VEC * q4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; e += 4)
+                *reinterpret_cast<f32x4*>(o + VEC * i + e) = f32x4{acc[e][i], acc[e + 1][i], acc[e + 2][i], acc[e + 3][i]};
+    }
+    __syncthreads();
+    const int quads = D / 4;
+    for (int id = threadIdx.x; id < nh * quads; id += NW * 64) {
+        const int hd = id / quads, c = 4 * (id - hd * quads);
+        float mx = lm[hd], sum = 0.0f;
+#pragma unroll
+        for (int w = 1; w < NW; ++w) mx = fmaxf(mx, lm[w * 16 + hd]);
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float f = __builtin_amdgcn_exp2f(lm[w * 16 + hd] - mx);
+            sum += f * ll[w * 16 + hd];
+            o += f * *reinterpret_cast<const f32x4*>(lo + (w * nh + hd) * LD + c);
+        }
+        const int64_t head = head0 + hd;
+        if (pieces == 1) {
+            // no token with a weight: zeros, and -inf
+            const float inv = sum == 0.0f ? 0.0f : g.v_scale / sum;
+            *reinterpret_cast<u32x2*>(g.out + (int64_t)b * g.out_stride + head * D + c) =
+                u32x2{f32_to_act2<BF16>(o[0] * inv, o[1] * inv), f32_to_act2<BF16>(o[2] * inv, o[3] * inv)};
+            if (g.lse && c == 0) g.lse[(int64_t)b * g.heads + head] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * LN2;
+        } else {
+            const int64_t slot = (int64_t)blockIdx.x * g.heads + head;
+            *reinterpret_cast<f32x4*>(g.part_o + slot * D + c) = o;
+            if (c == 0) {
+                g.part_ml[2 * slot] = mx;
+                g.part_ml[2 * slot + 1] = sum;
+            }
+        }
+    }
+    if (g.splits > 0 && at == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+        g.part_at[2 * b] = blockIdx.x;
+        g.part_at[2 * b + 1] = pieces;
+    }
+}
+
+// the pieces of one sequence and head: 256 threads as 256 / (D / 4) pieces at a
+// time by D / 4 vectors of 4 channels
+template <bool BF16>
+__global__ __launch_bounds__(256) void paged_join_kernel(PagedAttnArgs g) {
+    __shared__ f32x4 so[256];
+    __shared__ float sl[256];
+    const int b = blockIdx.y, head = blockIdx.x;
+    const int first = g.part_at[2 * b], n = g.part_at[2 * b + 1];
+    if (n <= 1) return;
+    const float* ml = g.part_ml + 2 * ((int64_t)first * g.heads + head);
+    float mx = M_NONE;
+    for (int p = 0; p < n; ++p) mx = fmaxf(mx, ml[2 * (int64_t)p * g.heads]);
+    const int quads = g.D / 4, side = 256 / quads;
+    const int row = threadIdx.x / quads, c = 4 * (threadIdx.x - row * quads);
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float sum = 0.0f;
+    if (row < side)
+        for (int p = row; p < n; p += side) {
+            const float f = __builtin_amdgcn_exp2f(ml[2 * (int64_t)p * g.heads] - mx);
+            sum += f * ml[2 * (int64_t)p * g.heads + 1];
+            o += f * *reinterpret_cast<const f32x4*>(g.part_o + ((int64_t)(first + p) * g.heads + head) * g.D + c);
+        }
+    so[threadIdx.x] = o;
+    sl[threadIdx.x] = sum;
+    __syncthreads();
+    if (row != 0) return;
+    for (int i = 1; i < side; ++i) {
+        o += so[i * quads + threadIdx.x];
+        sum += sl[i * quads + threadIdx.x];
+    }
+    const float inv = sum == 0.0f ? 0.0f : g.v_scale / sum;
+    *reinterpret_cast<u32x2*>(g.out + (int64_t)b * g.out_stride + (int64_t)head * g.D + c) =
+        u32x2{f32_to_act2<BF16>(o[0] * inv, o[1] * inv), f32_to_act2<BF16>(o[2] * inv, o[3] * inv)};
+    if (g.lse && c == 0) g.lse[(int64_t)b * g.heads + head] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * LN2;
+}
+
+constexpr int NW = 4;
+constexpr int MIN_TILES = 2 * NW;
+
+template <bool BF16, int MODE, int DM, bool FULL>
+void launch_full(const PagedAttnArgs& g, hipStream_t s) {
+    const int group = g.heads / g.kv_heads;
+    const int nh = std::min(group, 16);
+    const size_t lds = (2 * NW * 16 + (size_t)NW * nh * (DM + 4)) * sizeof(float);
+    auto kern = paged_attention_kernel<BF16, MODE, DM, FULL, NW>;
+    if (lds > 65536)
+        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)lds);
+    const dim3 grid(g.B + g.splits, g.kv_heads * ((group + 15) / 16));
+    hipLaunchKernelGGL(kern, grid, dim3(NW * 64), lds, s, g);
+}
+
+template <bool BF16, int MODE>
+void launch_dim(const PagedAttnArgs& g, hipStream_t s) {
+    if (g.D == 64) launch_full<BF16, MODE, 64, true>(g, s);
+    else if (g.D == 128) launch_full<BF16, MODE, 128, true>(g, s);
+    else if (g.D == 256) launch_full<BF16, MODE, 256, true>(g, s);
+    else if (g.D < 64) launch_full<BF16, MODE, 64, false>(g, s);
+    else if (g.D < 128) launch_full<BF16, MODE, 128, false>(g, s);
+    else launch_full<BF16, MODE, 256, false>(g, s);
+}
+
+template <bool BF16>
+void launch_type(const PagedAttnArgs& g, hipStream_t s) {
+    if (g.mode == KV_16) launch_dim<BF16, KV_16>(g, s);
+    else if (g.mode == KV_E4M3_ROW) launch_dim<BF16, KV_E4M3_ROW>(g, s);
+    else launch_dim<BF16, KV_E4M3_STATIC>(g, s);
+    if (g.splits > 0) hipLaunchKernelGGL(paged_join_kernel<BF16>, dim3(g.heads, g.B), dim3(256), 0, s, g);
+}
+
+}  // namespace
+
+int paged_attn_splits(int B, int heads, int kv_heads, int64_t max_tokens) {
+    const int64_t tiles = (max_tokens + TILE - 1) / TILE;
+    if (tiles <= MIN_TILES) return 0;
+    const int units = kv_heads * ((heads / kv_heads + 15) / 16);
+    const int64_t want = std::max(1, (768 + units - 1) / units);
+    return (int)std::min<int64_t>(want, (int64_t)B * ((tiles + MIN_TILES - 1) / MIN_TILES));
+}
+
+void launch_paged_attention(const PagedAttnArgs& a, bool bf16, hipStream_t s) {
+    PagedAttnArgs g = a;
+    g.min_tiles = MIN_TILES;
+    if (bf16) launch_type<true>(g, s);
+    else launch_type<false>(g, s);
+}
+
+}  // namespace wq

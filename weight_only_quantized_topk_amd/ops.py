@@ -18,9 +18,9 @@ from typing import NamedTuple, Optional, Tuple
 import numpy as np
 
 from . import _lib
-from ._lib import (WQ_BF16, WQ_F16, WQ_F32, WQ_GROUP_MAX, WQ_GROUP_TOP2, WQ_PACK_INTERLEAVE_GATE_UP,
+from ._lib import (WQ_BF16, WQ_E4M3, WQ_F16, WQ_F32, WQ_GROUP_MAX, WQ_GROUP_TOP2, WQ_PACK_INTERLEAVE_GATE_UP,
                    WQ_SCORE_SIGMOID, WQ_SCORE_SOFTMAX, WQ_STAGE_DOWN, WQ_STAGE_GATE_UP, WQ_STAGE_RAW,
-                   WqMoeGemmDesc, check, load)
+                   WqKvCache, WqMoeGemmDesc, check, load)
 
 __all__ = [
     "moe_route", "moe_align", "moe_route_align", "moe_align_capacity", "moe_gemm_workspace_bytes", "moe_w4a16_gemm", "moe_w8a16_gemm",
@@ -29,6 +29,7 @@ __all__ = [
     "pack_w4", "pack_w8", "pack_sparse24", "act_code", "moe_fp8_gemm_workspace_bytes", "moe_fp8_w8a8_gemm",
     "pack_fp8", "moe_route_grouped", "moe_route_grouped_align", "rms_norm", "RmsNormOut", "moe_fp8_codes_gemm",
     "Lora", "pack_lora", "dense_lora_gemm", "dense_lora_workspace_bytes",
+    "KVCache", "kv_cache", "kv_cache_write", "kv_cache_read", "paged_attention", "paged_attention_workspace_bytes",
 ]
 
 
@@ -644,6 +645,184 @@ def dense_w8a16_gemm(x, N: int, w_packed, scales, out=None, workspace=None, stre
     """Dense int8 linear: x [M, K] bf16/fp16 (device) -> y [M, N], weights
     packed by pack_w8 with E = 1; lora: the rows' adapters, added to y."""
     return _dense(load().dense_w8a16_gemm, x, N, w_packed, scales, (), out, workspace, stream, False, lora)
+
+
+# ----------------------------------------------------------------------------
+# paged key-value cache and attention over it
+# ----------------------------------------------------------------------------
+class KVCache(NamedTuple):
+    """A paged key-value cache [pages, kv_heads, page_size, head_dim]: 16-bit
+    values, or E4M3 codes with a scale a row (tensors) or one for all (numbers)."""
+    k: object               # act dtype, or uint8 / float8_e4m3fn codes
+    v: object
+    k_scale: object = None  # of codes: float32 [pages, kv_heads, page_size], or a number
+    v_scale: object = None
+
+
+def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, act, quant: Optional[str] = None,
+             k_scale: Optional[float] = None, v_scale: Optional[float] = None, device="cuda") -> KVCache:
+    """An empty cache: of the act dtype, or of E4M3 codes with a scale a row
+    (quant="row") or the calibrated k_scale and v_scale (quant="static")."""
+    torch = _torch()
+    act_code(act)
+    if quant not in (None, "row", "static"):
+        raise ValueError("quant must be None, 'row' or 'static', got %r" % (quant,))
+    if (quant == "static") != (k_scale is not None) or (quant == "static") != (v_scale is not None):
+        raise ValueError("k_scale and v_scale go with quant='static'")
+    shape = (pages, kv_heads, page_size, head_dim)
+    k, v = (torch.empty(shape, dtype=torch.uint8 if quant else act, device=device) for _ in range(2))
+    if quant == "row":
+        k_scale, v_scale = (torch.empty(shape[:3], dtype=torch.float32, device=device) for _ in range(2))
+    c = KVCache(k, v, k_scale, v_scale)
+    _kv_desc(c, act)
+    return c
+
+
+def _kv_desc(c: KVCache, act, device=None) -> WqKvCache:
+    """Checks a cache for a call with activations of type act -> its descriptor."""
+    torch = _torch()
+    k, v, ks, vs = c
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError("the cache must be [pages, kv_heads, page_size, head_dim], got %s" % list(shape))
+    codes = k.dtype in (torch.uint8, torch.float8_e4m3fn)
+    if not codes and k.dtype != act:
+        raise TypeError("the cache must be %s or E4M3 codes, got %s" % (act, k.dtype))
+    dev = k.device if device is None else device
+    _check(k, "cache k", shape, (k.dtype,), dev)
+    _check(v, "cache v", shape, (k.dtype,), dev)
+    P, H, S, D = shape
+    _int32(pages=P, kv_heads=H, page_size=S, head_dim=D)
+    d = WqKvCache(C.sizeof(WqKvCache), k.data_ptr(), v.data_ptr(), None, None, 0.0, 0.0,
+                  WQ_E4M3 if codes else act_code(act), P, H, S, D)
+    if (ks is None) != (vs is None) or codes != (ks is not None):
+        raise ValueError("a cache of codes has k_scale and v_scale, one of 16-bit values neither")
+    if codes:
+        if isinstance(ks, torch.Tensor) != isinstance(vs, torch.Tensor):
+            raise TypeError("k_scale and v_scale are both tensors or both numbers")
+        if isinstance(ks, torch.Tensor):
+            _check(ks, "cache k_scale", shape[:3], (torch.float32,), dev)
+            _check(vs, "cache v_scale", shape[:3], (torch.float32,), dev)
+            d.d_k_scales, d.d_v_scales = ks.data_ptr(), vs.data_ptr()
+        else:
+            d.k_scale, d.v_scale = ks, vs
+    return d
+
+
+def _head_rows(t, name: str, shape, act, device) -> int:
+    """A [rows, heads, head_dim] argument whose heads lie next to each other (rows
+    may be strided) -> its row stride in elements."""
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if t.dtype != act:
+        raise TypeError("%s must be %s, got %s" % (name, act, t.dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s, the cache on %s" % (name, t.device, device))
+    T, H, D = shape
+    st = t.stride()
+    if t.numel() and (st[2] != 1 and D > 1 or st[1] != D and H > 1 or st[0] < H * D and T > 1):
+        raise ValueError("%s must be contiguous in its rows, got strides %s" % (name, list(st)))
+    return st[0] if T > 1 else H * D
+
+
+def kv_cache_write(k, v, cache: KVCache, slots, stream=None) -> KVCache:
+    """The rows of new tokens into the cache, quantised where it holds codes: k, v
+    [T, kv_heads, head_dim] bf16/fp16 (device; rows may be strided), slots [T]
+    int64 (page * page_size + position; outside the cache, as -1 of a padding
+    token: not written).  The slots of a call differ.  Returns the cache."""
+    torch = _torch()
+    dev = k.device
+    d = _kv_desc(cache, k.dtype, dev)
+    act = act_code(k.dtype)
+    shape = (k.shape[0], d.kv_heads, d.head_dim)
+    _int32(T=shape[0])
+    ks, vs = _head_rows(k, "k", shape, k.dtype, dev), _head_rows(v, "v", shape, k.dtype, dev)
+    _check(slots, "slots", shape[:1], (torch.int64,), dev)
+    check(load().wq_kv_cache_write(C.byref(d), k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), shape[0], act,
+                                   _stream(stream)), "wq_kv_cache_write")
+    return cache
+
+
+def kv_cache_read(cache: KVCache, slots, act, k=None, v=None, stream=None):
+    """The rows of slots [T] int64 back -> (k, v) [T, kv_heads, head_dim] of type
+    act (rows of given buffers may be strided); zeros where a slot is outside
+    the cache."""
+    torch = _torch()
+    dev = cache.k.device
+    d = _kv_desc(cache, act, dev)
+    code = act_code(act)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T], got %s" % list(slots.shape))
+    _check(slots, "slots", slots.shape, (torch.int64,), dev)
+    shape = (slots.shape[0], d.kv_heads, d.head_dim)
+    _int32(T=shape[0])
+    new = []
+    if k is None:
+        new.append(k := _alloc(stream, torch.empty, shape, dtype=act, device=dev))
+    if v is None:
+        new.append(v := _alloc(stream, torch.empty, shape, dtype=act, device=dev))
+    ks, vs = _head_rows(k, "k", shape, act, dev), _head_rows(v, "v", shape, act, dev)
+    check(load().wq_kv_cache_read(C.byref(d), slots.data_ptr(), shape[0], k.data_ptr(), ks, v.data_ptr(), vs, code,
+                                  _stream(stream)), "wq_kv_cache_read")
+    _keep_for(stream, *new)
+    return k, v
+
+
+def paged_attention_workspace_bytes(B: int, heads: int, kv_heads: int, head_dim: int, page_size: int,
+                                    table_width: int, window: int = 0) -> int:
+    _int32(B=B, heads=heads, kv_heads=kv_heads, head_dim=head_dim, page_size=page_size, table_width=table_width,
+           window=window)
+    return int(load().wq_paged_attention_workspace_bytes(B, heads, kv_heads, head_dim, page_size, table_width, window))
+
+
+def paged_attention(q, cache: KVCache, block_table, lengths, scale: Optional[float] = None, window: int = 0,
+                    out=None, want_lse: bool = False, lse=None, workspace=None, stream=None):
+    """Attention of one new token a sequence over its tokens in the cache: q [B,
+    heads, head_dim] bf16/fp16 (device; rows may be strided), block_table [B,
+    width] int32 (the page of each page_size tokens), lengths [B] int32 (0: no
+    tokens, zeros out), heads a multiple of the cache's; scale: head_dim ** -0.5
+    unless given; window: the last so many tokens only.  -> out like q, with
+    want_lse (out, lse [B, heads] float32), the logarithm of each row's sum."""
+    torch = _torch()
+    dev, dt = q.device, q.dtype
+    act = act_code(dt)
+    d = _kv_desc(cache, dt, dev)
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [B, heads, head_dim], block_table [B, width], got %s, %s"
+                         % (list(q.shape), list(block_table.shape)))
+    B, heads, D = q.shape
+    width = block_table.shape[1]
+    if D != d.head_dim or heads % d.kv_heads:
+        raise ValueError("q must be [B, a multiple of %d heads, %d], got %s" % (d.kv_heads, d.head_dim, list(q.shape)))
+    _int32(B=B, heads=heads, width=width, window=window)
+    qs = _head_rows(q, "q", (B, heads, D), dt, dev)
+    _check(block_table, "block_table", (B, width), (torch.int32,), dev)
+    _check(lengths, "lengths", (B,), (torch.int32,), dev)
+    if lse is not None and not want_lse:
+        raise ValueError("lse goes with want_lse")
+    new = []
+    if out is None:
+        new.append(out := _alloc(stream, torch.empty, (B, heads, D), dtype=dt, device=dev))
+    os_ = _head_rows(out, "out", (B, heads, D), dt, dev)
+    if want_lse:
+        if lse is None:
+            new.append(lse := _alloc(stream, torch.empty, (B, heads), dtype=torch.float32, device=dev))
+        else:
+            _check(lse, "lse", (B, heads), (torch.float32,), dev)
+    L = load()
+    if workspace is None:
+        nb = L.wq_paged_attention_workspace_bytes(B, heads, d.kv_heads, D, d.page_size, width, window)
+        if nb:
+            workspace = _alloc(stream, torch.empty, nb, dtype=torch.uint8, device=dev)
+    elif not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be contiguous on %s" % dev)
+    check(L.wq_paged_attention(C.byref(d), q.data_ptr(), qs, B, heads, block_table.data_ptr(), width,
+                               lengths.data_ptr(), D ** -0.5 if scale is None else scale, window, out.data_ptr(), os_,
+                               _ptr(lse), act, _ptr(workspace),
+                               0 if workspace is None else workspace.numel() * workspace.element_size(),
+                               _stream(stream)), "wq_paged_attention")
+    _keep_for(stream, *new)
+    return (out, lse) if want_lse else out
 
 
 def quantize_w8(w, q=None, scales=None, stream=None):
