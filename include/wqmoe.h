@@ -23,7 +23,8 @@
  *   wq_kv_cache_read      rows of the cache back as 16-bit values
  *   wq_paged_attention    attention of one new token a sequence over the cache
  * Beside them: dense_w4a16_gemm / dense_w8a16_gemm (one quantized weight
- * matrix, the same kernels with one expert) and wq_quantize_w8 (the int8
+ * matrix, the same kernels with one expert; dense_w4a16_epilogue_gemm /
+ * dense_w8a16_epilogue_gemm with bias, activation and residual) and wq_quantize_w8 (the int8
  * weights and scales from a 16-bit checkpoint on the device, at load time).
  * Off the hot path (host memory in and out): the packers that turn canonical
  * quantized tensors into the device layout these kernels read.
@@ -460,6 +461,42 @@ wq_status dense_w4a16_gemm(const void* d_x, int M, int K, int N, const void* d_w
                            size_t workspace_bytes, void* stream);
 wq_status dense_w8a16_gemm(const void* d_x, int M, int K, int N, const void* d_w_packed, const void* d_scales,
                            void* d_y, int act_dtype, void* d_workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The same with an epilogue on the fp32 sums, rounded once:
+ *   y[m, n] = f(sum_k x[m, k] W[n, k] + bias[n]) + residual[m, n]
+ *   d_bias      [N] act dtype, or NULL
+ *   activation  f: WQ_ACT_NONE, WQ_ACT_RELU, WQ_ACT_SILU (z / (1 + exp(-z))),
+ *               WQ_ACT_GELU (z (1 + erf(z / sqrt 2)) / 2) or WQ_ACT_GELU_TANH
+ *               (z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2)
+ *   d_residual  [M, N] act dtype or NULL, row stride in elements (>= N, a
+ *               multiple of 8); may be y (stride N), which is then added to in place
+ *   dense_epilogue_workspace_bytes(wbits, ...) bytes of workspace, 256-byte
+ *               aligned (NULL allowed for 0): K slices of a large batch that leaves most of the GPU
+ *               idle, the act-order gather
+ * One launch without act-order and a split of K (any number of rows).  Limits:
+ * those above, M <= 65535 * 64, K and N <= 2^24.  y and the workspace must not
+ * overlap anything else.
+ */
+#define WQ_ACT_NONE 0
+#define WQ_ACT_RELU 1
+#define WQ_ACT_SILU 2
+#define WQ_ACT_GELU 3
+#define WQ_ACT_GELU_TANH 4
+typedef struct wq_epilogue {
+    size_t struct_size;          /* = sizeof(wq_epilogue) */
+    const void* d_bias;
+    const void* d_residual;
+    int64_t residual_stride;
+    int activation;              /* WQ_ACT_* */
+} wq_epilogue;
+size_t dense_epilogue_workspace_bytes(int wbits, int M, int K, int N, int act_order);
+wq_status dense_w4a16_epilogue_gemm(const void* d_x, int M, int K, int N, const void* d_w_packed, const void* d_scales,
+                                    int group_size, const int32_t* d_k_perm, const wq_epilogue* epilogue, void* d_y,
+                                    int act_dtype, void* d_workspace, size_t workspace_bytes, void* stream);
+wq_status dense_w8a16_epilogue_gemm(const void* d_x, int M, int K, int N, const void* d_w_packed, const void* d_scales,
+                                    const wq_epilogue* epilogue, void* d_y, int act_dtype, void* d_workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Low-rank adapters beside the dense linear layer                           */

@@ -208,3 +208,71 @@ def test_attention_binding_refusals():
     for k in (dict(q=q.half(), cache=cache()), dict(block_table=tab.long()), dict(lengths=n.long()), dict(out=q.half()),
               dict(want_lse=True, lse=torch.zeros((3, 4), dtype=BFT))):
         refused(lambda: call(**k), TypeError)
+
+
+# ---------------------------------------------------------------------------
+# dense projections with an epilogue
+# ---------------------------------------------------------------------------
+def dense(bits=8, epi=None, **k):
+    from weight_only_quantized_topk_amd._lib import WqEpilogue
+    d = dict(x=at(), M=4, K=256, N=64, w=at(GB), s=at(2 * GB), group=128, perm=None, y=at(3 * GB), dt=wq.WQ_F16, ws=at(8 * GB),
+             nb=GB, struct_size=C.sizeof(WqEpilogue), bias=FAKE + 4 * GB, act=2, r=FAKE + 5 * GB, rs=64)
+    d.update(k)
+    e = C.byref(WqEpilogue(d["struct_size"], d["bias"], d["r"], d["rs"], d["act"])) if epi is None else epi
+    head = [d["x"], d["M"], d["K"], d["N"], d["w"], d["s"]]
+    tail = [e, d["y"], d["dt"], d["ws"], d["nb"], None]
+    if bits == 4:
+        return status("dense_w4a16_epilogue_gemm", *head, d["group"], d["perm"], *tail)
+    return status("dense_w8a16_epilogue_gemm", *head, *tail)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("change,want", [
+    (dict(M=-1), INV), (dict(K=0), INV), (dict(N=0), INV), (dict(dt=2), INV), (dict(K=96), UNS), (dict(N=72, rs=72), UNS),
+    (dict(M=(1 << 24) + 1), UNS), (dict(M=65535 * 64 + 1), UNS), (dict(M=1 << 20, K=8192), UNS), (dict(struct_size=0), INV),
+    (dict(act=5), INV), (dict(act=-1), INV), (dict(rs=63), INV), (dict(rs=0), INV), (dict(rs=1 << 62), INV), (dict(rs=68), UNS),
+    (dict(x=None), INV), (dict(w=None), INV), (dict(s=None), INV), (dict(y=None), INV), (dict(x=at(8)), INV),
+    (dict(bias=FAKE + 4), INV), (dict(r=FAKE + 8), INV), (dict(y=at(GB)), INV), (dict(y=at(4 * GB)), INV),
+    (dict(y=at(1024)), INV), (dict(y=at(5 * GB + 16)), INV), (dict(y=at(5 * GB), rs=128), INV)])
+def test_dense_refusals(bits, change, want):
+    st, msg = dense(bits, **change)
+    assert st == want, (change, msg)
+
+
+def test_dense_workspace_and_forms():
+    f = wq.dense_epilogue_workspace_bytes
+    assert f(8, 64, 4096, 4096) == 0 and f(8, 0, 4096, 4096) == 0 and f(8, 64, 100, 64) == 0
+    assert f(4, 5, 256, 64, True) > 0
+    many = f(8, 200, 4096, 128)
+    assert many > 0  # K is split there
+    big = dict(M=200, K=4096, N=128, rs=128)
+    assert dense(8, nb=many - 1, **big)[0] == INV
+    for change in (dict(ws=None), dict(ws=at(8 * GB + 16)), dict(ws=at(3 * GB)), dict(ws=at(5 * GB)), dict(ws=at(GB))):
+        assert dense(8, **{**big, **change})[0] == INV, change
+    assert dense(8, **big)[0] in NO_DEVICE
+    from weight_only_quantized_topk_amd._lib import WqEpilogue
+    assert dense(8, epi=C.cast(None, C.POINTER(WqEpilogue)))[0] == INV
+    for change in (dict(y=at(5 * GB)), dict(bias=None), dict(r=None, rs=0), dict(bias=None, r=None, rs=0, act=0)):
+        assert dense(8, **change)[0] in NO_DEVICE, change
+    assert dense(4, dt=wq.WQ_BF16)[0] == UNS and dense(4, group=64)[0] == UNS
+    assert dense(8, M=0, x=None, y=None, r=None)[0] == wq.WQ_OK
+
+
+def test_dense_binding_refusals():
+    x, b, r = torch.zeros((4, 256), dtype=BFT), torch.zeros(64, dtype=BFT), torch.zeros((4, 64), dtype=BFT)
+    w, s = torch.zeros(64 * 256, dtype=torch.int8), torch.zeros(64, dtype=torch.int16)
+
+    def call(x=x, N=64, w=w, s=s, **k):
+        return wq.dense_w8a16_gemm(x, N, w, s, **k)
+
+    lora = wq.Lora(torch.zeros(4, dtype=torch.int32), torch.zeros((1, 8, 256), dtype=BFT), torch.zeros((1, 64, 8), dtype=BFT), None)
+    for k in (dict(activation="swish"), dict(bias=b[:63]), dict(bias=torch.zeros(128, dtype=BFT)[::2]), dict(residual=r[:3]),
+              dict(residual=torch.zeros((4, 128), dtype=BFT)[:, ::2]), dict(bias=b, out=torch.zeros((4, 128), dtype=BFT)[:, :64]),
+              dict(bias=b, out=r[:3]), dict(bias=b, x=x[:, ::2]), dict(bias=b, x=x[0]), dict(bias=b, w=w[:-1]), dict(bias=b, s=s[:-1]),
+              dict(activation="gelu", lora=lora), dict(bias=b, workspace=torch.zeros(64, dtype=torch.uint8)[::2]),
+              dict(bias=b, N=1 << 40)):
+        refused(lambda: call(**k))
+    for k in (dict(bias=b.half()), dict(residual=r.float()), dict(bias=b, out=r.half()), dict(bias=b, s=s.float())):
+        refused(lambda: call(**k), TypeError)
+    with pytest.raises(TypeError):
+        wq.dense_w4a16_gemm(x.half(), 64, w, s.repeat(2), bias=b.half(), k_perm=torch.zeros(256))

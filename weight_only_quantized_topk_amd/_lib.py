@@ -15,6 +15,7 @@ WQ_SCORE_SOFTMAX, WQ_SCORE_SIGMOID = 0, 1
 WQ_GROUP_MAX, WQ_GROUP_TOP2 = 0, 1
 WQ_STAGE_GATE_UP, WQ_STAGE_DOWN, WQ_STAGE_RAW = 0, 1, 2
 WQ_PACK_INTERLEAVE_GATE_UP = 1
+WQ_ACT_NONE, WQ_ACT_RELU, WQ_ACT_SILU, WQ_ACT_GELU, WQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
 WQ_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 EXPORTS = (
@@ -24,6 +25,7 @@ EXPORTS = (
     "moe_gemm_workspace_bytes", "moe_w4a16_gemm", "moe_w8a16_gemm", "moe_w8a16_gemm_noalloc",
     "sparse24_w4a16_gemm", "sparse24_w8a16_gemm", "wq_quantize_w8",
     "dense_gemm_workspace_bytes", "dense_w4a16_gemm", "dense_w8a16_gemm",
+    "dense_epilogue_workspace_bytes", "dense_w4a16_epilogue_gemm", "dense_w8a16_epilogue_gemm",
     "dense_lora_workspace_bytes", "dense_lora_gemm",
     "wq_kv_cache_write", "wq_kv_cache_read", "wq_paged_attention_workspace_bytes", "wq_paged_attention",
     "wq_pack_w4_bytes", "wq_pack_w8_bytes", "wq_pack_w4", "wq_pack_w8",
@@ -52,6 +54,15 @@ class WqMoeGemmDesc(C.Structure):
         ("d_out", C.c_void_p),
         ("d_workspace", C.c_void_p),
         ("workspace_bytes", C.c_size_t),
+    ]
+
+
+class WqEpilogue(C.Structure):
+    _fields_ = [
+        ("struct_size", C.c_size_t),
+        ("d_bias", C.c_void_p), ("d_residual", C.c_void_p),
+        ("residual_stride", C.c_int64),
+        ("activation", C.c_int),
     ]
 
 
@@ -117,6 +128,11 @@ def load():
     L.dense_gemm_workspace_bytes.restype = sz
     L.dense_w4a16_gemm.argtypes = [p, i, i, i, p, p, i, p, p, i, p, sz, p]
     L.dense_w8a16_gemm.argtypes = [p, i, i, i, p, p, p, i, p, sz, p]
+    epi = C.POINTER(WqEpilogue)
+    L.dense_epilogue_workspace_bytes.argtypes = [i, i, i, i, i]
+    L.dense_epilogue_workspace_bytes.restype = sz
+    L.dense_w4a16_epilogue_gemm.argtypes = [p, i, i, i, p, p, i, p, epi, p, i, p, sz, p]
+    L.dense_w8a16_epilogue_gemm.argtypes = [p, i, i, i, p, p, epi, p, i, p, sz, p]
     L.dense_lora_workspace_bytes.argtypes = [i, i, i, i, i]
     L.dense_lora_workspace_bytes.restype = sz
     L.dense_lora_gemm.argtypes = [p, i64, i, i, i, i, i, p, p, p, p, p, i64, i, p, sz, p]
@@ -148,7 +164,8 @@ def load():
               "moe_route_grouped_align", "wq_rms_norm", "moe_w4a16_gemm", "moe_w8a16_gemm",
               "moe_w8a16_gemm_noalloc", "sparse24_w4a16_gemm",
               "sparse24_w8a16_gemm",
-              "wq_quantize_w8", "dense_w4a16_gemm", "dense_w8a16_gemm", "dense_lora_gemm", "wq_kv_cache_write",
+              "wq_quantize_w8", "dense_w4a16_gemm", "dense_w8a16_gemm", "dense_lora_gemm",
+              "dense_w4a16_epilogue_gemm", "dense_w8a16_epilogue_gemm", "wq_kv_cache_write",
               "wq_kv_cache_read", "wq_paged_attention", "wq_pack_w4",
               "wq_pack_w8", "wq_pack_sparse24", "moe_fp8_w8a8_gemm", "moe_fp8_codes_gemm", "wq_pack_fp8"):
         getattr(L, fn).restype = i

@@ -1478,6 +1478,138 @@ wq_status wq_paged_attention(const wq_kv_cache* c, const void* d_q, int64_t q_st
 }
 
 // ---------------------------------------------------------------------------
+// the dense linear layer with an epilogue
+// ---------------------------------------------------------------------------
+namespace {
+struct EpilogueLayout {
+    bool rows;   // 1..128 rows in one launch
+    int ks;      // K slices through fp32 slabs
+    size_t off_gather, total;
+};
+EpilogueLayout epilogue_layout(int wbits, int M, int K, int N, bool act_order) {
+    EpilogueLayout L{};
+    L.rows = wq::dense_decode_supported(M, K);
+    L.ks = L.rows ? 1 : wq::dense_large_split(wbits, M, K, N);
+    size_t o = L.ks > 1 ? round256((size_t)L.ks * M * N * sizeof(float)) : 0;
+    L.off_gather = o;
+    if (act_order) o += round256((size_t)M * K * 2);
+    L.total = o;
+    return L;
+}
+
+const char* epilogue_sizes(int wbits, int M, int K, int N) {
+    if (M < 0 || K <= 0 || N <= 0) return "sizes must be positive (M >= 0)";
+    if (M > MAX_PAIRS || K > (1 << 24) || N > (1 << 24)) return "M, K or N > 2^24";
+    if (K % (wbits == 4 ? wq::WFmt<4>::KCHUNK : wq::WFmt<8>::KCHUNK)) return "K must be a multiple of 128 (int4) or 64 (int8)";
+    if (N % 16) return "N must be a multiple of 16";
+    if (!wq::dense_decode_supported(M, K) && !wq::prefill_fits((size_t)M + 128, K)) return "more than 4 GiB of activations";
+    if (M > 65535 * 64) return "more than 65535 * 64 rows";
+    return nullptr;
+}
+
+wq_status dense_epilogue(int wbits, const void* d_x, int M, int K, int N, const void* d_w, const void* d_scales,
+                         int group_size, const int32_t* d_k_perm, const wq_epilogue* e, void* d_y, int act_dtype,
+                         void* d_ws, size_t ws_bytes, void* stream, const char* who) {
+    WQ_REQUIRE(M >= 0 && K > 0 && N > 0, WQ_ERR_INVALID, "%s: bad sizes M %d K %d N %d", who, M, K, N);
+    WQ_REQUIRE(act_dtype == WQ_F16 || act_dtype == WQ_BF16, WQ_ERR_INVALID, "%s: bad act dtype", who);
+    if (wbits == 4) WQ_REQUIRE(act_dtype == WQ_F16, WQ_ERR_UNSUPPORTED, "%s: int4 path takes fp16 activations", who);
+    const char* bad = epilogue_sizes(wbits, M, K, N);
+    WQ_REQUIRE(!bad, WQ_ERR_UNSUPPORTED, "%s: %s", who, bad);
+    if (wbits == 4)
+        WQ_REQUIRE(group_size == 128 || group_size == -1, WQ_ERR_UNSUPPORTED, "%s: group_size %d", who, group_size);
+    WQ_REQUIRE(e != nullptr && e->struct_size == sizeof(wq_epilogue), WQ_ERR_INVALID,
+               "%s: epilogue is NULL or of another struct_size", who);
+    WQ_REQUIRE(e->activation >= WQ_ACT_NONE && e->activation <= WQ_ACT_GELU_TANH, WQ_ERR_INVALID, "%s: activation %d",
+               who, e->activation);
+    const bool act_order = d_k_perm != nullptr;
+    const EpilogueLayout L = epilogue_layout(wbits, M, K, N, act_order);
+    WQ_REQUIRE(ws_bytes >= L.total, WQ_ERR_INVALID, "%s: workspace %zu < required %zu", who, ws_bytes, L.total);
+    if (M == 0) return ok();
+    const int64_t rs = e->d_residual ? e->residual_stride : N;
+    WQ_REQUIRE(rs >= N && rs <= INT64_MAX / 4 / M, WQ_ERR_INVALID, "%s: residual row stride %lld (N %d)", who,
+               (long long)rs, N);
+    WQ_REQUIRE(rs % 8 == 0, WQ_ERR_UNSUPPORTED, "%s: the residual's row stride must be a multiple of 8", who);
+    const int groups = (wbits == 4 && group_size == 128) ? K / 128 : 1;
+    const Span8 in[6] = {{d_x, (int64_t)M * K * 2, "x"},
+                         {d_w, (int64_t)N * K * wbits / 8, "w_packed"},
+                         {d_scales, (int64_t)groups * N * 2, "scales"},
+                         {d_k_perm, (int64_t)K * 4, "k_perm"},
+                         {e->d_bias, (int64_t)N * 2, "bias"},
+                         {e->d_residual, ((int64_t)(M - 1) * rs + N) * 2, "residual"}};
+    const Span8 out[2] = {{d_y, (int64_t)M * N * 2, "y"}, {L.total ? d_ws : nullptr, (int64_t)L.total, "workspace"}};
+    for (int i = 0; i < 6; ++i)
+        if (in[i].p || i < 3) WQ_TRY(check_ptr(in[i].p, in[i].name));
+    WQ_TRY(check_ptr(d_y, "y"));
+    if (L.total) {
+        WQ_TRY(check_ptr(d_ws, "workspace"));
+        WQ_REQUIRE(reinterpret_cast<uintptr_t>(d_ws) % 256 == 0, WQ_ERR_INVALID, "%s: workspace not 256-byte aligned",
+                   who);
+    }
+    // y may be the residual
+    const bool in_place = e->d_residual == d_y && rs == N;
+    WQ_TRY(apart(out, 2, in, 5, who));
+    WQ_REQUIRE(in_place || !e->d_residual || !rows_overlap(d_y, (int64_t)N * 2, (int64_t)N * 2, e->d_residual, rs * 2,
+                                                           (int64_t)N * 2, M),
+               WQ_ERR_INVALID, "%s: y overlaps residual", who);
+    WQ_REQUIRE(!spans_overlap(out[1], in[5]) && !spans_overlap(out[0], out[1]), WQ_ERR_INVALID,
+               "%s: the workspace overlaps y or residual", who);
+    int cur = -1;
+    WQ_TRY(current_device(&cur));
+    for (const Span8& a : in)
+        if (a.p) WQ_TRY(check_dev(a.p, a.name, cur));
+    for (const Span8& a : out)
+        if (a.p) WQ_TRY(check_dev(a.p, a.name, cur));
+    hipStream_t s = (hipStream_t)stream;
+    const bool bf16 = act_dtype == WQ_BF16;
+    uint8_t* ws = static_cast<uint8_t*>(d_ws);
+    const uint16_t* x = static_cast<const uint16_t*>(d_x);
+    if (act_order) {
+        uint16_t* a1 = reinterpret_cast<uint16_t*>(ws + L.off_gather);
+        wq::launch_gather_columns(x, d_k_perm, M, K, a1, s);
+        WQ_TRY(after_launch(who));
+        x = a1;
+    }
+    const wq::Epilogue ep{static_cast<const uint16_t*>(e->d_bias),
+                          in_place ? nullptr : static_cast<const uint16_t*>(e->d_residual), rs, in_place,
+                          e->activation};
+    const uint8_t* w = static_cast<const uint8_t*>(d_w);
+    const uint16_t* sc = static_cast<const uint16_t*>(d_scales);
+    if (L.rows) wq::launch_dense_decode(wbits, bf16, x, M, K, N, w, sc, groups, static_cast<uint16_t*>(d_y), s, &ep);
+    else
+        wq::launch_dense_large(wbits, bf16, x, M, K, N, w, sc, groups, ep, reinterpret_cast<float*>(ws),
+                               static_cast<uint16_t*>(d_y), s);
+    return after_launch(who);
+}
+}  // namespace
+
+size_t dense_epilogue_workspace_bytes(int wbits, int M, int K, int N, int act_order) {
+    if ((wbits != 4 && wbits != 8) || M == 0 || epilogue_sizes(wbits, M, K, N)) return 0;
+    return epilogue_layout(wbits, M, K, N, act_order != 0).total;
+}
+
+wq_status dense_w4a16_epilogue_gemm(const void* d_x, int M, int K, int N, const void* d_w_packed, const void* d_scales,
+                                    int group_size, const int32_t* d_k_perm, const wq_epilogue* epilogue, void* d_y,
+                                    int act_dtype, void* d_workspace, size_t workspace_bytes, void* stream) {
+    try {
+        return dense_epilogue(4, d_x, M, K, N, d_w_packed, d_scales, group_size, d_k_perm, epilogue, d_y, act_dtype,
+                              d_workspace, workspace_bytes, stream, "dense_w4a16_epilogue_gemm");
+    } catch (...) {
+        return fail(WQ_ERR_HIP, "dense_w4a16_epilogue_gemm: unexpected exception");
+    }
+}
+
+wq_status dense_w8a16_epilogue_gemm(const void* d_x, int M, int K, int N, const void* d_w_packed, const void* d_scales,
+                                    const wq_epilogue* epilogue, void* d_y, int act_dtype, void* d_workspace,
+                                    size_t workspace_bytes, void* stream) {
+    try {
+        return dense_epilogue(8, d_x, M, K, N, d_w_packed, d_scales, -1, nullptr, epilogue, d_y, act_dtype,
+                              d_workspace, workspace_bytes, stream, "dense_w8a16_epilogue_gemm");
+    } catch (...) {
+        return fail(WQ_ERR_HIP, "dense_w8a16_epilogue_gemm: unexpected exception");
+    }
+}
+
+// ---------------------------------------------------------------------------
 wq_status wq_quantize_w8(const void* d_w, int64_t rows, int k, int dtype, int8_t* d_q, uint16_t* d_scales,
                          void* stream) {
     try {

@@ -13,17 +13,19 @@
 // small-batch kernel: int4 codes exact in fp16, the group scale applied to the
 // fp32 partial sum of each 128-channel chunk; int8 exact, the per-column scale
 // in the fp32 epilogue.  The NW partial sums are added in LDS in wave order and
-// rounded once to the activation type.
+// rounded once to the activation type, after bias, activation and residual
+// where the call has them (EPI).
 #include "common.hpp"
+#include "epilogue.hpp"
 #include "launch.hpp"
 
 namespace wq {
 
-template <int WBITS, bool BF16, int NW, int DEPTH>
+template <int WBITS, bool BF16, int NW, int DEPTH, bool EPI>
 __global__ __launch_bounds__(NW * 64) void dense_decode_kernel(const uint16_t* __restrict__ x, int M, int K, int N,
                                                                const uint8_t* __restrict__ w,
                                                                const uint16_t* __restrict__ s, int groups,
-                                                               uint16_t* __restrict__ y) {
+                                                               uint16_t* __restrict__ y, Epilogue ep) {
     constexpr int KCHUNK = WFmt<WBITS>::KCHUNK;
     constexpr int KSTEPS = KCHUNK / 32;
     extern __shared__ __attribute__((aligned(16))) uint8_t xs_dyn[];
@@ -108,6 +110,10 @@ __global__ __launch_bounds__(NW * 64) void dense_decode_kernel(const uint16_t* _
                 o[r] = acc[r];
                 if constexpr (WBITS == 8) o[r] *= act_to_f32<BF16>(s[n0 + r]);
             }
+            if constexpr (EPI) {
+                finish4<BF16>(ep, f32x4{o[0], o[1], o[2], o[3]}, m, n0, N, y);
+                return;
+            }
             u32x2 stv;
             stv[0] = (uint32_t)f32_to_act<BF16>(o[0]) | ((uint32_t)f32_to_act<BF16>(o[1]) << 16);
             stv[1] = (uint32_t)f32_to_act<BF16>(o[2]) | ((uint32_t)f32_to_act<BF16>(o[3]) << 16);
@@ -143,11 +149,11 @@ constexpr int DS_ROWB = 2 * 128 + 16;  // LDS bytes per token row of one chunk (
 #define DS_R4 4
 #endif
 
-template <int WBITS, bool BF16, int NWV, int PF, int R>
+template <int WBITS, bool BF16, int NWV, int PF, int R, bool EPI>
 __global__ __launch_bounds__(NWV * 64) void dense_stream_kernel(const uint16_t* __restrict__ x, int M, int K, int N,
                                                                 const uint8_t* __restrict__ w,
                                                                 const uint16_t* __restrict__ s, int groups,
-                                                                uint16_t* __restrict__ y) {
+                                                                uint16_t* __restrict__ y, Epilogue ep) {
     constexpr int KCHUNK = WFmt<WBITS>::KCHUNK;
     constexpr int KSTEPS = KCHUNK / 32;
     constexpr int NT = NWV * 64;
@@ -266,6 +272,10 @@ __global__ __launch_bounds__(NWV * 64) void dense_stream_kernel(const uint16_t* 
                     o[i] = acc[r][i];
                     if constexpr (WBITS == 8) o[i] *= act_to_f32<BF16>(s[n0 + i]);
                 }
+                if constexpr (EPI) {
+                    finish4<BF16>(ep, f32x4{o[0], o[1], o[2], o[3]}, m, n0, N, y);
+                    continue;
+                }
                 u32x2 stv;
                 stv[0] = (uint32_t)f32_to_act<BF16>(o[0]) | ((uint32_t)f32_to_act<BF16>(o[1]) << 16);
                 stv[1] = (uint32_t)f32_to_act<BF16>(o[2]) | ((uint32_t)f32_to_act<BF16>(o[3]) << 16);
@@ -287,45 +297,53 @@ static bool dense_rows_in_lds(int M, int K) { return M >= 1 && M <= 2 && dense_d
 #endif
 bool dense_decode_supported(int M, int K) { return dense_rows_in_lds(M, K) || (M >= 1 && M <= DS_MAX_ROWS); }
 
-template <int WBITS, bool BF16>
+template <int WBITS, bool BF16, bool EPI>
 static void launch_dd(const uint16_t* x, int M, int K, int N, const uint8_t* w, const uint16_t* s, int groups,
-                      uint16_t* y, hipStream_t st) {
+                      uint16_t* y, const Epilogue& ep, hipStream_t st) {
     constexpr int NW = 4, DEPTH = 4;
     const size_t lds = dense_decode_lds(M, K);
-    auto kern = dense_decode_kernel<WBITS, BF16, NW, DEPTH>;
+    auto kern = dense_decode_kernel<WBITS, BF16, NW, DEPTH, EPI>;
     if (lds + sizeof(f32x4) * 64 * NW > 65536)
         (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)lds);
-    hipLaunchKernelGGL(kern, dim3(N / TILE_ROWS), dim3(NW * 64), lds, st, x, M, K, N, w, s, groups, y);
+    hipLaunchKernelGGL(kern, dim3(N / TILE_ROWS), dim3(NW * 64), lds, st, x, M, K, N, w, s, groups, y, ep);
 }
 
-template <int WBITS, bool BF16, int NWV, int PF, int R>
+template <int WBITS, bool BF16, int NWV, int PF, int R, bool EPI>
 static void launch_ds_r(const uint16_t* x, int M, int K, int N, const uint8_t* w, const uint16_t* s, int groups,
-                        uint16_t* y, hipStream_t st) {
+                        uint16_t* y, const Epilogue& ep, hipStream_t st) {
     const dim3 grid((N / TILE_ROWS + NWV - 1) / NWV, (M + 16 * R - 1) / (16 * R));
-    hipLaunchKernelGGL((dense_stream_kernel<WBITS, BF16, NWV, PF, R>), grid, dim3(NWV * 64), 0, st, x, M, K, N, w, s,
-                       groups, y);
+    hipLaunchKernelGGL((dense_stream_kernel<WBITS, BF16, NWV, PF, R, EPI>), grid, dim3(NWV * 64), 0, st, x, M, K, N,
+                       w, s, groups, y, ep);
 }
 
-template <int WBITS, bool BF16>
+template <int WBITS, bool BF16, bool EPI>
 static void launch_ds(const uint16_t* x, int M, int K, int N, const uint8_t* w, const uint16_t* s, int groups,
-                      uint16_t* y, hipStream_t st) {
-    if (M <= 16) launch_ds_r<WBITS, BF16, DS_NW1, DS_PF1, 1>(x, M, K, N, w, s, groups, y, st);
-    else if (M <= 32) launch_ds_r<WBITS, BF16, DS_NW2, 6, 2>(x, M, K, N, w, s, groups, y, st);
-    else launch_ds_r<WBITS, BF16, DS_NW4, DS_PF4, DS_R4>(x, M, K, N, w, s, groups, y, st);
+                      uint16_t* y, const Epilogue& ep, hipStream_t st) {
+    if (M <= 16) launch_ds_r<WBITS, BF16, DS_NW1, DS_PF1, 1, EPI>(x, M, K, N, w, s, groups, y, ep, st);
+    else if (M <= 32) launch_ds_r<WBITS, BF16, DS_NW2, 6, 2, EPI>(x, M, K, N, w, s, groups, y, ep, st);
+    else launch_ds_r<WBITS, BF16, DS_NW4, DS_PF4, DS_R4, EPI>(x, M, K, N, w, s, groups, y, ep, st);
+}
+
+template <int WBITS, bool BF16, bool EPI>
+static void launch_dense_rows(const uint16_t* x, int M, int K, int N, const uint8_t* w, const uint16_t* s, int groups,
+                              uint16_t* y, const Epilogue& ep, hipStream_t st) {
+    if (dense_rows_in_lds(M, K)) launch_dd<WBITS, BF16, EPI>(x, M, K, N, w, s, groups, y, ep, st);
+    else launch_ds<WBITS, BF16, EPI>(x, M, K, N, w, s, groups, y, ep, st);
+}
+
+template <bool EPI>
+static void launch_dense_type(int wbits, bool bf16, const uint16_t* x, int M, int K, int N, const uint8_t* w,
+                              const uint16_t* s, int groups, uint16_t* y, const Epilogue& ep, hipStream_t st) {
+    if (wbits == 4) launch_dense_rows<4, false, EPI>(x, M, K, N, w, s, groups, y, ep, st);
+    else if (bf16) launch_dense_rows<8, true, EPI>(x, M, K, N, w, s, groups, y, ep, st);
+    else launch_dense_rows<8, false, EPI>(x, M, K, N, w, s, groups, y, ep, st);
 }
 
 void launch_dense_decode(int wbits, bool bf16, const uint16_t* x, int M, int K, int N, const uint8_t* w,
-                         const uint16_t* s, int groups, uint16_t* y, hipStream_t st) {
-    if (dense_rows_in_lds(M, K)) {
-        if (wbits == 4) launch_dd<4, false>(x, M, K, N, w, s, groups, y, st);
-        else if (bf16) launch_dd<8, true>(x, M, K, N, w, s, groups, y, st);
-        else launch_dd<8, false>(x, M, K, N, w, s, groups, y, st);
-    } else {
-        if (wbits == 4) launch_ds<4, false>(x, M, K, N, w, s, groups, y, st);
-        else if (bf16) launch_ds<8, true>(x, M, K, N, w, s, groups, y, st);
-        else launch_ds<8, false>(x, M, K, N, w, s, groups, y, st);
-    }
+                         const uint16_t* s, int groups, uint16_t* y, hipStream_t st, const Epilogue* ep) {
+    if (ep) launch_dense_type<true>(wbits, bf16, x, M, K, N, w, s, groups, y, *ep, st);
+    else launch_dense_type<false>(wbits, bf16, x, M, K, N, w, s, groups, y, Epilogue{}, st);
 }
 
 }  // namespace wq

@@ -24,6 +24,7 @@
 // Faster Kernels", vLLM issue 3289, the GEMV/GEMM mix and the batch-dimension
 // heuristics).
 #include "common.hpp"
+#include "epilogue.hpp"
 #include "launch.hpp"
 #include "route_common.hpp"
 
@@ -500,6 +501,28 @@ void launch_gather_perm(const uint16_t* x, const int32_t* perm, const int32_t* s
                        M * topk, k_in, block_size, a1);
 }
 
+// the same for the rows of one weight matrix
+__global__ __launch_bounds__(256) void gather_columns_kernel(const uint16_t* __restrict__ x,
+                                                             const int32_t* __restrict__ perm, int K,
+                                                             uint16_t* __restrict__ a1) {
+    const uint16_t* src = x + (size_t)blockIdx.x * K;
+    uint16_t* dst = a1 + (size_t)blockIdx.x * K;
+    for (int k = threadIdx.x * 8; k < K; k += 256 * 8) {
+        const u32x4 i0 = ldg128(perm + k);
+        const u32x4 i1 = ldg128(perm + k + 4);
+        u32x4 v;
+        v[0] = (uint32_t)src[i0[0]] | ((uint32_t)src[i0[1]] << 16);
+        v[1] = (uint32_t)src[i0[2]] | ((uint32_t)src[i0[3]] << 16);
+        v[2] = (uint32_t)src[i1[0]] | ((uint32_t)src[i1[1]] << 16);
+        v[3] = (uint32_t)src[i1[2]] | ((uint32_t)src[i1[3]] << 16);
+        *reinterpret_cast<u32x4*>(dst + k) = v;
+    }
+}
+
+void launch_gather_columns(const uint16_t* x, const int32_t* perm, int M, int K, uint16_t* a1, hipStream_t s) {
+    hipLaunchKernelGGL(gather_columns_kernel, dim3(M), dim3(256), 0, s, x, perm, K, a1);
+}
+
 // ---------------------------------------------------------------------------
 // top-k weighted combine: out[m, c] = sum_{j<topk} sum_{z<ksplit} Y[z][m*topk+j, c]
 // (Y already carries the routed weight; z runs over the K slices of a split
@@ -576,6 +599,25 @@ __global__ __launch_bounds__(256) void combine_act_kernel(const uint16_t* __rest
     st[0] = (uint32_t)f32_to_act<BF16>(acc[0]) | ((uint32_t)f32_to_act<BF16>(acc[1]) << 16);
     st[1] = (uint32_t)f32_to_act<BF16>(acc[2]) | ((uint32_t)f32_to_act<BF16>(acc[3]) << 16);
     *reinterpret_cast<u32x2*>(out + m * n + c) = st;
+}
+
+// a dense projection's K slices and its epilogue
+template <bool BF16>
+__global__ __launch_bounds__(256) void combine_epilogue_kernel(const float* __restrict__ slabs, int M, int N, int ks,
+                                                               Epilogue ep, uint16_t* __restrict__ y) {
+    const size_t q = (size_t)blockIdx.x * 256 + threadIdx.x;  // 4 outputs each
+    const size_t slab = (size_t)M * N;
+    if (q * 4 >= slab) return;
+    f32x4 acc = *reinterpret_cast<const f32x4*>(slabs + q * 4);
+    for (int z = 1; z < ks; ++z) acc += *reinterpret_cast<const f32x4*>(slabs + z * slab + q * 4);
+    finish4<BF16>(ep, acc, (int64_t)(q * 4 / N), (int)(q * 4 % N), N, y);
+}
+
+void launch_combine_epilogue(const float* slabs, int M, int N, int ks, bool bf16, const Epilogue& ep, uint16_t* y,
+                             hipStream_t s) {
+    const dim3 grid((unsigned)(((size_t)M * N / 4 + 255) / 256));
+    if (bf16) hipLaunchKernelGGL(combine_epilogue_kernel<true>, grid, dim3(256), 0, s, slabs, M, N, ks, ep, y);
+    else hipLaunchKernelGGL(combine_epilogue_kernel<false>, grid, dim3(256), 0, s, slabs, M, N, ks, ep, y);
 }
 
 void launch_combine_act(const uint16_t* y, int M, int topk, int n, bool bf16, uint16_t* out, hipStream_t s) {

@@ -32,10 +32,16 @@
 //    (one uniform branch per tile), and when they fit in the slice's first
 //    half the LDS reads of the second half too.
 //
+// One weight matrix with an epilogue (STAGE_DENSE) is the same kernel without
+// the sort: token row p is row p of x, the last workgroup's missing weight tiles
+// read the last one and store nothing (n_out any multiple of 16), and the float32
+// sums go through bias, activation and residual to y.
+//
 // DOWN may split K over gridDim.z slices when its output grid is too small to
 // fill the chip: slice z writes its partial sums to its own fp32 slab of Y and
 // the combine kernel adds the slabs in ascending order (deterministic).
 #include "common.hpp"
+#include "epilogue.hpp"
 #include "launch.hpp"
 
 #include <algorithm>
@@ -73,10 +79,14 @@ __global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(GemmArgs g) 
     const int ntile = blockIdx.x, mtile = blockIdx.y;
     const int T = g.M * g.topk;
     const int row0 = mtile * BM;
-    if (row0 >= *g.ntpp) return;
-    const int e = g.expert_ids[row0 / g.block_size];
+    constexpr bool DENSE = STAGE == STAGE_DENSE;
+    int e = 0;
+    if constexpr (!DENSE) {
+        if (row0 >= *g.ntpp) return;
+        e = g.expert_ids[row0 / g.block_size];
+    }
 
-    if (g.sorted[row0] >= T) {  // a slice of pad rows only (blocks larger than BM)
+    if (!DENSE && g.sorted[row0] >= T) {  // a slice of pad rows only (blocks larger than BM)
         if constexpr (STAGE == STAGE_GATE_UP) {
             const int N = g.n_out / 2;
             for (int k = tid; k < BM * (BN / 2); k += NT)
@@ -100,8 +110,12 @@ __global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(GemmArgs g) 
     // piece's address a 32-bit offset from the activations' base, which frees
     // the vector registers 64-bit addresses would hold (int4 large-batch
     // Mixtral gate/up 1.83 -> 1.77 ms at M = 4096).
-    const int rt0 = ntile * (BN / TILE_ROWS) + __builtin_amdgcn_readfirstlane(wave) * RT;  // first tile of the wave
+    const int rt_own = ntile * (BN / TILE_ROWS) + __builtin_amdgcn_readfirstlane(wave) * RT;  // first tile of the wave
+    const int tiles_left = g.n_out / TILE_ROWS - rt_own;                                       // STAGE_DENSE: may be < RT
+    const int rt0 = DENSE && tiles_left < 1 ? g.n_out / TILE_ROWS - 1 : rt_own;
     const int tile_stride = C * CHUNK_BYTES;
+    // tile t of the wave, or its last (or the matrix's)
+    auto tile_at = [&](int t) { return DENSE ? max(0, min(t, tiles_left - 1)) : t; };
     const __amdgpu_buffer_rsrc_t wres = make_rsrc(g.w + (size_t)e * expert_bytes + (size_t)rt0 * tile_stride);
     const int wlane = lane * 16;
     const uint16_t* ssrc = se + rt0 * TILE_ROWS + (lane & 15);  // int4: scale of this lane's row
@@ -112,13 +126,13 @@ __global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(GemmArgs g) 
     // raw weights (and int4 group scale) of weight tile t for one K step
     auto wload_t = [&](int step, int t) {
         if constexpr (WBITS == 8) {
-            w8[t] = __builtin_amdgcn_raw_buffer_load_b128(wres, wlane, t * tile_stride + step * CHUNK_BYTES, 0);
+            w8[t] = __builtin_amdgcn_raw_buffer_load_b128(wres, wlane, tile_at(t) * tile_stride + step * CHUNK_BYTES, 0);
         } else {
             const int c = step >> 1, half = step & 1;  // a 128-channel chunk spans two K steps
             // cached: the token tiles of an expert re-read its weight tiles
-            w4[t] = __builtin_amdgcn_raw_buffer_load_b64(wres, wlane, t * tile_stride + c * CHUNK_BYTES + 8 * half, 0);
+            w4[t] = __builtin_amdgcn_raw_buffer_load_b64(wres, wlane, tile_at(t) * tile_stride + c * CHUNK_BYTES + 8 * half, 0);
             const int grp = g.groups > 1 ? c : 0;
-            sc[t] = ssrc[(size_t)grp * g.n_out + t * TILE_ROWS];
+            sc[t] = ssrc[(size_t)grp * g.n_out + tile_at(t) * TILE_ROWS];
         }
     };
     auto wload = [&](int step) {
@@ -133,8 +147,13 @@ __global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(GemmArgs g) 
     for (int i = 0; i < TPIECES; ++i) {
         const int id = tid + NT * i;
         const int p = row0 + (id >> 3);
-        const int pair = g.sorted[p];
-        const int src = g.a_direct ? p : (pair < T ? pair / g.topk : 0);
+        int src;
+        if constexpr (DENSE) {
+            src = min(p, g.M - 1);
+        } else {
+            const int pair = g.sorted[p];
+            src = g.a_direct ? p : (pair < T ? pair / g.topk : 0);
+        }
         toff[i] = (uint32_t)src * (uint32_t)(g.k_in * 2) + (id & 7) * 16;
     }
     u32x4 tv[TPIECES];
@@ -159,7 +178,10 @@ __global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(GemmArgs g) 
     const int brow = lane & 15, g4 = lane >> 4;
     int jact = 0;  // token tiles holding a valid row (a prefix: the alignment pads each expert at the end)
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) jact += __builtin_amdgcn_readfirstlane(g.sorted[row0 + 16 * j]) < T ? 1 : 0;
+    for (int j = 0; j < TJ; ++j) {
+        if constexpr (DENSE) jact += row0 + 16 * j < g.M ? 1 : 0;
+        else jact += __builtin_amdgcn_readfirstlane(g.sorted[row0 + 16 * j]) < T ? 1 : 0;
+    }
     // the MFMAs of token tiles j >= jact (padding only) are skipped, one
     // uniform branch per tile; the second half's LDS reads too when jact <= TJ/2
     // (DeepSeek-V2 shape, 4096 tokens: 75 of its 293 token tiles hold at most 16 rows)
@@ -257,6 +279,27 @@ __global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(GemmArgs g) 
 
     // epilogue
     float* yslab = nullptr;
+    if constexpr (DENSE) {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+            const int m = row0 + 16 * j + brow;
+            if (m < g.M) {
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    if (t >= tiles_left) continue;
+                    const int n0 = (rt0 + t) * TILE_ROWS + 4 * g4;
+                    f32x4 o = acc[t][j];
+                    if constexpr (WBITS == 8) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) o[r] *= act_to_f32<BF16>(se[n0 + r]);
+                    }
+                    if (gridDim.z == 1) finish4<BF16>(g.ep, o, m, n0, g.n_out, static_cast<uint16_t*>(g.out));
+                    else *reinterpret_cast<f32x4*>(g.slabs + ((size_t)blockIdx.z * g.M + m) * g.n_out + n0) = o;
+                }
+            }
+        }
+        return;
+    }
     if constexpr (STAGE != STAGE_GATE_UP)
         yslab = static_cast<float*>(g.out) + (size_t)blockIdx.z * ((size_t)T * g.n_out);
 #pragma unroll
@@ -428,6 +471,49 @@ int launch_gemm_prefill(int wbits, bool bf16, int stage, const GemmArgs& g, hipS
     else if (bf16) launch_prefill_s<8, true>(stage, g, ksplit, s);
     else launch_prefill_s<8, false>(stage, g, ksplit, s);
     return ksplit;
+}
+// ------------------------------------------------------- one weight matrix
+static bool dense_large_small_tiles(int M) { return M <= 192; }
+
+template <int WBITS, bool BF16, int NW, int RT, int BM, int OCC>
+static void launch_dense_cfg(const GemmArgs& g, int ksplit, hipStream_t s) {
+    constexpr int BN = NW * RT * 16;
+    const dim3 grid((g.n_out + BN - 1) / BN, (g.M + BM - 1) / BM, ksplit);
+    hipLaunchKernelGGL((gemm_prefill_kernel<WBITS, BF16, STAGE_DENSE, NW, RT, BM, OCC>), grid, dim3(NW * 64), 0, s, g);
+}
+
+int dense_large_split(int wbits, int M, int K, int N) {
+    const int bs = dense_large_small_tiles(M) ? 64 : 128;
+    return prefill_down_split(M, 1, (N + 127) / 128 * 128, K, bs);
+}
+
+template <int WBITS, bool BF16>
+static void launch_dense_shape(const GemmArgs& g, int ksplit, hipStream_t s) {
+    if (dense_large_small_tiles(g.M)) launch_dense_cfg<WBITS, BF16, 4, 2, 64, 3>(g, ksplit, s);
+    else if (g.n_out % 512 == 0) launch_dense_cfg<WBITS, BF16, 8, 4, 128, 1>(g, ksplit, s);
+    else launch_dense_cfg<WBITS, BF16, 4, 2, 128, 3>(g, ksplit, s);
+}
+
+void launch_dense_large(int wbits, bool bf16, const uint16_t* x, int M, int K, int N, const uint8_t* w,
+                        const uint16_t* s, int groups, const Epilogue& ep, float* slabs, uint16_t* y, hipStream_t st) {
+    GemmArgs g{};
+    g.a = x;
+    g.w = w;
+    g.s = s;
+    g.out = y;
+    g.M = M;
+    g.topk = 1;
+    g.E = 1;
+    g.n_out = N;
+    g.k_in = K;
+    g.groups = groups;
+    g.slabs = slabs;
+    g.ep = ep;
+    const int ks = dense_large_split(wbits, M, K, N);
+    if (wbits == 4) launch_dense_shape<4, false>(g, ks, st);
+    else if (bf16) launch_dense_shape<8, true>(g, ks, st);
+    else launch_dense_shape<8, false>(g, ks, st);
+    if (ks > 1) launch_combine_epilogue(slabs, M, N, ks, bf16, ep, y, st);
 }
 #endif  // WQ_PREFILL_KERNEL_ONLY
 

@@ -11,6 +11,7 @@ namespace wq {
 constexpr int STAGE_GATE_UP = 0;
 constexpr int STAGE_DOWN = 1;
 constexpr int STAGE_RAW = 2;
+constexpr int STAGE_DENSE = 3;  // large-batch kernel of one weight matrix, with an epilogue
 
 // Packed weight geometry: tiles of 16 output rows; a chunk of one tile holds
 // 64 lanes x 16 bytes = 1 KiB and spans KCHUNK input channels.
@@ -81,6 +82,17 @@ struct LoraArgs {
 int lora_k_slices(int M, int K, int N, int R);
 void launch_lora(const LoraArgs& g, bool bf16, hipStream_t s);
 
+// what a dense projection does to its float32 sums (epilogue.hpp): y = f(sum +
+// bias) + residual, rounded once
+constexpr int ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4;
+struct Epilogue {
+    const uint16_t* bias;      // [N], or null
+    const uint16_t* residual;  // [M, N], or null
+    int64_t r_stride;          // in elements
+    int in_place;              // the residual is y itself (residual null): read through y
+    int act;
+};
+
 struct GemmArgs {
     const uint16_t* a;        // activations (x, gathered x, or H), 16-bit
     const uint8_t* w;         // packed weights, all experts
@@ -96,6 +108,9 @@ struct GemmArgs {
     int a_direct;             // 1: A row = sorted position; 0: A row = token of the pair
     int cap;
     int y_act;                // large-batch DOWN without a K split: Y rows in the activation type
+    // STAGE_DENSE (x in a, y [M, n_out] in out)
+    float* slabs;             // a K slice each [M, n_out], where K is split
+    Epilogue ep;              // applied where it is not
 };
 
 // ---------------------------------------------------------------------------
@@ -211,6 +226,16 @@ int prefill_down_split_max(int T, int E, int n_out, int k_in);
 // returns the number of K slices (Y slabs) it wrote
 int launch_gemm_prefill(int wbits, bool bf16, int stage, const GemmArgs& g, hipStream_t s);
 
+// one weight matrix with an epilogue, more rows than dense_decode_supported
+// takes (gemm_prefill.hip): K slices (and the fp32 slabs [ks][M, N] that they
+// are added through) and the launches
+int dense_large_split(int wbits, int M, int K, int N);
+void launch_dense_large(int wbits, bool bf16, const uint16_t* x, int M, int K, int N, const uint8_t* w,
+                        const uint16_t* s, int groups, const Epilogue& ep, float* slabs, uint16_t* y, hipStream_t st);
+// y = f(sum over ks slabs [M, N] in ascending order + bias) + residual
+void launch_combine_epilogue(const float* slabs, int M, int N, int ks, bool bf16, const Epilogue& ep, uint16_t* y,
+                             hipStream_t s);
+
 // the routing arrays of a dense layer (E = 1, top-1): sorted = 0..M-1 then pad
 // ids M up to cap, expert 0 per block, ntpp = M rounded up to BS, weights 1
 void launch_identity_route(int M, int cap, int BS, int32_t* sorted, int32_t* expert_ids, int32_t* ntpp, float* w,
@@ -220,6 +245,8 @@ void launch_identity_route(int M, int cap, int BS, int32_t* sorted, int32_t* exp
 void launch_gather_perm(const uint16_t* x, const int32_t* perm, const int32_t* sorted, const int32_t* expert_ids,
                         const int32_t* ntpp, int M, int topk, int k_in, int block_size, int cap, uint16_t* a1,
                         hipStream_t s);
+// A1[m, k'] = x[m, perm[k']] (one weight matrix)
+void launch_gather_columns(const uint16_t* x, const int32_t* perm, int M, int K, uint16_t* a1, hipStream_t s);
 // out[m, c] = sum_j sum_z Y[z][m*topk + j, c] over top-k slots j and K slices z
 // (ascending, fp32), rounded to act; slab z starts at y + z * M*topk*n
 void launch_combine_act(const uint16_t* y, int M, int topk, int n, bool bf16, uint16_t* out, hipStream_t s);
@@ -233,7 +260,7 @@ void launch_sparse24(int bits, const uint16_t* x, int M, int K, int N, const uin
 // dense single-expert linear at 1..4 token rows (rows staged in LDS, at most 96 KiB)
 bool dense_decode_supported(int M, int K);
 void launch_dense_decode(int wbits, bool bf16, const uint16_t* x, int M, int K, int N, const uint8_t* w,
-                         const uint16_t* s, int groups, uint16_t* y, hipStream_t st);
+                         const uint16_t* s, int groups, uint16_t* y, hipStream_t st, const Epilogue* ep = nullptr);
 
 // ExpertsInt8 load-time quantizer: rows of k 16-bit weights -> int8 codes and
 // one 16-bit scale per row

@@ -20,12 +20,12 @@ import numpy as np
 from . import _lib
 from ._lib import (WQ_BF16, WQ_E4M3, WQ_F16, WQ_F32, WQ_GROUP_MAX, WQ_GROUP_TOP2, WQ_PACK_INTERLEAVE_GATE_UP,
                    WQ_SCORE_SIGMOID, WQ_SCORE_SOFTMAX, WQ_STAGE_DOWN, WQ_STAGE_GATE_UP, WQ_STAGE_RAW,
-                   WqKvCache, WqMoeGemmDesc, check, load)
+                   WqEpilogue, WqKvCache, WqMoeGemmDesc, check, load)
 
 __all__ = [
     "moe_route", "moe_align", "moe_route_align", "moe_align_capacity", "moe_gemm_workspace_bytes", "moe_w4a16_gemm", "moe_w8a16_gemm",
     "moe_route_gate_up",
-    "moe_w8a16_gemm_noalloc", "sparse24_w4a16_gemm", "sparse24_w8a16_gemm", "quantize_w8", "dense_gemm_workspace_bytes", "dense_w4a16_gemm", "dense_w8a16_gemm",
+    "moe_w8a16_gemm_noalloc", "sparse24_w4a16_gemm", "sparse24_w8a16_gemm", "quantize_w8", "dense_gemm_workspace_bytes", "dense_epilogue_workspace_bytes", "dense_w4a16_gemm", "dense_w8a16_gemm",
     "pack_w4", "pack_w8", "pack_sparse24", "act_code", "moe_fp8_gemm_workspace_bytes", "moe_fp8_w8a8_gemm",
     "pack_fp8", "moe_route_grouped", "moe_route_grouped_align", "rms_norm", "RmsNormOut", "moe_fp8_codes_gemm",
     "Lora", "pack_lora", "dense_lora_gemm", "dense_lora_workspace_bytes",
@@ -609,6 +609,69 @@ def _lora_call(sizes, x, adapter_ids, a, b, scales, y, workspace, stream):
     return y
 
 
+_ACTIVATION = {None: _lib.WQ_ACT_NONE, "relu": _lib.WQ_ACT_RELU, "silu": _lib.WQ_ACT_SILU, "gelu": _lib.WQ_ACT_GELU,
+               "gelu_tanh": _lib.WQ_ACT_GELU_TANH}
+
+
+def dense_epilogue_workspace_bytes(wbits: int, M: int, K: int, N: int, act_order: bool = False) -> int:
+    _int32(M=M, K=K, N=N)
+    return int(load().dense_epilogue_workspace_bytes(wbits, M, K, N, int(bool(act_order))))
+
+
+def _dense_epilogue(wbits, x, N, w_packed, scales, group_size, k_perm, out, workspace, stream, lora, bias, activation,
+                    residual):
+    """The dense call that has a bias, an activation or a residual."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K], got %s" % list(x.shape))
+    (M, K), dt, dev = x.shape, x.dtype, x.device
+    act = act_code(dt)
+    _int32(M=M, K=K, N=N)
+    same = (dt,)
+    _check(x, "x", (M, K), same)
+    if activation not in _ACTIVATION:
+        raise ValueError("activation must be one of %s, got %r" % (list(_ACTIVATION), activation))
+    if lora is not None and activation is not None:
+        raise ValueError("an activation beside adapters: they are added to the output, not before it")
+    # (uint8, int8: the packers' bytes; 16-bit scales in the activation type or as its bits)
+    _holds(w_packed, "w_packed", N * K * wbits // 8, (torch.uint8, torch.int8))
+    _holds(scales, "scales", N * (K // 128 if group_size == 128 else 1), (dt, torch.int16, torch.uint16))
+    if k_perm is not None:
+        _holds(k_perm, "k_perm", K, (torch.int32,))
+    e = WqEpilogue(C.sizeof(WqEpilogue), None, None, 0, _ACTIVATION[activation])
+    if bias is not None:
+        _check(bias, "bias", (N,), same, dev)
+        e.d_bias = bias.data_ptr()
+    if residual is not None:
+        _check(residual, "residual", (M, N), same, dev, row_stride=True)
+        e.d_residual, e.residual_stride = residual.data_ptr(), _row_stride(residual)
+    new = []
+    if out is None:
+        new.append(out := _alloc(stream, torch.empty, (M, N), dtype=dt, device=dev))
+    else:
+        _check(out, "out", (M, N), same, dev)
+    sizes = None if lora is None else _lora_sizes(x, *lora, out)  # before anything is launched
+    L = load()
+    if workspace is None:
+        nb = L.dense_epilogue_workspace_bytes(wbits, M, K, N, int(k_perm is not None))
+        if nb:
+            workspace = _alloc(stream, torch.empty, nb, dtype=torch.uint8, device=dev)
+    elif not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be contiguous on %s" % dev)
+    tail = (C.byref(e), out.data_ptr(), act, _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    if wbits == 4:
+        check(L.dense_w4a16_epilogue_gemm(x.data_ptr(), M, K, N, _ptr(w_packed), _ptr(scales), group_size, _ptr(k_perm),
+                                          *tail), "dense_w4a16_epilogue_gemm")
+    else:
+        check(L.dense_w8a16_epilogue_gemm(x.data_ptr(), M, K, N, _ptr(w_packed), _ptr(scales), *tail),
+              "dense_w8a16_epilogue_gemm")
+    if lora is not None:
+        _lora_call(sizes, x, *lora, out, None, stream)
+    _keep_for(stream, *new)
+    return out
+
+
 def _dense(fn, x, N, w_packed, scales, extra, out, workspace, stream, act_order, lora):
     torch = _torch()
     M, K = x.shape
@@ -633,17 +696,28 @@ def _dense(fn, x, N, w_packed, scales, extra, out, workspace, stream, act_order,
 
 
 def dense_w4a16_gemm(x, N: int, w_packed, scales, group_size: int = 128, k_perm=None, out=None, workspace=None,
-                     stream=None, lora: Optional[Lora] = None):
+                     stream=None, lora: Optional[Lora] = None, bias=None, activation: Optional[str] = None,
+                     residual=None):
     """Dense int4 linear: x [M, K] fp16 (device) -> y [M, N] fp16, weights
-    packed by pack_w4 with E = 1; lora: the rows' adapters, added to y."""
+    packed by pack_w4 with E = 1; lora: the rows' adapters, added to y.  With a
+    bias [N], an activation ("relu", "silu", "gelu", "gelu_tanh") or a residual
+    [M, N] (rows may be strided; may be out): y = activation(x W^T + bias) +
+    residual, rounded once (workspace: dense_epilogue_workspace_bytes)."""
+    if bias is not None or activation is not None or residual is not None:
+        return _dense_epilogue(4, x, N, w_packed, scales, group_size, k_perm, out, workspace, stream, lora, bias,
+                               activation, residual)
     return _dense(load().dense_w4a16_gemm, x, N, w_packed, scales, (group_size, _ptr(k_perm)), out, workspace,
                   stream, k_perm is not None, lora)
 
 
 def dense_w8a16_gemm(x, N: int, w_packed, scales, out=None, workspace=None, stream=None,
-                     lora: Optional[Lora] = None):
+                     lora: Optional[Lora] = None, bias=None, activation: Optional[str] = None, residual=None):
     """Dense int8 linear: x [M, K] bf16/fp16 (device) -> y [M, N], weights
-    packed by pack_w8 with E = 1; lora: the rows' adapters, added to y."""
+    packed by pack_w8 with E = 1; lora: the rows' adapters, added to y; bias,
+    activation and residual as for dense_w4a16_gemm."""
+    if bias is not None or activation is not None or residual is not None:
+        return _dense_epilogue(8, x, N, w_packed, scales, -1, None, out, workspace, stream, lora, bias, activation,
+                               residual)
     return _dense(load().dense_w8a16_gemm, x, N, w_packed, scales, (), out, workspace, stream, False, lora)
 
 
