@@ -1369,12 +1369,12 @@ static AttnLayout attn_layout(int B, int heads, int kv_heads, int head_dim, int 
     int64_t most = (int64_t)table_width * page_size;
     if (window > 0) most = std::min<int64_t>(most, (int64_t)window + wq::KV_TOKENS - 1);  // it begins anywhere in 16
     AttnLayout L{};
-    L.splits = wq::paged_attn_splits(B, heads, kv_heads, most);
+    L.splits = wq::paged_attn_splits(B, heads, kv_heads, head_dim, most);
     if (L.splits == 0) return L;
-    const size_t n = (size_t)(B + L.splits) * heads;
+    const size_t n = (size_t)2 * L.splits * heads;  // two pieces a share
     L.off_ml = round256(n * head_dim * sizeof(float));
     L.off_at = L.off_ml + round256(n * 2 * sizeof(float));
-    L.total = L.off_at + round256((size_t)B * 2 * sizeof(int32_t));
+    L.total = L.off_at + round256((size_t)L.splits * 2 * sizeof(int32_t));
     return L;
 }
 

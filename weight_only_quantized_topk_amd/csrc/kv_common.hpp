@@ -41,19 +41,19 @@ struct PagedAttnArgs {
     const int32_t* lengths;   // [B]
     uint16_t* out;            // [B, heads, D]
     float* lse;               // [B, heads] or null
-    float* part_o;            // workspace of a split: [B + splits, heads, D]
-    float* part_ml;           // [B + splits, heads, 2]
-    int32_t* part_at;         // [B, 2]: a sequence's first piece, its number of pieces
+    float* part_o;            // workspace of a split: [splits, 2, heads, D]
+    float* part_ml;           // [splits, 2, heads, 2]
+    int32_t* part_at;         // [splits, 2]: the sequence that begins in a share and goes on in the next, its pieces
     int64_t q_stride, out_stride;
     float qk_scale;           // on the products, for exponents of 2 (the keys' static scale within)
     float v_scale;            // on the output (the values' static scale, or 1)
     int B, heads, kv_heads, D, pages, page_size, width, window, mode;
-    int splits;               // pieces beyond one a sequence; 0: no sequence is split
-    int min_tiles;            // of 32 tokens: a piece has no fewer
+    int splits;               // shares that the batch's tiles are cut into; 0: a sequence each
+    int min_tiles;            // of 32 tokens: a share has no fewer
 };
-// pieces beyond one a sequence that a call's grid and workspace have room for;
-// max_tokens: the most that a sequence reads
-int paged_attn_splits(int B, int heads, int kv_heads, int64_t max_tokens);
+// shares of a call, for which its grid and workspace have room; max_tokens: the
+// most that a sequence reads
+int paged_attn_splits(int B, int heads, int kv_heads, int D, int64_t max_tokens);
 void launch_paged_attention(const PagedAttnArgs& g, bool bf16, hipStream_t s);
 
 }  // namespace wq

@@ -46,7 +46,11 @@ namespace wq {
 
 namespace {
 
+constexpr int NW = 4;              // waves of a workgroup
 constexpr int TILE = 32;           // tokens of a wave's step
+// head_dim rounded up, and the waves a SIMD (workgroups a CU) that its registers leave room for
+constexpr int dim_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+constexpr int waves_of(int DM) { return DM == 256 ? 2 : DM == 128 ? 3 : 4; }
 constexpr float M_NONE = -3.4028234e38f;  // the running maximum before any score
 constexpr float M_SLACK = 8.0f;    // scores may pass it by this much (exponents of 2)
 constexpr float LN2 = 0.693147180559945309f;
@@ -66,6 +70,12 @@ __device__ __forceinline__ Span span_of(const PagedAttnArgs& g, int len) {
     return s;
 }
 
+// a wave-uniform index into an array that the kernel does not write: a scalar
+// load, which the counter of the vector loads in flight does not wait for
+__device__ __forceinline__ int uniform_at(const int32_t* p, int64_t i) {
+    return *(const __attribute__((address_space(4))) int32_t*)(p + i);
+}
+
 template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ int dpp_add(int v) {
     return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROW_MASK, 0xF, false);
@@ -82,33 +92,37 @@ __device__ __forceinline__ int wave_scan(int v) {
     return v;
 }
 
-// piece x of the batch: sequence b, its piece `at` of n (n = 0: x is past the last)
-struct Piece {
-    int b, at, n;
+// a sequence takes at least one tile of the cut, so that every one is in some
+// workgroup's share
+__device__ __forceinline__ int tiles_of(const PagedAttnArgs& g, int b) { return max(1, span_of(g, g.lengths[b]).tiles); }
+
+// workgroup x's share of the batch's tiles, one sequence's after another's: `tiles`
+// from tile `off` of sequence b on (0: none); every share but the last has `cut`
+struct Share {
+    int b, off, tiles, cut;
 };
-__device__ __forceinline__ Piece piece_of(const PagedAttnArgs& g, int x) {
-    if (g.splits == 0) return Piece{x, 0, 1};
+__device__ __forceinline__ Share share_of(const PagedAttnArgs& g, int x) {
+    if (g.splits == 0) return Share{x, 0, tiles_of(g, x), 0};
     const int lane = threadIdx.x & 63;
     const int each = (g.B + 63) / 64;  // consecutive sequences of a lane
     const int b0 = lane * each, b1 = min(b0 + each, g.B);
     int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += span_of(g, g.lengths[b]).tiles;
-    const int total = __builtin_amdgcn_readlane(wave_scan(sum), 63);
-    // sum over the batch of max(1, ceil(tiles / cut)) <= total / cut + B <= splits + B
-    const int cut = max(g.min_tiles, (total + g.splits - 1) / g.splits);
-    sum = 0;
-    for (int b = b0; b < b1; ++b) sum += max(1, (span_of(g, g.lengths[b]).tiles + cut - 1) / cut);
+    for (int b = b0; b < b1; ++b) sum += tiles_of(g, b);
     const int upto = wave_scan(sum);
-    const uint64_t past = __ballot(upto > x);
-    if (past == 0) return Piece{0, 0, 0};
-    const int owner = __ffsll((unsigned long long)past) - 1;
-    int at = x - (__builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(sum, owner));
-    for (int b = owner * each; b < min((owner + 1) * each, g.B); ++b) {
-        const int n = max(1, (span_of(g, g.lengths[b]).tiles + cut - 1) / cut);
-        if (at < n) return Piece{b, at, n};
-        at -= n;
+    const int total = __builtin_amdgcn_readlane(upto, 63);
+    const int cut = max(g.min_tiles, (total + g.splits - 1) / g.splits);
+    const int64_t lo64 = (int64_t)x * cut;
+    if (lo64 >= total) return Share{0, 0, 0, cut};
+    const int lo = (int)lo64, hi = min(lo + cut, total);
+    const int owner = __ffsll((unsigned long long)__ballot(upto > lo)) - 1;
+    int off = lo - (__builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(sum, owner));
+    int b = owner * each;
+    for (; b < g.B - 1; ++b) {
+        const int n = tiles_of(g, b);
+        if (off < n) break;
+        off -= n;
     }
-    return Piece{0, 0, 0};  // (not reached: the owner's pieces hold x)
+    return Share{b, off, hi - lo, cut};
 }
 
 template <bool BF16>
@@ -125,23 +139,28 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w, bool hi) {
     }
 }
 
+// a buffer resource over the rows from base on (raw addressing: byte offsets)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const uint8_t* base) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0, -1, 0x00020000);
+}
+
 template <int N>
 struct Dwords {
     uint32_t d[N];
 };
-template <int BYTES>
-__device__ __forceinline__ Dwords<BYTES / 4> load_bytes(const uint8_t* p) {
+template <int BYTES, int AUX>
+__device__ __forceinline__ Dwords<BYTES / 4> load_bytes(__amdgpu_buffer_rsrc_t rows, int voff, int soff) {
     Dwords<BYTES / 4> r;
     if constexpr (BYTES == 4) {
-        r.d[0] = *reinterpret_cast<const uint32_t*>(p);
+        r.d[0] = __builtin_amdgcn_raw_buffer_load_b32(rows, voff, soff, AUX);
     } else if constexpr (BYTES == 8) {
-        const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rows, voff, soff, AUX);
         r.d[0] = v[0];
         r.d[1] = v[1];
     } else {
 #pragma unroll
         for (int i = 0; i < BYTES / 16; ++i) {
-            const u32x4 v = ldg128(p + 16 * i);
+            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rows, voff + 16 * i, soff, AUX);
 #pragma unroll
             for (int j = 0; j < 4; ++j) r.d[4 * i + j] = v[j];
         }
@@ -157,8 +176,12 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 }
 
 // DM: head_dim rounded up to 64, 128 or 256 (FULL: it is DM)
-template <bool BF16, int MODE, int DM, bool FULL, int NW>
-__global__ __launch_bounds__(NW * 64) void paged_attention_kernel(PagedAttnArgs g) {
+// NT: the cache's rows are read with non-temporal loads.
+// (3 or 4 waves a SIMD: without the bound the compiler keeps the accumulators in
+// the other register file and moves them there and back in every step)
+template <bool BF16, int MODE, int DM, bool FULL, bool NT>
+__global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(PagedAttnArgs g) {
+    constexpr int AUX = NT ? 2 : 0;
     constexpr bool F8 = MODE != KV_16;
     constexpr bool ROW = MODE == KV_E4M3_ROW;
     constexpr bool PBF = BF16 || F8;              // P's type: E4M3 values and scales go as bf16
@@ -172,12 +195,6 @@ __global__ __launch_bounds__(NW * 64) void paged_attention_kernel(PagedAttnArgs 
     const int D = FULL ? DM : g.D;
     const int lane = threadIdx.x & 63, r = lane & 15, q4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Piece pc = piece_of(g, blockIdx.x);
-    const int b = __builtin_amdgcn_readfirstlane(pc.b), at = __builtin_amdgcn_readfirstlane(pc.at);
-    const int pieces = __builtin_amdgcn_readfirstlane(pc.n);
-    if (pieces == 0) return;
-    const Span sp = span_of(g, g.lengths[b]);
-    const int t0 = (int)((int64_t)sp.tiles * at / pieces), t1 = (int)((int64_t)sp.tiles * (at + 1) / pieces);
     const int group = g.heads / g.kv_heads;
     const int htiles = (group + 15) / 16;
     const int kvh = blockIdx.y / htiles, h0 = (blockIdx.y - kvh * htiles) * 16;
@@ -191,38 +208,21 @@ __global__ __launch_bounds__(NW * 64) void paged_attention_kernel(PagedAttnArgs 
         int64_t rows;  // (page, head)'s first row in the cache + the position in the page
         bool good;
     };
-    const int last16 = (sp.len - 1) / KV_TOKENS;  // (not used of an empty sequence)
-    const int32_t* table = g.table + (int64_t)b * g.width;
-    auto half_at = [&](int tok) {
-        const uint32_t u = (uint32_t)min(tok / KV_TOKENS, last16);
-        const uint32_t col = (uint32_t)(((uint64_t)u * magic) >> 32);  // u / page16: the host checks the range
-        const int page = table[col];
-        Half h;
-        h.good = page >= 0 && page < g.pages;     // a bad page holds no tokens
-        h.rows = ((int64_t)(h.good ? page : 0) * g.kv_heads + kvh) * g.page_size + (u - col * page16) * KV_TOKENS;
-        return h;
-    };
-
-    // Q, the B operand of every K step: head r, the channels in K's order
-    u32x4 qv[DM / 32];
-#pragma unroll
-    for (int c = 0; c < DM / 32; ++c) {
-        const int ch = F8 ? 64 * (c / 2) + 16 * q4 + 8 * (c % 2) : 32 * c + 8 * q4;
-        qv[c] = u32x4{0, 0, 0, 0};
-        if (r < nh && ch < D) qv[c] = ldg128(g.q + (int64_t)b * g.q_stride + (int64_t)(head0 + r) * D + ch);
-    }
-
     u32x4 kv[2][KL];
     Dwords<VD> vv[8];
     f32x4 ksv[2], vsv[2];
+    // the wave-uniform part of an address is the resource's base, the lane's a
+    // 32-bit offset
+    const int koff = r * (D * ELT) + 16 * q4, voff = 4 * q4 * (D * ELT) + r * (VEC * ELT);
     auto kload = [&](const Half (&h)[2]) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const uint8_t* p = g.k + h[s].rows * (D * ELT);
+            const __amdgpu_buffer_rsrc_t rows = rows_at(g.k + h[s].rows * (D * ELT));
 #pragma unroll
             for (int c = 0; c < KL; ++c) {
                 if (!FULL) kv[s][c] = u32x4{0, 0, 0, 0};
-                if (FULL || KD * c + (16 / ELT) * q4 < D) kv[s][c] = ldg128(p + r * (D * ELT) + (KD * c) * ELT + 16 * q4);
+                if (FULL || KD * c + (16 / ELT) * q4 < D)
+                    kv[s][c] = __builtin_amdgcn_raw_buffer_load_b128(rows, koff + KD * c * ELT, 0, AUX);
             }
             if constexpr (ROW) ksv[s] = *reinterpret_cast<const f32x4*>(g.ks + h[s].rows + 4 * q4);
         }
@@ -230,36 +230,84 @@ __global__ __launch_bounds__(NW * 64) void paged_attention_kernel(PagedAttnArgs 
     auto vload = [&](const Half (&h)[2]) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const uint8_t* p = g.v + h[s].rows * (D * ELT);
+            const __amdgpu_buffer_rsrc_t rows = rows_at(g.v + h[s].rows * (D * ELT));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (!FULL)
 #pragma unroll
                     for (int i = 0; i < VD; ++i) vv[4 * s + j].d[i] = 0;
-                if (FULL || r * VEC < D)
-                    vv[4 * s + j] = load_bytes<VEC * ELT>(p + (4 * q4 + j) * (D * ELT) + r * (VEC * ELT));
+                if (FULL) vv[4 * s + j] = load_bytes<VEC * ELT, AUX>(rows, voff + j * (DM * ELT), 0);
+                else if (r * VEC < D) vv[4 * s + j] = load_bytes<VEC * ELT, AUX>(rows, voff, j * (D * ELT));
             }
             if constexpr (ROW) vsv[s] = *reinterpret_cast<const f32x4*>(g.vs + h[s].rows + 4 * q4);
         }
     };
 
-    f32x4 acc[VEC];
+    const Share share = share_of(g, blockIdx.x);
+    int left = __builtin_amdgcn_readfirstlane(share.tiles);
+    const int cut = __builtin_amdgcn_readfirstlane(share.cut);
+    int goes_on = 0, begins = 0;  // pieces of the sequence that begins here and ends in another share; it
+    if (left > 0) {
+        // one sequence's tiles [t0, t1) of the share; a step is NW of them, a wave each
+        struct Part {
+            int b, t0, t1, tiles, lo, len, begin;
+        };
+        auto part_of = [&](int b, int off) {
+            const Span sp = span_of(g, uniform_at(g.lengths, b));
+            const int tiles = max(1, sp.tiles);
+            return Part{b, off, min(tiles, off + left), tiles, sp.lo, sp.len, sp.begin};
+        };
+        // half s of this wave's tile in step i, its last tile's past the end (from the cache, unused)
+        auto half_at = [&](const Part& pt, int i, int s) {
+            const int tok = pt.begin + TILE * min(pt.t0 + NW * i + wave, pt.t1 - 1) + KV_TOKENS * s;
+            const uint32_t u = (uint32_t)min(tok, max(pt.len - 1, 0)) / KV_TOKENS;
+            const uint32_t col = (uint32_t)(((uint64_t)u * magic) >> 32);  // u / page16: the host checks the range
+            const int page = uniform_at(g.table, (int64_t)pt.b * g.width + col);
+            Half h;
+            h.good = page >= 0 && page < g.pages;  // a bad page holds no tokens
+            h.rows = ((int64_t)(h.good ? page : 0) * g.kv_heads + kvh) * g.page_size + (u - col * page16) * KV_TOKENS;
+            return h;
+        };
+        // Q, the B operand of every K step: head r, the channels in K's order
+        u32x4 qv[DM / 32];
+        auto qload = [&](int b) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = M_NONE, l = 0.0f;  // head r's running maximum (the same in its 4 lanes); the lane's own sum
+            for (int c = 0; c < DM / 32; ++c) {
+                const int ch = F8 ? 64 * (c / 2) + 16 * q4 + 8 * (c % 2) : 32 * c + 8 * q4;
+                qv[c] = u32x4{0, 0, 0, 0};
+                if (r < nh && ch < D) qv[c] = ldg128(g.q + (int64_t)b * g.q_stride + (int64_t)(head0 + r) * D + ch);
+            }
+        };
 
-    int t = t0 + wave;
-    if (t < t1) {
-        Half cur[2], nxt[2];
+        Part pt = part_of(__builtin_amdgcn_readfirstlane(share.b), __builtin_amdgcn_readfirstlane(share.off));
+        left -= pt.t1 - pt.t0;
+        f32x4 acc[VEC];
+        float m, l;  // head r's running maximum (the same in its 4 lanes); the lane's own sum
+        auto clear = [&]() {
+            m = M_NONE;
+            l = 0.0f;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) cur[s] = half_at(sp.begin + TILE * t + 16 * s);
+            for (int e = 0; e < VEC; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+        };
+        clear();
+        Half cur[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) cur[s] = half_at(pt, 0, s);
+        qload(pt.b);
         kload(cur);
         vload(cur);
-        for (; t < t1; t += NW) {
-            const int tok = sp.begin + TILE * t;
-            const int tn = min(t + NW, t1 - 1);  // past the end: a tile again, from the cache, unused
+        for (int i = 0;;) {
+            // the next step, of this sequence or the next one, is loaded while this one is multiplied
+            const bool last = NW * (i + 1) >= pt.t1 - pt.t0, more = left > 0 && pt.b + 1 < g.B;
+            Part np = pt;
+            int ni = i + 1;
+            if (last && more) {
+                np = part_of(pt.b + 1, 0);
+                ni = 0;
+            }
+            Half nxt[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) nxt[s] = half_at(sp.begin + TILE * tn + 16 * s);
+            for (int s = 0; s < 2; ++s) nxt[s] = half_at(np, ni, s);
 
             f32x4 sc[2];
 #pragma unroll
@@ -282,9 +330,12 @@ __global__ __launch_bounds__(NW * 64) void paged_attention_kernel(PagedAttnArgs 
                 if constexpr (ROW) sc[s] *= ksv[s];
             }
             kload(nxt);
+            if (last && more) qload(np.b);
 
             // scores in exponents of 2; tokens outside the span or in a bad page have none
-            const bool edge = tok < sp.lo || tok + TILE > sp.len || !cur[0].good || !cur[1].good;
+            const int tile = pt.t0 + NW * i + wave, tok = pt.begin + TILE * tile;
+            const int end = tile < pt.t1 ? pt.len : 0;
+            const bool edge = tok < pt.lo || tok + TILE > end || !cur[0].good || !cur[1].good;
             float x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = sc[j / 4][j % 4] * g.qk_scale;
@@ -292,11 +343,11 @@ __global__ __launch_bounds__(NW * 64) void paged_attention_kernel(PagedAttnArgs 
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int k = tok + 16 * (j / 4) + 4 * q4 + j % 4;
-                    const bool live = k >= sp.lo && k < sp.len && cur[j / 4].good;
+                    const bool live = k >= pt.lo && k < end && cur[j / 4].good;
                     x[j] = live ? x[j] : -INFINITY;
                     // what lies there may be anything, and 0 * NaN is one
 #pragma unroll
-                    for (int i = 0; i < VD; ++i) vv[j].d[i] = live ? vv[j].d[i] : 0;
+                    for (int w = 0; w < VD; ++w) vv[j].d[w] = live ? vv[j].d[w] : 0;
                     if constexpr (ROW) vsv[j / 4][j % 4] = live ? vsv[j / 4][j % 4] : 0.0f;
                 }
             }
@@ -360,114 +411,178 @@ __global__ __launch_bounds__(NW * 64) void paged_attention_kernel(PagedAttnArgs 
             vload(nxt);
 #pragma unroll
             for (int s = 0; s < 2; ++s) cur[s] = nxt[s];
-        }
-    }
+            if (!last) {
+                ++i;
+                continue;
+            }
 
-    // join the waves: lane l holds channels [4 VEC q4, +4 VEC) of head r
-    constexpr int LD = DM + 4;
-    float* lm = lds;                   // [NW][16]
-    float* ll = lds + NW * 16;         // [NW][16]
-    float* lo = lds + 2 * NW * 16;     // [NW][nh][LD]
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-    if (q4 == 0) {
-        lm[wave * 16 + r] = m;
-        ll[wave * 16 + r] = l;
-    }
-    if (r < nh) {
-        float* o = lo + (wave * nh + r) * LD + 4 * VEC * q4;
+            // join the waves: lane l holds channels [4 VEC q4, +4 VEC) of head r
+            constexpr int LD = DM + 4;
+            float* lm = lds;                // [NW][16]
+            float* ll = lds + NW * 16;      // [NW][16]
+            float* lo = lds + 2 * NW * 16;  // [NW][nh][LD]
+            l += __shfl_xor(l, 16, 64);
+            l += __shfl_xor(l, 32, 64);
+            __syncthreads();  // the sequence before is read
+            if (q4 == 0) {
+                lm[wave * 16 + r] = m;
+                ll[wave * 16 + r] = l;
+            }
+            if (r < nh) {
+                float* o = lo + (wave * nh + r) * LD + 4 * VEC * q4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int e = 0; e < VEC; e += 4)
-                *reinterpret_cast<f32x4*>(o + VEC * i + e) = f32x4{acc[e][i], acc[e + 1][i], acc[e + 2][i], acc[e + 3][i]};
-    }
-    __syncthreads();
-    const int quads = D / 4;
-    for (int id = threadIdx.x; id < nh * quads; id += NW * 64) {
-        const int hd = id / quads, c = 4 * (id - hd * quads);
-        float mx = lm[hd], sum = 0.0f;
+                    for (int e = 0; e < VEC; e += 4)
+                        *reinterpret_cast<f32x4*>(o + VEC * k + e) =
+                            f32x4{acc[e][k], acc[e + 1][k], acc[e + 2][k], acc[e + 3][k]};
+            }
+            __syncthreads();
+            const bool whole = pt.t1 - pt.t0 == pt.tiles;
+            const int quads = D / 4;
+            for (int id = threadIdx.x; id < nh * quads; id += NW * 64) {
+                const int hd = id / quads, c = 4 * (id - hd * quads);
+                float mx = lm[hd], sum = 0.0f;
 #pragma unroll
-        for (int w = 1; w < NW; ++w) mx = fmaxf(mx, lm[w * 16 + hd]);
-        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+                for (int w = 1; w < NW; ++w) mx = fmaxf(mx, lm[w * 16 + hd]);
+                f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float f = __builtin_amdgcn_exp2f(lm[w * 16 + hd] - mx);
-            sum += f * ll[w * 16 + hd];
-            o += f * *reinterpret_cast<const f32x4*>(lo + (w * nh + hd) * LD + c);
+                for (int w = 0; w < NW; ++w) {
+                    const float f = __builtin_amdgcn_exp2f(lm[w * 16 + hd] - mx);
+                    sum += f * ll[w * 16 + hd];
+                    o += f * *reinterpret_cast<const f32x4*>(lo + (w * nh + hd) * LD + c);
+                }
+                const int64_t head = head0 + hd;
+                if (whole) {
+                    // no token with a weight: zeros, and -inf
+                    const float inv = sum == 0.0f ? 0.0f : g.v_scale / sum;
+                    *reinterpret_cast<u32x2*>(g.out + (int64_t)pt.b * g.out_stride + head * D + c) =
+                        u32x2{f32_to_act2<BF16>(o[0] * inv, o[1] * inv), f32_to_act2<BF16>(o[2] * inv, o[3] * inv)};
+                    if (g.lse && c == 0)
+                        g.lse[(int64_t)pt.b * g.heads + head] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * LN2;
+                } else {
+                    const int64_t slot = (int64_t)(2 * blockIdx.x + (pt.t0 == 0)) * g.heads + head;
+                    *reinterpret_cast<f32x4*>(g.part_o + slot * D + c) = o;
+                    if (c == 0) {
+                        g.part_ml[2 * slot] = mx;
+                        g.part_ml[2 * slot + 1] = sum;
+                    }
+                }
+            }
+            if (!more) {
+                if (pt.t0 == 0 && !whole) {
+                    goes_on = 1 + (pt.tiles - pt.t1 + cut - 1) / cut;
+                    begins = pt.b;
+                }
+                break;
+            }
+            pt = np;
+            left -= pt.t1 - pt.t0;
+            i = 0;
+            clear();
         }
-        const int64_t head = head0 + hd;
-        if (pieces == 1) {
-            // no token with a weight: zeros, and -inf
-            const float inv = sum == 0.0f ? 0.0f : g.v_scale / sum;
-            *reinterpret_cast<u32x2*>(g.out + (int64_t)b * g.out_stride + head * D + c) =
-                u32x2{f32_to_act2<BF16>(o[0] * inv, o[1] * inv), f32_to_act2<BF16>(o[2] * inv, o[3] * inv)};
-            if (g.lse && c == 0) g.lse[(int64_t)b * g.heads + head] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * LN2;
-        } else {
-            const int64_t slot = (int64_t)blockIdx.x * g.heads + head;
-            *reinterpret_cast<f32x4*>(g.part_o + slot * D + c) = o;
-            if (c == 0) {
-                g.part_ml[2 * slot] = mx;
-                g.part_ml[2 * slot + 1] = sum;
+    }
+    if (g.splits > 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+        g.part_at[2 * blockIdx.x] = begins;
+        g.part_at[2 * blockIdx.x + 1] = goes_on;
+    }
+}
+
+// the pieces of sequences in more than one share, for one head: 256 threads as
+// 256 / (D / 4) rows of D / 4 vectors of 4 channels; a row joins every so many-th
+// piece, JOIN_AHEAD of them loaded together with their statistics, then the
+// rows are joined.  A workgroup looks at `shares` of them one after another, in
+// each of which at most one such sequence begins
+constexpr int JOIN_AHEAD = 8;
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void paged_join_kernel(PagedAttnArgs g, int shares) {
+    __shared__ f32x4 so[256];
+    __shared__ float sm[256], sl[256];
+    const int head = blockIdx.x, tid = threadIdx.x;
+    const int quads = g.D / 4, side = 256 / quads;
+    const int row = tid / quads, c = 4 * (tid - row * quads);
+    const int x1 = min((int)(blockIdx.y + 1) * shares, g.splits);
+    for (int x = blockIdx.y * shares; x < x1; ++x) {
+        const int n = g.part_at[2 * x + 1];
+        if (n == 0) continue;  // (the same for all threads)
+        float m = M_NONE, l = 0.0f;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        for (int p0 = row; p0 < n && row < side; p0 += side * JOIN_AHEAD) {
+            float pm[JOIN_AHEAD], pl[JOIN_AHEAD];
+            f32x4 po[JOIN_AHEAD];
+#pragma unroll
+            for (int k = 0; k < JOIN_AHEAD; ++k) {
+                // piece 0 is share x's second, piece p share x + p's first; past the last: it again, without weight
+                const int p = min(p0 + k * side, n - 1);
+                const int64_t slot = (int64_t)(2 * (x + p) + (p == 0)) * g.heads + head;
+                pm[k] = p0 + k * side < n ? g.part_ml[2 * slot] : M_NONE;
+                pl[k] = p0 + k * side < n ? g.part_ml[2 * slot + 1] : 0.0f;
+                po[k] = *reinterpret_cast<const f32x4*>(g.part_o + slot * g.D + c);
+            }
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < JOIN_AHEAD; ++k) top = fmaxf(top, pm[k]);
+            const float f0 = __builtin_amdgcn_exp2f(m - top);
+            m = top;
+            l *= f0;
+            o *= f0;
+#pragma unroll
+            for (int k = 0; k < JOIN_AHEAD; ++k) {
+                const float f = p0 + k * side < n ? __builtin_amdgcn_exp2f(pm[k] - top) : 0.0f;
+                l += f * pl[k];
+                if (p0 + k * side < n) o += f * po[k];  // (a repeated piece may hold infinities)
             }
         }
-    }
-    if (g.splits > 0 && at == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-        g.part_at[2 * b] = blockIdx.x;
-        g.part_at[2 * b + 1] = pieces;
-    }
-}
-
-// the pieces of one sequence and head: 256 threads as 256 / (D / 4) pieces at a
-// time by D / 4 vectors of 4 channels
-template <bool BF16>
-__global__ __launch_bounds__(256) void paged_join_kernel(PagedAttnArgs g) {
-    __shared__ f32x4 so[256];
-    __shared__ float sl[256];
-    const int b = blockIdx.y, head = blockIdx.x;
-    const int first = g.part_at[2 * b], n = g.part_at[2 * b + 1];
-    if (n <= 1) return;
-    const float* ml = g.part_ml + 2 * ((int64_t)first * g.heads + head);
-    float mx = M_NONE;
-    for (int p = 0; p < n; ++p) mx = fmaxf(mx, ml[2 * (int64_t)p * g.heads]);
-    const int quads = g.D / 4, side = 256 / quads;
-    const int row = threadIdx.x / quads, c = 4 * (threadIdx.x - row * quads);
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    float sum = 0.0f;
-    if (row < side)
-        for (int p = row; p < n; p += side) {
-            const float f = __builtin_amdgcn_exp2f(ml[2 * (int64_t)p * g.heads] - mx);
-            sum += f * ml[2 * (int64_t)p * g.heads + 1];
-            o += f * *reinterpret_cast<const f32x4*>(g.part_o + ((int64_t)(first + p) * g.heads + head) * g.D + c);
+        so[tid] = o;
+        sm[tid] = m;
+        sl[tid] = l;
+        __syncthreads();
+        if (row == 0) {
+            float top = m;
+            for (int i = 1; i < side; ++i) top = fmaxf(top, sm[i * quads]);
+            const float f0 = __builtin_amdgcn_exp2f(m - top);
+            o *= f0;
+            float sum = l * f0;
+            for (int i = 1; i < side; ++i) {
+                const float f = __builtin_amdgcn_exp2f(sm[i * quads] - top);
+                sum += f * sl[i * quads];
+                o += f * so[i * quads + tid];
+            }
+            const int b = g.part_at[2 * x];
+            const float inv = sum == 0.0f ? 0.0f : g.v_scale / sum;
+            *reinterpret_cast<u32x2*>(g.out + (int64_t)b * g.out_stride + (int64_t)head * g.D + c) =
+                u32x2{f32_to_act2<BF16>(o[0] * inv, o[1] * inv), f32_to_act2<BF16>(o[2] * inv, o[3] * inv)};
+            if (g.lse && c == 0) g.lse[(int64_t)b * g.heads + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * LN2;
         }
-    so[threadIdx.x] = o;
-    sl[threadIdx.x] = sum;
-    __syncthreads();
-    if (row != 0) return;
-    for (int i = 1; i < side; ++i) {
-        o += so[i * quads + threadIdx.x];
-        sum += sl[i * quads + threadIdx.x];
+        __syncthreads();
     }
-    const float inv = sum == 0.0f ? 0.0f : g.v_scale / sum;
-    *reinterpret_cast<u32x2*>(g.out + (int64_t)b * g.out_stride + (int64_t)head * g.D + c) =
-        u32x2{f32_to_act2<BF16>(o[0] * inv, o[1] * inv), f32_to_act2<BF16>(o[2] * inv, o[3] * inv)};
-    if (g.lse && c == 0) g.lse[(int64_t)b * g.heads + head] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * LN2;
 }
 
-constexpr int NW = 4;
-constexpr int MIN_TILES = 2 * NW;
-
-template <bool BF16, int MODE, int DM, bool FULL>
-void launch_full(const PagedAttnArgs& g, hipStream_t s) {
+template <bool BF16, int MODE, int DM, bool FULL, bool NT>
+void launch_kernel(const PagedAttnArgs& g, hipStream_t s) {
     const int group = g.heads / g.kv_heads;
     const int nh = std::min(group, 16);
     const size_t lds = (2 * NW * 16 + (size_t)NW * nh * (DM + 4)) * sizeof(float);
-    auto kern = paged_attention_kernel<BF16, MODE, DM, FULL, NW>;
+    auto kern = paged_attention_kernel<BF16, MODE, DM, FULL, NT>;
     if (lds > 65536)
         (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)lds);
-    const dim3 grid(g.B + g.splits, g.kv_heads * ((group + 15) / 16));
+    const dim3 grid(g.splits > 0 ? g.splits : g.B, g.kv_heads * ((group + 15) / 16));
     hipLaunchKernelGGL(kern, grid, dim3(NW * 64), lds, s, g);
+}
+
+// Non-temporal loads where the keys and values are more than the last-level
+// cache (256 MB) holds from one step to the next: one sequence of 131072 tokens, 8
+// heads of 128 in bf16 (537 MB), 98 against 105 us; 61 sequences of up to 8192 in
+// E4M3 (536 MB) 114 against 119.  A cache that fits is read from there (56 MB: 22
+// against 26), and sequences of a workgroup each are slower with them (116
+// against 106 us, 256 x up to 1024 tokens, 16 heads of 64)
+template <bool BF16, int MODE, int DM, bool FULL>
+void launch_full(const PagedAttnArgs& g, hipStream_t s) {
+    const int64_t bytes = (int64_t)g.pages * g.page_size * g.kv_heads * g.D * (MODE == KV_16 ? 4 : 2);
+    if (FULL && g.splits > 0 && bytes > (256 << 20)) launch_kernel<BF16, MODE, DM, FULL, FULL>(g, s);
+    else launch_kernel<BF16, MODE, DM, FULL, false>(g, s);
 }
 
 template <bool BF16, int MODE>
@@ -485,22 +600,32 @@ void launch_type(const PagedAttnArgs& g, hipStream_t s) {
     if (g.mode == KV_16) launch_dim<BF16, KV_16>(g, s);
     else if (g.mode == KV_E4M3_ROW) launch_dim<BF16, KV_E4M3_ROW>(g, s);
     else launch_dim<BF16, KV_E4M3_STATIC>(g, s);
-    if (g.splits > 0) hipLaunchKernelGGL(paged_join_kernel<BF16>, dim3(g.heads, g.B), dim3(256), 0, s, g);
+    if (g.splits > 0) {
+        // about one sequence to join a workgroup: few of the shares begin one where there are few
+        const int shares = std::max(1, std::min(16, g.splits / g.B));
+        hipLaunchKernelGGL(paged_join_kernel<BF16>, dim3(g.heads, (g.splits + shares - 1) / shares), dim3(256), 0, s, g,
+                           shares);
+    }
 }
 
 }  // namespace
 
-int paged_attn_splits(int B, int heads, int kv_heads, int64_t max_tokens) {
-    const int64_t tiles = (max_tokens + TILE - 1) / TILE;
-    if (tiles <= MIN_TILES) return 0;
+// Shares: as many as are resident at once on 256 CUs, none smaller than a tile a
+// wave.  A workgroup a sequence, and no second kernel, where they are
+// short and enough to fill the GPU (16 heads of 64, 256 sequences of up to 1024: 106
+// against 121 us in shares), or shorter than two steps of a workgroup.
+int paged_attn_splits(int B, int heads, int kv_heads, int D, int64_t max_tokens) {
+    constexpr int SHORT = 1024, TWO_STEPS = 2 * NW * TILE;
+    const int RESIDENT = 256 * waves_of(dim_of(D));
     const int units = kv_heads * ((heads / kv_heads + 15) / 16);
-    const int64_t want = std::max(1, (768 + units - 1) / units);
-    return (int)std::min<int64_t>(want, (int64_t)B * ((tiles + MIN_TILES - 1) / MIN_TILES));
+    if (max_tokens <= TWO_STEPS || (max_tokens <= SHORT && (int64_t)B * units >= RESIDENT)) return 0;
+    const int64_t tiles = (max_tokens + TILE - 1) / TILE;
+    return (int)std::min<int64_t>((RESIDENT + units - 1) / units, (int64_t)B * ((tiles + NW - 1) / NW));
 }
 
 void launch_paged_attention(const PagedAttnArgs& a, bool bf16, hipStream_t s) {
     PagedAttnArgs g = a;
-    g.min_tiles = MIN_TILES;
+    g.min_tiles = NW;
     if (bf16) launch_type<true>(g, s);
     else launch_type<false>(g, s);
 }
