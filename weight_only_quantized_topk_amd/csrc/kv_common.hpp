@@ -48,8 +48,7 @@ struct PagedAttnArgs {
     float qk_scale;           // on the products, for exponents of 2 (the keys' static scale within)
     float v_scale;            // on the output (the values' static scale, or 1)
     int B, heads, kv_heads, D, pages, page_size, width, window, mode;
-    int splits;               // shares that the batch's tiles are cut into; 0: a sequence each
-    int min_tiles;            // of 32 tokens: a share has no fewer
+    int splits;               // shares that the batch's tokens are cut into; 0: a sequence each
 };
 // shares of a call, for which its grid and workspace have room; max_tokens: the
 // most that a sequence reads

@@ -92,25 +92,26 @@ __device__ __forceinline__ int wave_scan(int v) {
     return v;
 }
 
-// a sequence takes at least one tile of the cut, so that every one is in some
-// workgroup's share
-__device__ __forceinline__ int tiles_of(const PagedAttnArgs& g, int b) { return max(1, span_of(g, g.lengths[b]).tiles); }
+// steps of a workgroup (NW tiles, the last one of a sequence partly idle); at
+// least one each, so that every sequence is in some workgroup's share
+__device__ __forceinline__ int steps_for(int tiles) { return max(1, (tiles + NW - 1) / NW); }
+__device__ __forceinline__ int steps_of(const PagedAttnArgs& g, int b) { return steps_for(span_of(g, g.lengths[b]).tiles); }
 
-// workgroup x's share of the batch's tiles, one sequence's after another's: `tiles`
-// from tile `off` of sequence b on (0: none); every share but the last has `cut`
+// workgroup x's share of the batch's steps, one sequence's after another's: `steps`
+// from step `off` of sequence b on (0: none); every share but the last has `cut`
 struct Share {
-    int b, off, tiles, cut;
+    int b, off, steps, cut;
 };
 __device__ __forceinline__ Share share_of(const PagedAttnArgs& g, int x) {
-    if (g.splits == 0) return Share{x, 0, tiles_of(g, x), 0};
+    if (g.splits == 0) return Share{x, 0, steps_of(g, x), 0};
     const int lane = threadIdx.x & 63;
     const int each = (g.B + 63) / 64;  // consecutive sequences of a lane
     const int b0 = lane * each, b1 = min(b0 + each, g.B);
     int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += tiles_of(g, b);
+    for (int b = b0; b < b1; ++b) sum += steps_of(g, b);
     const int upto = wave_scan(sum);
     const int total = __builtin_amdgcn_readlane(upto, 63);
-    const int cut = max(g.min_tiles, (total + g.splits - 1) / g.splits);
+    const int cut = (total + g.splits - 1) / g.splits;
     const int64_t lo64 = (int64_t)x * cut;
     if (lo64 >= total) return Share{0, 0, 0, cut};
     const int lo = (int)lo64, hi = min(lo + cut, total);
@@ -118,7 +119,7 @@ __device__ __forceinline__ Share share_of(const PagedAttnArgs& g, int x) {
     int off = lo - (__builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(sum, owner));
     int b = owner * each;
     for (; b < g.B - 1; ++b) {
-        const int n = tiles_of(g, b);
+        const int n = steps_of(g, b);
         if (off < n) break;
         off -= n;
     }
@@ -244,22 +245,22 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
     };
 
     const Share share = share_of(g, blockIdx.x);
-    int left = __builtin_amdgcn_readfirstlane(share.tiles);
+    int left = __builtin_amdgcn_readfirstlane(share.steps);
     const int cut = __builtin_amdgcn_readfirstlane(share.cut);
     int goes_on = 0, begins = 0;  // pieces of the sequence that begins here and ends in another share; it
     if (left > 0) {
-        // one sequence's tiles [t0, t1) of the share; a step is NW of them, a wave each
+        // one sequence's steps [s0, s1) of all its `steps` in the share
         struct Part {
-            int b, t0, t1, tiles, lo, len, begin;
+            int b, s0, s1, steps, lo, len, begin;
         };
         auto part_of = [&](int b, int off) {
             const Span sp = span_of(g, uniform_at(g.lengths, b));
-            const int tiles = max(1, sp.tiles);
-            return Part{b, off, min(tiles, off + left), tiles, sp.lo, sp.len, sp.begin};
+            const int steps = steps_for(sp.tiles);
+            return Part{b, off, min(steps, off + left), steps, sp.lo, sp.len, sp.begin};
         };
-        // half s of this wave's tile in step i, its last tile's past the end (from the cache, unused)
+        // half s of this wave's tile in step i, its sequence's last 16 tokens past the end
         auto half_at = [&](const Part& pt, int i, int s) {
-            const int tok = pt.begin + TILE * min(pt.t0 + NW * i + wave, pt.t1 - 1) + KV_TOKENS * s;
+            const int tok = pt.begin + TILE * (NW * min(i, pt.s1 - 1) + wave) + KV_TOKENS * s;
             const uint32_t u = (uint32_t)min(tok, max(pt.len - 1, 0)) / KV_TOKENS;
             const uint32_t col = (uint32_t)(((uint64_t)u * magic) >> 32);  // u / page16: the host checks the range
             const int page = uniform_at(g.table, (int64_t)pt.b * g.width + col);
@@ -280,7 +281,7 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
         };
 
         Part pt = part_of(__builtin_amdgcn_readfirstlane(share.b), __builtin_amdgcn_readfirstlane(share.off));
-        left -= pt.t1 - pt.t0;
+        left -= pt.s1 - pt.s0;
         f32x4 acc[VEC];
         float m, l;  // head r's running maximum (the same in its 4 lanes); the lane's own sum
         auto clear = [&]() {
@@ -292,13 +293,13 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
         clear();
         Half cur[2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) cur[s] = half_at(pt, 0, s);
+        for (int s = 0; s < 2; ++s) cur[s] = half_at(pt, pt.s0, s);
         qload(pt.b);
         kload(cur);
         vload(cur);
-        for (int i = 0;;) {
+        for (int i = pt.s0;;) {
             // the next step, of this sequence or the next one, is loaded while this one is multiplied
-            const bool last = NW * (i + 1) >= pt.t1 - pt.t0, more = left > 0 && pt.b + 1 < g.B;
+            const bool last = i + 1 >= pt.s1, more = left > 0 && pt.b + 1 < g.B;
             Part np = pt;
             int ni = i + 1;
             if (last && more) {
@@ -333,9 +334,8 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
             if (last && more) qload(np.b);
 
             // scores in exponents of 2; tokens outside the span or in a bad page have none
-            const int tile = pt.t0 + NW * i + wave, tok = pt.begin + TILE * tile;
-            const int end = tile < pt.t1 ? pt.len : 0;
-            const bool edge = tok < pt.lo || tok + TILE > end || !cur[0].good || !cur[1].good;
+            const int tok = pt.begin + TILE * (NW * i + wave);
+            const bool edge = tok < pt.lo || tok + TILE > pt.len || !cur[0].good || !cur[1].good;
             float x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = sc[j / 4][j % 4] * g.qk_scale;
@@ -343,7 +343,7 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int k = tok + 16 * (j / 4) + 4 * q4 + j % 4;
-                    const bool live = k >= pt.lo && k < end && cur[j / 4].good;
+                    const bool live = k >= pt.lo && k < pt.len && cur[j / 4].good;
                     x[j] = live ? x[j] : -INFINITY;
                     // what lies there may be anything, and 0 * NaN is one
 #pragma unroll
@@ -438,7 +438,7 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
                             f32x4{acc[e][k], acc[e + 1][k], acc[e + 2][k], acc[e + 3][k]};
             }
             __syncthreads();
-            const bool whole = pt.t1 - pt.t0 == pt.tiles;
+            const bool whole = pt.s1 - pt.s0 == pt.steps;
             const int quads = D / 4;
             for (int id = threadIdx.x; id < nh * quads; id += NW * 64) {
                 const int hd = id / quads, c = 4 * (id - hd * quads);
@@ -461,7 +461,7 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
                     if (g.lse && c == 0)
                         g.lse[(int64_t)pt.b * g.heads + head] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * LN2;
                 } else {
-                    const int64_t slot = (int64_t)(2 * blockIdx.x + (pt.t0 == 0)) * g.heads + head;
+                    const int64_t slot = (int64_t)(2 * blockIdx.x + (pt.s0 == 0)) * g.heads + head;
                     *reinterpret_cast<f32x4*>(g.part_o + slot * D + c) = o;
                     if (c == 0) {
                         g.part_ml[2 * slot] = mx;
@@ -470,14 +470,14 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
                 }
             }
             if (!more) {
-                if (pt.t0 == 0 && !whole) {
-                    goes_on = 1 + (pt.tiles - pt.t1 + cut - 1) / cut;
+                if (pt.s0 == 0 && !whole) {
+                    goes_on = 1 + (pt.steps - pt.s1 + cut - 1) / cut;
                     begins = pt.b;
                 }
                 break;
             }
             pt = np;
-            left -= pt.t1 - pt.t0;
+            left -= pt.s1 - pt.s0;
             i = 0;
             clear();
         }
@@ -502,10 +502,14 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedAttnArgs g, int sh
     const int head = blockIdx.x, tid = threadIdx.x;
     const int quads = g.D / 4, side = 256 / quads;
     const int row = tid / quads, c = 4 * (tid - row * quads);
-    const int x1 = min((int)(blockIdx.y + 1) * shares, g.splits);
-    for (int x = blockIdx.y * shares; x < x1; ++x) {
-        const int n = g.part_at[2 * x + 1];
-        if (n == 0) continue;  // (the same for all threads)
+    // lane k of every wave: the k-th share's sequence and its pieces (0: none begins there to be joined)
+    const int mine = blockIdx.y * shares + (tid & 63);
+    const bool there = (tid & 63) < shares && mine < g.splits;
+    const int bs = there ? g.part_at[2 * mine] : 0, ns = there ? g.part_at[2 * mine + 1] : 0;
+    for (uint64_t todo = __ballot(ns > 0); todo != 0; todo &= todo - 1) {
+        const int k = __ffsll((unsigned long long)todo) - 1;
+        const int x = blockIdx.y * shares + k;
+        const int n = __builtin_amdgcn_readlane(ns, k), b = __builtin_amdgcn_readlane(bs, k);
         float m = M_NONE, l = 0.0f;
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
         for (int p0 = row; p0 < n && row < side; p0 += side * JOIN_AHEAD) {
@@ -549,7 +553,6 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedAttnArgs g, int sh
                 sum += f * sl[i * quads];
                 o += f * so[i * quads + tid];
             }
-            const int b = g.part_at[2 * x];
             const float inv = sum == 0.0f ? 0.0f : g.v_scale / sum;
             *reinterpret_cast<u32x2*>(g.out + (int64_t)b * g.out_stride + (int64_t)head * g.D + c) =
                 u32x2{f32_to_act2<BF16>(o[0] * inv, o[1] * inv), f32_to_act2<BF16>(o[2] * inv, o[3] * inv)};
@@ -602,7 +605,7 @@ void launch_type(const PagedAttnArgs& g, hipStream_t s) {
     else launch_dim<BF16, KV_E4M3_STATIC>(g, s);
     if (g.splits > 0) {
         // about one sequence to join a workgroup: few of the shares begin one where there are few
-        const int shares = std::max(1, std::min(16, g.splits / g.B));
+        const int shares = std::max(1, std::min(64, g.splits / g.B));
         hipLaunchKernelGGL(paged_join_kernel<BF16>, dim3(g.heads, (g.splits + shares - 1) / shares), dim3(256), 0, s, g,
                            shares);
     }
@@ -619,13 +622,11 @@ int paged_attn_splits(int B, int heads, int kv_heads, int D, int64_t max_tokens)
     const int RESIDENT = 256 * waves_of(dim_of(D));
     const int units = kv_heads * ((heads / kv_heads + 15) / 16);
     if (max_tokens <= TWO_STEPS || (max_tokens <= SHORT && (int64_t)B * units >= RESIDENT)) return 0;
-    const int64_t tiles = (max_tokens + TILE - 1) / TILE;
-    return (int)std::min<int64_t>((RESIDENT + units - 1) / units, (int64_t)B * ((tiles + NW - 1) / NW));
+    const int64_t steps = (max_tokens + NW * TILE - 1) / (NW * TILE);
+    return (int)std::min<int64_t>((RESIDENT + units - 1) / units, B * steps);
 }
 
-void launch_paged_attention(const PagedAttnArgs& a, bool bf16, hipStream_t s) {
-    PagedAttnArgs g = a;
-    g.min_tiles = NW;
+void launch_paged_attention(const PagedAttnArgs& g, bool bf16, hipStream_t s) {
     if (bf16) launch_type<true>(g, s);
     else launch_type<false>(g, s);
 }
