@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libwqmoe.so")
 # bandwidth the weight-streaming kernels are read against
 PROBE_SRC = "stream_probe.hip"
 PROBE = os.path.join(HERE, "stream_probe")
-SOURCES = ["abi.cpp", "route_align.hip", "gemm_decode.hip", "gemm_prefill.hip", "gemm_prefill_n256.hip", "sparse24.hip", "quant.hip", "dense_decode.hip", "gemm_tiny.hip", "gemm_fp8.hip", "rms_norm.hip", "route_grouped.hip", "lora.hip", "lora_wide.hip", "kv_cache.hip", "paged_attention.hip"]
+SOURCES = ["abi.cpp", "route_align.hip", "gemm_decode.hip", "gemm_prefill.hip", "gemm_prefill_n256.hip", "sparse24.hip", "quant.hip", "dense_decode.hip", "dense_split.hip", "gemm_tiny.hip", "gemm_fp8.hip", "rms_norm.hip", "route_grouped.hip", "lora.hip", "lora_wide.hip", "kv_cache.hip", "paged_attention.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1482,14 +1482,16 @@ wq_status wq_paged_attention(const wq_kv_cache* c, const void* d_q, int64_t q_st
 // ---------------------------------------------------------------------------
 namespace {
 struct EpilogueLayout {
-    bool rows;   // 1..128 rows in one launch
+    bool split;  // dense_split.hip: one launch
+    bool rows;   // otherwise 1..128 rows in one launch
     int ks;      // K slices through fp32 slabs
     size_t off_gather, total;
 };
 EpilogueLayout epilogue_layout(int wbits, int M, int K, int N, bool act_order) {
     EpilogueLayout L{};
-    L.rows = wq::dense_decode_supported(M, K);
-    L.ks = L.rows ? 1 : wq::dense_large_split(wbits, M, K, N);
+    L.split = wq::dense_split_supported(wbits, M, N);
+    L.rows = !L.split && wq::dense_decode_supported(M, K);
+    L.ks = L.split || L.rows ? 1 : wq::dense_large_split(wbits, M, K, N);
     size_t o = L.ks > 1 ? round256((size_t)L.ks * M * N * sizeof(float)) : 0;
     L.off_gather = o;
     if (act_order) o += round256((size_t)M * K * 2);
@@ -1502,7 +1504,7 @@ const char* epilogue_sizes(int wbits, int M, int K, int N) {
     if (M > MAX_PAIRS || K > (1 << 24) || N > (1 << 24)) return "M, K or N > 2^24";
     if (K % (wbits == 4 ? wq::WFmt<4>::KCHUNK : wq::WFmt<8>::KCHUNK)) return "K must be a multiple of 128 (int4) or 64 (int8)";
     if (N % 16) return "N must be a multiple of 16";
-    if (!wq::dense_decode_supported(M, K) && !wq::prefill_fits((size_t)M + 128, K)) return "more than 4 GiB of activations";
+    if (!wq::dense_split_supported(wbits, M, N) && !wq::dense_decode_supported(M, K) && !wq::prefill_fits((size_t)M + 128, K)) return "more than 4 GiB of activations";
     if (M > 65535 * 64) return "more than 65535 * 64 rows";
     return nullptr;
 }
@@ -1574,7 +1576,8 @@ wq_status dense_epilogue(int wbits, const void* d_x, int M, int K, int N, const 
                           e->activation};
     const uint8_t* w = static_cast<const uint8_t*>(d_w);
     const uint16_t* sc = static_cast<const uint16_t*>(d_scales);
-    if (L.rows) wq::launch_dense_decode(wbits, bf16, x, M, K, N, w, sc, groups, static_cast<uint16_t*>(d_y), s, &ep);
+    if (L.split) wq::launch_dense_split(wbits, bf16, x, M, K, N, w, sc, groups, static_cast<uint16_t*>(d_y), ep, s);
+    else if (L.rows) wq::launch_dense_decode(wbits, bf16, x, M, K, N, w, sc, groups, static_cast<uint16_t*>(d_y), s, &ep);
     else
         wq::launch_dense_large(wbits, bf16, x, M, K, N, w, sc, groups, ep, reinterpret_cast<float*>(ws),
                                static_cast<uint16_t*>(d_y), s);

@@ -232,6 +232,11 @@ int launch_gemm_prefill(int wbits, bool bf16, int stage, const GemmArgs& g, hipS
 int dense_large_split(int wbits, int M, int K, int N);
 void launch_dense_large(int wbits, bool bf16, const uint16_t* x, int M, int K, int N, const uint8_t* w,
                         const uint16_t* s, int groups, const Epilogue& ep, float* slabs, uint16_t* y, hipStream_t st);
+// one weight matrix with an epilogue where one round of workgroups covers it
+// (dense_split.hip); supported: whether it is the fastest kernel for these sizes
+bool dense_split_supported(int wbits, int M, int N);
+void launch_dense_split(int wbits, bool bf16, const uint16_t* x, int M, int K, int N, const uint8_t* w,
+                        const uint16_t* s, int groups, uint16_t* y, const Epilogue& ep, hipStream_t st);
 // y = f(sum over ks slabs [M, N] in ascending order + bias) + residual
 void launch_combine_epilogue(const float* slabs, int M, int N, int ks, bool bf16, const Epilogue& ep, uint16_t* y,
                              hipStream_t s);
