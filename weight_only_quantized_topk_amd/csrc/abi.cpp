@@ -1484,15 +1484,13 @@ namespace {
 struct EpilogueLayout {
     bool split;  // dense_split.hip: one launch
     bool rows;   // otherwise 1..128 rows in one launch
-    int ks;      // K slices through fp32 slabs
     size_t off_gather, total;
 };
 EpilogueLayout epilogue_layout(int wbits, int M, int K, int N, bool act_order) {
     EpilogueLayout L{};
-    L.split = wq::dense_split_supported(wbits, M, N);
+    L.split = wq::dense_split_supported(wbits, M, K, N);
     L.rows = !L.split && wq::dense_decode_supported(M, K);
-    L.ks = L.split || L.rows ? 1 : wq::dense_large_split(wbits, M, K, N);
-    size_t o = L.ks > 1 ? round256((size_t)L.ks * M * N * sizeof(float)) : 0;
+    size_t o = L.split || L.rows ? 0 : round256(wq::dense_large_slab_bytes(M, K, N));
     L.off_gather = o;
     if (act_order) o += round256((size_t)M * K * 2);
     L.total = o;
@@ -1504,7 +1502,7 @@ const char* epilogue_sizes(int wbits, int M, int K, int N) {
     if (M > MAX_PAIRS || K > (1 << 24) || N > (1 << 24)) return "M, K or N > 2^24";
     if (K % (wbits == 4 ? wq::WFmt<4>::KCHUNK : wq::WFmt<8>::KCHUNK)) return "K must be a multiple of 128 (int4) or 64 (int8)";
     if (N % 16) return "N must be a multiple of 16";
-    if (!wq::dense_split_supported(wbits, M, N) && !wq::dense_decode_supported(M, K) && !wq::prefill_fits((size_t)M + 128, K)) return "more than 4 GiB of activations";
+    if (!wq::dense_split_supported(wbits, M, K, N) && !wq::dense_decode_supported(M, K) && !wq::prefill_fits((size_t)M + 128, K)) return "more than 4 GiB of activations";
     if (M > 65535 * 64) return "more than 65535 * 64 rows";
     return nullptr;
 }

@@ -146,9 +146,6 @@ void launch_cfg(const uint16_t* x, int M, int K, int N, const uint8_t* w, const 
 // the plans: RT, R, waves, chunks ahead (int4 holds more of x a chunk: no room for 8 x 2 tiles)
 enum SplitPlan { SPLIT_1X1, SPLIT_2X1, SPLIT_4X1, SPLIT_4X2, SPLIT_4X4, SPLIT_8X2, SPLIT_NONE };
 
-#ifndef SPLIT_MAX
-#define SPLIT_MAX 128
-#endif
 constexpr int ROUND = 256;  // workgroups of one round: one a CU
 
 int64_t groups_of(int M, int N, int RT, int R) {
@@ -160,7 +157,12 @@ int64_t groups_of(int M, int N, int RT, int R) {
 // to 8 rows 2 tiles (int4 / int8 at 4 rows 23 / 28.5 against 27.7 / 43.4 us), int8 up to 16
 // rows 4 tiles (36.4 against 44.4; int4 29.4 against 28.0), int8 up to 32 rows 8 x 2 (43.9
 // against 47.3).  1 or 2 rows: dense_decode_kernel there (N = 6144, K = 4096: 6.8 / 7.8
-// against 7.0 / 8.0 us; N = 20480 18.4 / 27 against 22 / 28)
+// against 7.0 / 8.0 us; N = 20480 18.4 / 27 against 22 / 28).  Above 128 rows the tile of one
+// round against the large-batch kernel by the times both expect: 5 us and STEP_US a 1024
+// channels here (M = 256, N = K = 4096 23 / 20.5 us, that kernel 24 / 23; N = 1024 11.8 / 10.9,
+// that 18; but M = 160, K = 14336, N = 4096 70 / 60 us, that 46 / 42)
+constexpr float STEP_US[] = {1.0f, 1.25f, 1.75f, 2.6f, 4.1f, 3.9f};
+
 SplitPlan split_plan(int wbits, int M, int N) {
     if (groups_of(M, N, 1, 1) <= ROUND) return SPLIT_1X1;
     if (M <= 2) return SPLIT_NONE;
@@ -169,6 +171,7 @@ SplitPlan split_plan(int wbits, int M, int N) {
     if (groups_of(M, N, 4, 2) <= ROUND) return SPLIT_4X2;
     if (wbits == 4 && groups_of(M, N, 4, 4) <= ROUND) return SPLIT_4X4;
     if (wbits == 8 && groups_of(M, N, 8, 2) <= ROUND) return SPLIT_8X2;
+    if (M > 128) return SPLIT_NONE;
     if (M <= 8) return SPLIT_2X1;
     if (wbits == 8 && M <= 16) return SPLIT_4X1;
     if (wbits == 8 && M <= 32) return SPLIT_8X2;
@@ -191,7 +194,10 @@ void launch_split(const uint16_t* x, int M, int K, int N, const uint8_t* w, cons
 
 }  // namespace
 
-bool dense_split_supported(int wbits, int M, int N) { return M <= SPLIT_MAX && split_plan(wbits, M, N) != SPLIT_NONE; }
+bool dense_split_supported(int wbits, int M, int K, int N) {
+    const SplitPlan p = split_plan(wbits, M, N);
+    return p != SPLIT_NONE && (M <= 128 || 5.0f + (float)K / 1024.0f * STEP_US[p] <= dense_large_us(M, K, N));
+}
 
 void launch_dense_split(int wbits, bool bf16, const uint16_t* x, int M, int K, int N, const uint8_t* w,
                         const uint16_t* s, int groups, uint16_t* y, const Epilogue& ep, hipStream_t st) {

@@ -22,7 +22,7 @@ __device__ __forceinline__ float activate(float z, int f) {
     }
 }
 
-// outputs n0 .. n0 + 3 of row m (n0 a multiple of 4) to y [M, N]
+// outputs n0 .. n0 + 3 of row m (n0 a multiple of 4) to y, whose rows are N long
 template <bool BF16>
 __device__ __forceinline__ void finish4(const Epilogue& ep, f32x4 o, int64_t m, int n0, int N, uint16_t* y) {
     if (ep.bias) {

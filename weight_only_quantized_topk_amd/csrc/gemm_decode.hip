@@ -604,20 +604,20 @@ __global__ __launch_bounds__(256) void combine_act_kernel(const uint16_t* __rest
 // a dense projection's K slices and its epilogue
 template <bool BF16>
 __global__ __launch_bounds__(256) void combine_epilogue_kernel(const float* __restrict__ slabs, int M, int N, int ks,
-                                                               Epilogue ep, uint16_t* __restrict__ y) {
+                                                               Epilogue ep, uint16_t* __restrict__ y, int ld) {
     const size_t q = (size_t)blockIdx.x * 256 + threadIdx.x;  // 4 outputs each
     const size_t slab = (size_t)M * N;
     if (q * 4 >= slab) return;
     f32x4 acc = *reinterpret_cast<const f32x4*>(slabs + q * 4);
     for (int z = 1; z < ks; ++z) acc += *reinterpret_cast<const f32x4*>(slabs + z * slab + q * 4);
-    finish4<BF16>(ep, acc, (int64_t)(q * 4 / N), (int)(q * 4 % N), N, y);
+    finish4<BF16>(ep, acc, (int64_t)(q * 4 / N), (int)(q * 4 % N), ld, y);
 }
 
 void launch_combine_epilogue(const float* slabs, int M, int N, int ks, bool bf16, const Epilogue& ep, uint16_t* y,
-                             hipStream_t s) {
+                             int ld, hipStream_t s) {
     const dim3 grid((unsigned)(((size_t)M * N / 4 + 255) / 256));
-    if (bf16) hipLaunchKernelGGL(combine_epilogue_kernel<true>, grid, dim3(256), 0, s, slabs, M, N, ks, ep, y);
-    else hipLaunchKernelGGL(combine_epilogue_kernel<false>, grid, dim3(256), 0, s, slabs, M, N, ks, ep, y);
+    if (bf16) hipLaunchKernelGGL(combine_epilogue_kernel<true>, grid, dim3(256), 0, s, slabs, M, N, ks, ep, y, ld);
+    else hipLaunchKernelGGL(combine_epilogue_kernel<false>, grid, dim3(256), 0, s, slabs, M, N, ks, ep, y, ld);
 }
 
 void launch_combine_act(const uint16_t* y, int M, int topk, int n, bool bf16, uint16_t* out, hipStream_t s) {

@@ -132,7 +132,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(GemmArgs g) 
             // cached: the token tiles of an expert re-read its weight tiles
             w4[t] = __builtin_amdgcn_raw_buffer_load_b64(wres, wlane, tile_at(t) * tile_stride + c * CHUNK_BYTES + 8 * half, 0);
             const int grp = g.groups > 1 ? c : 0;
-            sc[t] = ssrc[(size_t)grp * g.n_out + tile_at(t) * TILE_ROWS];
+            sc[t] = ssrc[(size_t)grp * (DENSE ? g.ld : g.n_out) + tile_at(t) * TILE_ROWS];
         }
     };
     auto wload = [&](int step) {
@@ -293,7 +293,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(GemmArgs g) 
 #pragma unroll
                         for (int r = 0; r < 4; ++r) o[r] *= act_to_f32<BF16>(se[n0 + r]);
                     }
-                    if (gridDim.z == 1) finish4<BF16>(g.ep, o, m, n0, g.n_out, static_cast<uint16_t*>(g.out));
+                    if (gridDim.z == 1) finish4<BF16>(g.ep, o, m, n0, g.ld, static_cast<uint16_t*>(g.out));
                     else *reinterpret_cast<f32x4*>(g.slabs + ((size_t)blockIdx.z * g.M + m) * g.n_out + n0) = o;
                 }
             }
@@ -473,7 +473,73 @@ int launch_gemm_prefill(int wbits, bool bf16, int stage, const GemmArgs& g, hipS
     return ksplit;
 }
 // ------------------------------------------------------- one weight matrix
-static bool dense_large_small_tiles(int M) { return M <= 192; }
+// The shapes as STAGE_DENSE takes them, with the microseconds of a K step (64
+// channels) when 1, 2 or 3 workgroups share a CU, as measured over 160..1024 rows,
+// 560..20480 outputs, K 1024..14336 (int8; int4 about a tenth more).  512 x 128 does
+// the most a step; the others are for what does not fill its rounds.
+struct DenseShape {
+    int bn, bm, per_cu;
+    float step_us[3];
+};
+constexpr int DENSE_SHAPES = 3;
+static const DenseShape dense_shapes[DENSE_SHAPES] = {
+    {128, 64, 3, {0.58f, 0.80f, 1.10f}}, {128, 128, 3, {0.95f, 1.15f, 1.75f}}, {512, 128, 1, {1.80f, 0.f, 0.f}}};
+constexpr float LAUNCH_US = 3.0f, SLAB_BYTES_US = 6.0e6f;  // a launch; slabs written and read
+
+static float dense_cost(const DenseShape& sh, int M, int K, int N, int ks) {
+    const int64_t n = (int64_t)((N + sh.bn - 1) / sh.bn) * ((M + sh.bm - 1) / sh.bm) * ks;
+    const int64_t round = 256 * sh.per_cu, rest = n % round;
+    const float steps = (float)((K / PF_BK + ks - 1) / ks);
+    float us = (float)(n / round) * sh.step_us[sh.per_cu - 1];
+    if (rest) us += sh.step_us[(rest + 255) / 256 - 1];
+    us *= steps;
+    if (ks > 1) us += LAUNCH_US + (float)ks * (float)M * (float)N * 8.0f / SLAB_BYTES_US;
+    return us;
+}
+
+// columns [0, main) in full rounds of 512 x 128 (one launch), the others in one
+// shape and ks K slices
+struct DensePlan {
+    int main, shape, ks;
+    float us;
+};
+static DensePlan dense_rest(int M, int K, int N) {
+    DensePlan best{0, 0, 1, 0.0f};
+    if (N == 0) return best;
+    best.us = 1e30f;
+    static const int slices[] = {1, 2, 3, 4, 6, 8};
+    for (int i = 0; i < DENSE_SHAPES; ++i)
+        for (const int ks : slices) {
+            if (ks > 1 && K / PF_BK / ks < 8) break;
+            const float us = dense_cost(dense_shapes[i], M, K, N, ks);
+            if (us < best.us) best = DensePlan{0, i, ks, us};
+        }
+    return best;
+}
+// A grid of more than a round of 512 x 128 that does not fill its last one is cut
+// by columns (1024 rows, K = 7168, N = 20480: 320 workgroups are 1.25 rounds)
+static DensePlan dense_plan(int M, int K, int N) {
+    DensePlan best = dense_rest(M, K, N);
+    const int mt = (M + 127) / 128;
+    if (mt <= 256) {
+        const int cols = 256 / mt * 512;  // of a round
+        const int rounds = N / cols;
+        if (rounds > 0) {
+            DensePlan cut = dense_rest(M, K, N - rounds * cols);
+            cut.main = rounds * cols;
+            cut.us += (float)rounds * (float)(K / PF_BK) * dense_shapes[DENSE_SHAPES - 1].step_us[0] + (cut.main < N ? LAUNCH_US : 0.0f);
+            if (cut.us < best.us) best = cut;
+        }
+    }
+    return best;
+}
+
+float dense_large_us(int M, int K, int N) { return dense_plan(M, K, N).us; }
+
+size_t dense_large_slab_bytes(int M, int K, int N) {
+    const DensePlan p = dense_plan(M, K, N);
+    return p.ks > 1 ? (size_t)p.ks * M * (N - p.main) * sizeof(float) : 0;
+}
 
 template <int WBITS, bool BF16, int NW, int RT, int BM, int OCC>
 static void launch_dense_cfg(const GemmArgs& g, int ksplit, hipStream_t s) {
@@ -482,16 +548,26 @@ static void launch_dense_cfg(const GemmArgs& g, int ksplit, hipStream_t s) {
     hipLaunchKernelGGL((gemm_prefill_kernel<WBITS, BF16, STAGE_DENSE, NW, RT, BM, OCC>), grid, dim3(NW * 64), 0, s, g);
 }
 
-int dense_large_split(int wbits, int M, int K, int N) {
-    const int bs = dense_large_small_tiles(M) ? 64 : 128;
-    return prefill_down_split(M, 1, (N + 127) / 128 * 128, K, bs);
-}
-
 template <int WBITS, bool BF16>
-static void launch_dense_shape(const GemmArgs& g, int ksplit, hipStream_t s) {
-    if (dense_large_small_tiles(g.M)) launch_dense_cfg<WBITS, BF16, 4, 2, 64, 3>(g, ksplit, s);
-    else if (g.n_out % 512 == 0) launch_dense_cfg<WBITS, BF16, 8, 4, 128, 1>(g, ksplit, s);
-    else launch_dense_cfg<WBITS, BF16, 4, 2, 128, 3>(g, ksplit, s);
+static void launch_dense_plan(GemmArgs g, const DensePlan& p, hipStream_t s) {
+    const int N = g.n_out;
+    if (p.main > 0) {
+        g.n_out = p.main;
+        launch_dense_cfg<WBITS, BF16, 8, 4, 128, 1>(g, 1, s);
+        if (p.main == N) return;
+        // the other columns: packed tiles, scales, bias, residual and y from there on
+        g.w += (size_t)p.main * g.k_in * WBITS / 8;
+        g.s += p.main;
+        g.out = static_cast<uint16_t*>(g.out) + p.main;
+        if (g.ep.bias) g.ep.bias += p.main;
+        if (g.ep.residual) g.ep.residual += p.main;
+        g.n_out = N - p.main;
+    }
+    if (p.shape == 0) launch_dense_cfg<WBITS, BF16, 4, 2, 64, 3>(g, p.ks, s);
+    else if (p.shape == 1) launch_dense_cfg<WBITS, BF16, 4, 2, 128, 3>(g, p.ks, s);
+    else launch_dense_cfg<WBITS, BF16, 8, 4, 128, 1>(g, p.ks, s);
+    if (p.ks > 1)
+        launch_combine_epilogue(g.slabs, g.M, g.n_out, p.ks, BF16, g.ep, static_cast<uint16_t*>(g.out), g.ld, s);
 }
 
 void launch_dense_large(int wbits, bool bf16, const uint16_t* x, int M, int K, int N, const uint8_t* w,
@@ -505,15 +581,15 @@ void launch_dense_large(int wbits, bool bf16, const uint16_t* x, int M, int K, i
     g.topk = 1;
     g.E = 1;
     g.n_out = N;
+    g.ld = N;
     g.k_in = K;
     g.groups = groups;
     g.slabs = slabs;
     g.ep = ep;
-    const int ks = dense_large_split(wbits, M, K, N);
-    if (wbits == 4) launch_dense_shape<4, false>(g, ks, st);
-    else if (bf16) launch_dense_shape<8, true>(g, ks, st);
-    else launch_dense_shape<8, false>(g, ks, st);
-    if (ks > 1) launch_combine_epilogue(slabs, M, N, ks, bf16, ep, y, st);
+    const DensePlan p = dense_plan(M, K, N);
+    if (wbits == 4) launch_dense_plan<4, false>(g, p, st);
+    else if (bf16) launch_dense_plan<8, true>(g, p, st);
+    else launch_dense_plan<8, false>(g, p, st);
 }
 #endif  // WQ_PREFILL_KERNEL_ONLY
 

@@ -109,6 +109,7 @@ struct GemmArgs {
     int cap;
     int y_act;                // large-batch DOWN without a K split: Y rows in the activation type
     // STAGE_DENSE (x in a, y [M, n_out] in out)
+    int ld;                   // row length of y and of the scales (n_out of its columns are computed)
     float* slabs;             // a K slice each [M, n_out], where K is split
     Epilogue ep;              // applied where it is not
 };
@@ -226,20 +227,20 @@ int prefill_down_split_max(int T, int E, int n_out, int k_in);
 // returns the number of K slices (Y slabs) it wrote
 int launch_gemm_prefill(int wbits, bool bf16, int stage, const GemmArgs& g, hipStream_t s);
 
-// one weight matrix with an epilogue, more rows than dense_decode_supported
-// takes (gemm_prefill.hip): K slices (and the fp32 slabs [ks][M, N] that they
-// are added through) and the launches
-int dense_large_split(int wbits, int M, int K, int N);
+// one weight matrix with an epilogue at large batches (gemm_prefill.hip): the
+// fp32 slabs that a split of K is added through (0: none), the time its plan expects
+size_t dense_large_slab_bytes(int M, int K, int N);
+float dense_large_us(int M, int K, int N);
 void launch_dense_large(int wbits, bool bf16, const uint16_t* x, int M, int K, int N, const uint8_t* w,
                         const uint16_t* s, int groups, const Epilogue& ep, float* slabs, uint16_t* y, hipStream_t st);
 // one weight matrix with an epilogue where one round of workgroups covers it
 // (dense_split.hip); supported: whether it is the fastest kernel for these sizes
-bool dense_split_supported(int wbits, int M, int N);
+bool dense_split_supported(int wbits, int M, int K, int N);
 void launch_dense_split(int wbits, bool bf16, const uint16_t* x, int M, int K, int N, const uint8_t* w,
                         const uint16_t* s, int groups, uint16_t* y, const Epilogue& ep, hipStream_t st);
-// y = f(sum over ks slabs [M, N] in ascending order + bias) + residual
+// y = f(sum over ks slabs [M, N] in ascending order + bias) + residual; y's rows are ld long
 void launch_combine_epilogue(const float* slabs, int M, int N, int ks, bool bf16, const Epilogue& ep, uint16_t* y,
-                             hipStream_t s);
+                             int ld, hipStream_t s);
 
 // the routing arrays of a dense layer (E = 1, top-1): sorted = 0..M-1 then pad
 // ids M up to cap, expert 0 per block, ntpp = M rounded up to BS, weights 1
