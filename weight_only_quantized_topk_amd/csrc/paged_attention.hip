@@ -488,40 +488,42 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
     }
 }
 
-// the pieces of sequences in more than one share, for one head: 256 threads as
-// 256 / (D / 4) rows of D / 4 vectors of 4 channels; a row joins every so many-th
-// piece, JOIN_AHEAD of them loaded together with their statistics, then the
-// rows are joined.  A workgroup looks at `shares` of them one after another, in
-// each of which at most one such sequence begins
+// The pieces of sequences in more than one share: 256 threads as rows of D / 4
+// vectors of 4 channels.  The rows are shared out over `hb` heads; a head's rows take
+// every so many-th piece, JOIN_AHEAD of them loaded together with their statistics, and
+// are joined through LDS where there are several.  A workgroup looks at `shares`
+// of them one after another, in each of which at most one such sequence begins.
 constexpr int JOIN_AHEAD = 8;
 
 template <bool BF16>
-__global__ __launch_bounds__(256) void paged_join_kernel(PagedAttnArgs g, int shares) {
+__global__ __launch_bounds__(256) void paged_join_kernel(PagedAttnArgs g, int shares, int hb) {
     __shared__ f32x4 so[256];
     __shared__ float sm[256], sl[256];
-    const int head = blockIdx.x, tid = threadIdx.x;
-    const int quads = g.D / 4, side = 256 / quads;
+    const int tid = threadIdx.x;
+    const int quads = g.D / 4, per = 256 / quads / hb;  // rows of a head
     const int row = tid / quads, c = 4 * (tid - row * quads);
+    const int head = blockIdx.x * hb + row / per, first = row - row / per * per;
+    const bool mine_too = row < per * hb && head < g.heads;
     // lane k of every wave: the k-th share's sequence and its pieces (0: none begins there to be joined)
     const int mine = blockIdx.y * shares + (tid & 63);
     const bool there = (tid & 63) < shares && mine < g.splits;
     const int bs = there ? g.part_at[2 * mine] : 0, ns = there ? g.part_at[2 * mine + 1] : 0;
     for (uint64_t todo = __ballot(ns > 0); todo != 0; todo &= todo - 1) {
-        const int k = __ffsll((unsigned long long)todo) - 1;
-        const int x = blockIdx.y * shares + k;
-        const int n = __builtin_amdgcn_readlane(ns, k), b = __builtin_amdgcn_readlane(bs, k);
+        const int k0 = __ffsll((unsigned long long)todo) - 1;
+        const int x = blockIdx.y * shares + k0;
+        const int n = __builtin_amdgcn_readlane(ns, k0), b = __builtin_amdgcn_readlane(bs, k0);
         float m = M_NONE, l = 0.0f;
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        for (int p0 = row; p0 < n && row < side; p0 += side * JOIN_AHEAD) {
+        for (int p0 = first; p0 < n && mine_too; p0 += per * JOIN_AHEAD) {
             float pm[JOIN_AHEAD], pl[JOIN_AHEAD];
             f32x4 po[JOIN_AHEAD];
 #pragma unroll
             for (int k = 0; k < JOIN_AHEAD; ++k) {
                 // piece 0 is share x's second, piece p share x + p's first; past the last: it again, without weight
-                const int p = min(p0 + k * side, n - 1);
+                const int p = min(p0 + k * per, n - 1);
                 const int64_t slot = (int64_t)(2 * (x + p) + (p == 0)) * g.heads + head;
-                pm[k] = p0 + k * side < n ? g.part_ml[2 * slot] : M_NONE;
-                pl[k] = p0 + k * side < n ? g.part_ml[2 * slot + 1] : 0.0f;
+                pm[k] = p0 + k * per < n ? g.part_ml[2 * slot] : M_NONE;
+                pl[k] = p0 + k * per < n ? g.part_ml[2 * slot + 1] : 0.0f;
                 po[k] = *reinterpret_cast<const f32x4*>(g.part_o + slot * g.D + c);
             }
             float top = m;
@@ -533,32 +535,37 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedAttnArgs g, int sh
             o *= f0;
 #pragma unroll
             for (int k = 0; k < JOIN_AHEAD; ++k) {
-                const float f = p0 + k * side < n ? __builtin_amdgcn_exp2f(pm[k] - top) : 0.0f;
+                const float f = p0 + k * per < n ? __builtin_amdgcn_exp2f(pm[k] - top) : 0.0f;
                 l += f * pl[k];
-                if (p0 + k * side < n) o += f * po[k];  // (a repeated piece may hold infinities)
+                if (p0 + k * per < n) o += f * po[k];  // (a repeated piece may hold infinities)
             }
         }
-        so[tid] = o;
-        sm[tid] = m;
-        sl[tid] = l;
-        __syncthreads();
-        if (row == 0) {
-            float top = m;
-            for (int i = 1; i < side; ++i) top = fmaxf(top, sm[i * quads]);
-            const float f0 = __builtin_amdgcn_exp2f(m - top);
-            o *= f0;
-            float sum = l * f0;
-            for (int i = 1; i < side; ++i) {
-                const float f = __builtin_amdgcn_exp2f(sm[i * quads] - top);
-                sum += f * sl[i * quads];
-                o += f * so[i * quads + tid];
+        if (per > 1) {
+            so[tid] = o;
+            sm[tid] = m;
+            sl[tid] = l;
+            __syncthreads();
+            if (first == 0 && mine_too) {
+                float top = m;
+                for (int i = 1; i < per; ++i) top = fmaxf(top, sm[tid + i * quads]);
+                const float f0 = __builtin_amdgcn_exp2f(m - top);
+                o *= f0;
+                l *= f0;
+                for (int i = 1; i < per; ++i) {
+                    const float f = __builtin_amdgcn_exp2f(sm[tid + i * quads] - top);
+                    l += f * sl[tid + i * quads];
+                    o += f * so[tid + i * quads];
+                }
+                m = top;
             }
-            const float inv = sum == 0.0f ? 0.0f : g.v_scale / sum;
+            __syncthreads();
+        }
+        if (first == 0 && mine_too) {
+            const float inv = l == 0.0f ? 0.0f : g.v_scale / l;
             *reinterpret_cast<u32x2*>(g.out + (int64_t)b * g.out_stride + (int64_t)head * g.D + c) =
                 u32x2{f32_to_act2<BF16>(o[0] * inv, o[1] * inv), f32_to_act2<BF16>(o[2] * inv, o[3] * inv)};
-            if (g.lse && c == 0) g.lse[(int64_t)b * g.heads + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * LN2;
+            if (g.lse && c == 0) g.lse[(int64_t)b * g.heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * LN2;
         }
-        __syncthreads();
     }
 }
 
@@ -604,10 +611,12 @@ void launch_type(const PagedAttnArgs& g, hipStream_t s) {
     else if (g.mode == KV_E4M3_ROW) launch_dim<BF16, KV_E4M3_ROW>(g, s);
     else launch_dim<BF16, KV_E4M3_STATIC>(g, s);
     if (g.splits > 0) {
-        // about one sequence to join a workgroup: few of the shares begin one where there are few
-        const int shares = std::max(1, std::min(64, g.splits / g.B));
-        hipLaunchKernelGGL(paged_join_kernel<BF16>, dim3(g.heads, (g.splits + shares - 1) / shares), dim3(256), 0, s, g,
-                           shares);
+        // about one sequence to join a workgroup: few of the shares begin one where there are few.  A row a
+        // head where a sequence has few pieces (48 heads, 228 sequences in 256 shares: 17 us a head a workgroup)
+        const int shares = std::max(1, std::min(64, g.splits / g.B)), rows = 256 / (g.D / 4);
+        const int hb = g.splits <= JOIN_AHEAD * g.B ? std::min(rows, g.heads) : 1;
+        hipLaunchKernelGGL(paged_join_kernel<BF16>, dim3((g.heads + hb - 1) / hb, (g.splits + shares - 1) / shares),
+                           dim3(256), 0, s, g, shares, hb);
     }
 }
 
