@@ -647,7 +647,7 @@ def _dense_epilogue(wbits, x, N, w_packed, scales, group_size, k_perm, out, work
         e.d_residual, e.residual_stride = residual.data_ptr(), _row_stride(residual)
     new = []
     if out is None:
-        new.append(out := _alloc(stream, torch.empty, (M, N), dtype=dt, device=dev))
+        out = _new(stream, new, (M, N), dt, dev)
     else:
         _check(out, "out", (M, N), same, dev)
     sizes = None if lora is None else _lora_sizes(x, *lora, out)  # before anything is launched
@@ -655,7 +655,7 @@ def _dense_epilogue(wbits, x, N, w_packed, scales, group_size, k_perm, out, work
     if workspace is None:
         nb = L.dense_epilogue_workspace_bytes(wbits, M, K, N, int(k_perm is not None))
         if nb:
-            workspace = _alloc(stream, torch.empty, nb, dtype=torch.uint8, device=dev)
+            workspace = _new(stream, [], nb, torch.uint8, dev)
     elif not workspace.is_contiguous() or workspace.device != dev:
         raise ValueError("workspace must be contiguous on %s" % dev)
     tail = (C.byref(e), out.data_ptr(), act, _ptr(workspace),
@@ -756,47 +756,64 @@ def _kv_desc(c: KVCache, act, device=None) -> WqKvCache:
     """Checks a cache for a call with activations of type act -> its descriptor."""
     torch = _torch()
     k, v, ks, vs = c
-    shape = k.shape
+    shape, dt = k.shape, k.dtype
     if len(shape) != 4:
         raise ValueError("the cache must be [pages, kv_heads, page_size, head_dim], got %s" % list(shape))
-    codes = k.dtype in (torch.uint8, torch.float8_e4m3fn)
-    if not codes and k.dtype != act:
-        raise TypeError("the cache must be %s or E4M3 codes, got %s" % (act, k.dtype))
+    codes = dt != act
+    if codes and dt not in (torch.uint8, torch.float8_e4m3fn):
+        raise TypeError("the cache must be %s or E4M3 codes, got %s" % (act, dt))
     dev = k.device if device is None else device
-    _check(k, "cache k", shape, (k.dtype,), dev)
-    _check(v, "cache v", shape, (k.dtype,), dev)
+    if not (v.shape == shape and v.dtype == dt and k.device == dev and v.device == dev and k.is_contiguous()
+            and v.is_contiguous()):
+        _check(k, "cache k", shape, (dt,), dev)
+        _check(v, "cache v", shape, (dt,), dev)
     P, H, S, D = shape
-    _int32(pages=P, kv_heads=H, page_size=S, head_dim=D)
-    d = WqKvCache(C.sizeof(WqKvCache), k.data_ptr(), v.data_ptr(), None, None, 0.0, 0.0,
-                  WQ_E4M3 if codes else act_code(act), P, H, S, D)
-    if (ks is None) != (vs is None) or codes != (ks is not None):
-        raise ValueError("a cache of codes has k_scale and v_scale, one of 16-bit values neither")
+    if P > 0x7fffffff or H > 0x7fffffff or S > 0x7fffffff or D > 0x7fffffff:
+        _int32(pages=P, kv_heads=H, page_size=S, head_dim=D)
     if codes:
+        if ks is None or vs is None:
+            raise ValueError("a cache of codes has k_scale and v_scale")
         if isinstance(ks, torch.Tensor) != isinstance(vs, torch.Tensor):
             raise TypeError("k_scale and v_scale are both tensors or both numbers")
         if isinstance(ks, torch.Tensor):
             _check(ks, "cache k_scale", shape[:3], (torch.float32,), dev)
             _check(vs, "cache v_scale", shape[:3], (torch.float32,), dev)
-            d.d_k_scales, d.d_v_scales = ks.data_ptr(), vs.data_ptr()
-        else:
-            d.k_scale, d.v_scale = ks, vs
-    return d
+            return WqKvCache(_KV_SIZE, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), 0.0, 0.0, WQ_E4M3, P,
+                             H, S, D)
+        return WqKvCache(_KV_SIZE, k.data_ptr(), v.data_ptr(), None, None, ks, vs, WQ_E4M3, P, H, S, D)
+    if ks is not None or vs is not None:
+        raise ValueError("a cache of 16-bit values has no scales")
+    return WqKvCache(_KV_SIZE, k.data_ptr(), v.data_ptr(), None, None, 0.0, 0.0, act_code(act), P, H, S, D)
 
 
-def _head_rows(t, name: str, shape, act, device) -> int:
-    """A [rows, heads, head_dim] argument whose heads lie next to each other (rows
-    may be strided) -> its row stride in elements."""
-    if t.shape != shape:
-        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+_KV_SIZE = C.sizeof(WqKvCache)
+
+
+def _head_rows(t, name: str, T: int, H: int, D: int, act, device) -> int:
+    """A [T, H, D] argument whose heads lie next to each other (rows may be
+    strided) -> its row stride in elements."""
+    if t.shape != (T, H, D):
+        raise ValueError("%s must be %s, got %s" % (name, [T, H, D], list(t.shape)))
     if t.dtype != act:
         raise TypeError("%s must be %s, got %s" % (name, act, t.dtype))
     if t.device != device:
-        raise ValueError("%s is on %s, the cache on %s" % (name, t.device, device))
-    T, H, D = shape
-    st = t.stride()
-    if t.numel() and (st[2] != 1 and D > 1 or st[1] != D and H > 1 or st[0] < H * D and T > 1):
-        raise ValueError("%s must be contiguous in its rows, got strides %s" % (name, list(st)))
-    return st[0] if T > 1 else H * D
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+    s0, s1, s2 = t.stride()
+    if T <= 1:
+        s0 = H * D
+    if (s2 != 1 and D > 1 or s1 != D and H > 1 or s0 < H * D) and t.numel():
+        raise ValueError("%s must be contiguous in its rows, got strides %s" % (name, list(t.stride())))
+    return s0
+
+
+def _new(stream, new, shape, dtype, device):
+    """A buffer that the call allocates, noted in `new`."""
+    if stream is None:
+        t = _torch().empty(shape, dtype=dtype, device=device)
+    else:
+        t = _alloc(stream, _torch().empty, shape, dtype=dtype, device=device)
+    new.append(t)
+    return t
 
 
 def kv_cache_write(k, v, cache: KVCache, slots, stream=None) -> KVCache:
@@ -804,15 +821,14 @@ def kv_cache_write(k, v, cache: KVCache, slots, stream=None) -> KVCache:
     [T, kv_heads, head_dim] bf16/fp16 (device; rows may be strided), slots [T]
     int64 (page * page_size + position; outside the cache, as -1 of a padding
     token: not written).  The slots of a call differ.  Returns the cache."""
-    torch = _torch()
-    dev = k.device
-    d = _kv_desc(cache, k.dtype, dev)
-    act = act_code(k.dtype)
-    shape = (k.shape[0], d.kv_heads, d.head_dim)
-    _int32(T=shape[0])
-    ks, vs = _head_rows(k, "k", shape, k.dtype, dev), _head_rows(v, "v", shape, k.dtype, dev)
-    _check(slots, "slots", shape[:1], (torch.int64,), dev)
-    check(load().wq_kv_cache_write(C.byref(d), k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), shape[0], act,
+    dt, dev = k.dtype, k.device
+    act = act_code(dt)
+    d = _kv_desc(cache, dt, dev)
+    T, H, D = k.shape[0], d.kv_heads, d.head_dim
+    _int32(T=T)
+    ks, vs = _head_rows(k, "k", T, H, D, dt, dev), _head_rows(v, "v", T, H, D, dt, dev)
+    _check(slots, "slots", (T,), (_torch().int64,), dev)
+    check(load().wq_kv_cache_write(C.byref(d), k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), T, act,
                                    _stream(stream)), "wq_kv_cache_write")
     return cache
 
@@ -821,22 +837,25 @@ def kv_cache_read(cache: KVCache, slots, act, k=None, v=None, stream=None):
     """The rows of slots [T] int64 back -> (k, v) [T, kv_heads, head_dim] of type
     act (rows of given buffers may be strided); zeros where a slot is outside
     the cache."""
-    torch = _torch()
     dev = cache.k.device
-    d = _kv_desc(cache, act, dev)
     code = act_code(act)
+    d = _kv_desc(cache, act, dev)
     if slots.dim() != 1:
         raise ValueError("slots must be [T], got %s" % list(slots.shape))
-    _check(slots, "slots", slots.shape, (torch.int64,), dev)
-    shape = (slots.shape[0], d.kv_heads, d.head_dim)
-    _int32(T=shape[0])
+    T, H, D = slots.shape[0], d.kv_heads, d.head_dim
+    _check(slots, "slots", (T,), (_torch().int64,), dev)
+    _int32(T=T)
     new = []
+    ks = vs = H * D
     if k is None:
-        new.append(k := _alloc(stream, torch.empty, shape, dtype=act, device=dev))
+        k = _new(stream, new, (T, H, D), act, dev)
+    else:
+        ks = _head_rows(k, "k", T, H, D, act, dev)
     if v is None:
-        new.append(v := _alloc(stream, torch.empty, shape, dtype=act, device=dev))
-    ks, vs = _head_rows(k, "k", shape, act, dev), _head_rows(v, "v", shape, act, dev)
-    check(load().wq_kv_cache_read(C.byref(d), slots.data_ptr(), shape[0], k.data_ptr(), ks, v.data_ptr(), vs, code,
+        v = _new(stream, new, (T, H, D), act, dev)
+    else:
+        vs = _head_rows(v, "v", T, H, D, act, dev)
+    check(load().wq_kv_cache_read(C.byref(d), slots.data_ptr(), T, k.data_ptr(), ks, v.data_ptr(), vs, code,
                                   _stream(stream)), "wq_kv_cache_read")
     _keep_for(stream, *new)
     return k, v
@@ -858,7 +877,7 @@ def paged_attention(q, cache: KVCache, block_table, lengths, scale: Optional[flo
     unless given; window: the last so many tokens only.  -> out like q, with
     want_lse (out, lse [B, heads] float32), the logarithm of each row's sum."""
     torch = _torch()
-    dev, dt = q.device, q.dtype
+    dt, dev = q.dtype, q.device
     act = act_code(dt)
     d = _kv_desc(cache, dt, dev)
     if q.dim() != 3 or block_table.dim() != 2:
@@ -869,33 +888,36 @@ def paged_attention(q, cache: KVCache, block_table, lengths, scale: Optional[flo
     if D != d.head_dim or heads % d.kv_heads:
         raise ValueError("q must be [B, a multiple of %d heads, %d], got %s" % (d.kv_heads, d.head_dim, list(q.shape)))
     _int32(B=B, heads=heads, width=width, window=window)
-    qs = _head_rows(q, "q", (B, heads, D), dt, dev)
-    _check(block_table, "block_table", (B, width), (torch.int32,), dev)
-    _check(lengths, "lengths", (B,), (torch.int32,), dev)
+    qs = _head_rows(q, "q", B, heads, D, dt, dev)
+    i32 = (torch.int32,)
+    _check(block_table, "block_table", (B, width), i32, dev)
+    _check(lengths, "lengths", (B,), i32, dev)
     if lse is not None and not want_lse:
         raise ValueError("lse goes with want_lse")
     new = []
     if out is None:
-        new.append(out := _alloc(stream, torch.empty, (B, heads, D), dtype=dt, device=dev))
-    os_ = _head_rows(out, "out", (B, heads, D), dt, dev)
+        out, os_ = _new(stream, new, (B, heads, D), dt, dev), heads * D
+    else:
+        os_ = _head_rows(out, "out", B, heads, D, dt, dev)
     if want_lse:
         if lse is None:
-            new.append(lse := _alloc(stream, torch.empty, (B, heads), dtype=torch.float32, device=dev))
+            lse = _new(stream, new, (B, heads), torch.float32, dev)
         else:
             _check(lse, "lse", (B, heads), (torch.float32,), dev)
     L = load()
     if workspace is None:
         nb = L.wq_paged_attention_workspace_bytes(B, heads, d.kv_heads, D, d.page_size, width, window)
         if nb:
-            workspace = _alloc(stream, torch.empty, nb, dtype=torch.uint8, device=dev)
-    elif not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError("workspace must be contiguous on %s" % dev)
+            workspace = _new(stream, [], nb, torch.uint8, dev)
+    else:
+        if not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError("workspace must be contiguous on %s" % dev)
+        nb = workspace.numel() * workspace.element_size()
     check(L.wq_paged_attention(C.byref(d), q.data_ptr(), qs, B, heads, block_table.data_ptr(), width,
                                lengths.data_ptr(), D ** -0.5 if scale is None else scale, window, out.data_ptr(), os_,
-                               _ptr(lse), act, _ptr(workspace),
-                               0 if workspace is None else workspace.numel() * workspace.element_size(),
-                               _stream(stream)), "wq_paged_attention")
-    _keep_for(stream, *new)
+                               _ptr(lse), act, _ptr(workspace), nb, _stream(stream)), "wq_paged_attention")
+    if stream is not None:
+        _keep_for(stream, *new)
     return (out, lse) if want_lse else out
 
 
