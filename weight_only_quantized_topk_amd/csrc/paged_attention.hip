@@ -55,19 +55,14 @@ constexpr float M_NONE = -3.4028234e38f;  // the running maximum before any scor
 constexpr float M_SLACK = 8.0f;    // scores may pass it by this much (exponents of 2)
 constexpr float LN2 = 0.693147180559945309f;
 
-// the sequence's tokens [lo, len) and its tiles of 32, the first beginning at
-// lo rounded down to half a tile
-struct Span {
-    int lo, len, begin, tiles;
-};
-__device__ __forceinline__ Span span_of(const PagedAttnArgs& g, int len) {
-    Span s;
-    const int64_t most = (int64_t)g.width * g.page_size;
-    s.len = (int)min((int64_t)max(len, 0), most);
-    s.lo = g.window > 0 ? max(0, s.len - g.window) : 0;
-    s.begin = s.lo & ~(KV_TOKENS - 1);
-    s.tiles = (int)(((int64_t)s.len - s.begin + TILE - 1) / TILE);
-    return s;
+// a sequence's tokens [lo, len), its first tile beginning at lo rounded down to
+// half a tile, and its steps of a workgroup (NW tiles, the last one partly idle);
+// at least one, so that every sequence is in some workgroup's share
+__device__ __forceinline__ int len_of(const PagedAttnArgs& g, int len) { return min(max(len, 0), g.width * g.page_size); }
+__device__ __forceinline__ int lo_of(const PagedAttnArgs& g, int len) { return g.window > 0 ? max(0, len - g.window) : 0; }
+__device__ __forceinline__ int begin_of(const PagedAttnArgs& g, int len) { return lo_of(g, len) & ~(KV_TOKENS - 1); }
+__device__ __forceinline__ int steps_of(const PagedAttnArgs& g, int len) {
+    return max(1, (len - begin_of(g, len) + NW * TILE - 1) / (NW * TILE));
 }
 
 // a wave-uniform index into an array that the kernel does not write: a scalar
@@ -92,23 +87,18 @@ __device__ __forceinline__ int wave_scan(int v) {
     return v;
 }
 
-// steps of a workgroup (NW tiles, the last one of a sequence partly idle); at
-// least one each, so that every sequence is in some workgroup's share
-__device__ __forceinline__ int steps_for(int tiles) { return max(1, (tiles + NW - 1) / NW); }
-__device__ __forceinline__ int steps_of(const PagedAttnArgs& g, int b) { return steps_for(span_of(g, g.lengths[b]).tiles); }
-
 // workgroup x's share of the batch's steps, one sequence's after another's: `steps`
 // from step `off` of sequence b on (0: none); every share but the last has `cut`
 struct Share {
     int b, off, steps, cut;
 };
 __device__ __forceinline__ Share share_of(const PagedAttnArgs& g, int x) {
-    if (g.splits == 0) return Share{x, 0, steps_of(g, x), 0};
+    if (g.splits == 0) return Share{x, 0, steps_of(g, len_of(g, g.lengths[x])), 0};
     const int lane = threadIdx.x & 63;
     const int each = (g.B + 63) / 64;  // consecutive sequences of a lane
     const int b0 = lane * each, b1 = min(b0 + each, g.B);
     int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += steps_of(g, b);
+    for (int b = b0; b < b1; ++b) sum += steps_of(g, len_of(g, g.lengths[b]));
     const int upto = wave_scan(sum);
     const int total = __builtin_amdgcn_readlane(upto, 63);
     const int cut = (total + g.splits - 1) / g.splits;
@@ -119,7 +109,7 @@ __device__ __forceinline__ Share share_of(const PagedAttnArgs& g, int x) {
     int off = lo - (__builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(sum, owner));
     int b = owner * each;
     for (; b < g.B - 1; ++b) {
-        const int n = steps_of(g, b);
+        const int n = steps_of(g, len_of(g, g.lengths[b]));
         if (off < n) break;
         off -= n;
     }
@@ -202,7 +192,9 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
     const int nh = min(16, group - h0);           // heads of this workgroup
     const int head0 = kvh * group + h0;
     const uint32_t page16 = (uint32_t)g.page_size / KV_TOKENS;
-    const uint64_t magic = ((uint64_t)1 << 32) / page16 + ((((uint64_t)1 << 32) % page16) ? 1 : 0);
+    // u / page16 by one multiplication: the host checks the range
+    const uint32_t magic = (uint32_t)(0xffffffffu / page16 + 1);
+    auto column_of = [&](uint32_t u) { return page16 == 1 ? u : __umulhi(u, magic); };
 
     // half a tile: 16 tokens, in one page; those past the sequence read its last
     struct Half {
@@ -249,21 +241,38 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
     const int cut = __builtin_amdgcn_readfirstlane(share.cut);
     int goes_on = 0, begins = 0;  // pieces of the sequence that begins here and ends in another share; it
     if (left > 0) {
-        // one sequence's steps [s0, s1) of all its `steps` in the share
+        // a sequence's steps in the share (up to s1), and blocks of AHEAD of them, whose pages one vector load
+        // fetches a block ahead: lane 2 k + s has that of half s of this wave's tile in the block's k-th step
+        constexpr int AHEAD = 32;
         struct Part {
-            int b, s0, s1, steps, lo, len, begin;
+            int b, len, s1;
         };
         auto part_of = [&](int b, int off) {
-            const Span sp = span_of(g, uniform_at(g.lengths, b));
-            const int steps = steps_for(sp.tiles);
-            return Part{b, off, min(steps, off + left), steps, sp.lo, sp.len, sp.begin};
+            const int len = len_of(g, uniform_at(g.lengths, b));
+            return Part{b, len, min(steps_of(g, len), off + left)};
         };
-        // half s of this wave's tile in step i, its sequence's last 16 tokens past the end
-        auto half_at = [&](const Part& pt, int i, int s) {
-            const int tok = pt.begin + TILE * (NW * min(i, pt.s1 - 1) + wave) + KV_TOKENS * s;
-            const uint32_t u = (uint32_t)min(tok, max(pt.len - 1, 0)) / KV_TOKENS;
-            const uint32_t col = (uint32_t)(((uint64_t)u * magic) >> 32);  // u / page16: the host checks the range
-            const int page = uniform_at(g.table, (int64_t)pt.b * g.width + col);
+        // the block after the one from `base` on: of the same sequence, or of the next
+        auto follow = [&](const Part& p, int base, Part& q, int& qbase) {
+            if (base + AHEAD < p.s1) {
+                q = p;
+                qbase = base + AHEAD;
+                return true;
+            }
+            if (left <= 0 || p.b + 1 >= g.B) return false;
+            q = part_of(p.b + 1, 0);
+            left -= q.s1;
+            qbase = 0;
+            return true;
+        };
+        // half s of the wave's tile in step i, the sequence's last 16 tokens past the end
+        auto half16 = [&](const Part& p, int i, int s) {
+            return (uint32_t)min(begin_of(g, p.len) + TILE * (NW * i + wave) + KV_TOKENS * s, max(p.len - 1, 0)) / KV_TOKENS;
+        };
+        auto pages_of = [&](const Part& p, int base) {
+            return g.table[(int64_t)p.b * g.width + column_of(half16(p, min(base + (lane >> 1), p.s1 - 1), lane & 1))];
+        };
+        auto half_at = [&](const Part& p, int i, int s, int page) {
+            const uint32_t u = half16(p, i, s), col = column_of(u);
             Half h;
             h.good = page >= 0 && page < g.pages;  // a bad page holds no tokens
             h.rows = ((int64_t)(h.good ? page : 0) * g.kv_heads + kvh) * g.page_size + (u - col * page16) * KV_TOKENS;
@@ -280,8 +289,13 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
             }
         };
 
-        Part pt = part_of(__builtin_amdgcn_readfirstlane(share.b), __builtin_amdgcn_readfirstlane(share.off));
-        left -= pt.s1 - pt.s0;
+        int s0 = __builtin_amdgcn_readfirstlane(share.off);  // the sequence's first step in the share
+        Part pt = part_of(__builtin_amdgcn_readfirstlane(share.b), s0), np = pt;
+        left -= pt.s1 - s0;
+        int base = s0, nbase = 0;
+        int pages = pages_of(pt, base), npages = 0;
+        bool more = follow(pt, base, np, nbase);
+        if (more) npages = pages_of(np, nbase);
         f32x4 acc[VEC];
         float m, l;  // head r's running maximum (the same in its 4 lanes); the lane's own sum
         auto clear = [&]() {
@@ -293,22 +307,28 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
         clear();
         Half cur[2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) cur[s] = half_at(pt, pt.s0, s);
+        for (int s = 0; s < 2; ++s) cur[s] = half_at(pt, s0, s, __builtin_amdgcn_readlane(pages, s));
         qload(pt.b);
         kload(cur);
         vload(cur);
-        for (int i = pt.s0;;) {
-            // the next step, of this sequence or the next one, is loaded while this one is multiplied
-            const bool last = i + 1 >= pt.s1, more = left > 0 && pt.b + 1 < g.B;
-            Part np = pt;
-            int ni = i + 1;
-            if (last && more) {
-                np = part_of(pt.b + 1, 0);
-                ni = 0;
-            }
+        for (int i = s0;;) {
+            // the next step, of this block or the next one, is loaded while this one is multiplied (this one again
+            // after the last)
+            const bool last = i + 1 >= pt.s1, cross = last || i + 1 >= base + AHEAD, on = cross && more;
+            const Part qt = on ? np : pt;
+            const int ni = on ? nbase : cross ? i : i + 1;
             Half nxt[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) nxt[s] = half_at(np, ni, s);
+            for (int s = 0; s < 2; ++s) {
+                const int here = __builtin_amdgcn_readlane(pages, 2 * ((cross ? i : i + 1) - base) + s);
+                nxt[s] = half_at(qt, ni, s, on ? __builtin_amdgcn_readlane(npages, s) : here);
+            }
+            if (on) {
+                pages = npages;
+                base = nbase;
+                more = follow(qt, base, np, nbase);
+                if (more) npages = pages_of(np, nbase);
+            }
 
             f32x4 sc[2];
 #pragma unroll
@@ -331,11 +351,11 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
                 if constexpr (ROW) sc[s] *= ksv[s];
             }
             kload(nxt);
-            if (last && more) qload(np.b);
+            if (last && on) qload(qt.b);
 
             // scores in exponents of 2; tokens outside the span or in a bad page have none
-            const int tok = pt.begin + TILE * (NW * i + wave);
-            const bool edge = tok < pt.lo || tok + TILE > pt.len || !cur[0].good || !cur[1].good;
+            const int tok = begin_of(g, pt.len) + TILE * (NW * i + wave), lo = lo_of(g, pt.len);
+            const bool edge = tok < lo || tok + TILE > pt.len || !cur[0].good || !cur[1].good;
             float x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = sc[j / 4][j % 4] * g.qk_scale;
@@ -343,7 +363,7 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int k = tok + 16 * (j / 4) + 4 * q4 + j % 4;
-                    const bool live = k >= pt.lo && k < pt.len && cur[j / 4].good;
+                    const bool live = k >= lo && k < pt.len && cur[j / 4].good;
                     x[j] = live ? x[j] : -INFINITY;
                     // what lies there may be anything, and 0 * NaN is one
 #pragma unroll
@@ -412,15 +432,15 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
 #pragma unroll
             for (int s = 0; s < 2; ++s) cur[s] = nxt[s];
             if (!last) {
-                ++i;
+                i = ni;
                 continue;
             }
 
             // join the waves: lane l holds channels [4 VEC q4, +4 VEC) of head r
             constexpr int LD = DM + 4;
-            float* lm = lds;                // [NW][16]
-            float* ll = lds + NW * 16;      // [NW][16]
-            float* lo = lds + 2 * NW * 16;  // [NW][nh][LD]
+            float* lm = lds;                  // [NW][16]
+            float* ll = lds + NW * 16;        // [NW][16]
+            float* lacc = lds + 2 * NW * 16;  // [NW][nh][LD]
             l += __shfl_xor(l, 16, 64);
             l += __shfl_xor(l, 32, 64);
             __syncthreads();  // the sequence before is read
@@ -429,7 +449,7 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
                 ll[wave * 16 + r] = l;
             }
             if (r < nh) {
-                float* o = lo + (wave * nh + r) * LD + 4 * VEC * q4;
+                float* o = lacc + (wave * nh + r) * LD + 4 * VEC * q4;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -438,7 +458,8 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
                             f32x4{acc[e][k], acc[e + 1][k], acc[e + 2][k], acc[e + 3][k]};
             }
             __syncthreads();
-            const bool whole = pt.s1 - pt.s0 == pt.steps;
+            const int steps = steps_of(g, pt.len);
+            const bool whole = s0 == 0 && pt.s1 == steps;
             const int quads = D / 4;
             for (int id = threadIdx.x; id < nh * quads; id += NW * 64) {
                 const int hd = id / quads, c = 4 * (id - hd * quads);
@@ -450,7 +471,7 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
                 for (int w = 0; w < NW; ++w) {
                     const float f = __builtin_amdgcn_exp2f(lm[w * 16 + hd] - mx);
                     sum += f * ll[w * 16 + hd];
-                    o += f * *reinterpret_cast<const f32x4*>(lo + (w * nh + hd) * LD + c);
+                    o += f * *reinterpret_cast<const f32x4*>(lacc + (w * nh + hd) * LD + c);
                 }
                 const int64_t head = head0 + hd;
                 if (whole) {
@@ -461,7 +482,7 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
                     if (g.lse && c == 0)
                         g.lse[(int64_t)pt.b * g.heads + head] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * LN2;
                 } else {
-                    const int64_t slot = (int64_t)(2 * blockIdx.x + (pt.s0 == 0)) * g.heads + head;
+                    const int64_t slot = (int64_t)(2 * blockIdx.x + (s0 == 0)) * g.heads + head;
                     *reinterpret_cast<f32x4*>(g.part_o + slot * D + c) = o;
                     if (c == 0) {
                         g.part_ml[2 * slot] = mx;
@@ -469,16 +490,15 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
                     }
                 }
             }
-            if (!more) {
-                if (pt.s0 == 0 && !whole) {
-                    goes_on = 1 + (pt.steps - pt.s1 + cut - 1) / cut;
+            if (!on) {
+                if (s0 == 0 && !whole) {
+                    goes_on = 1 + (steps - pt.s1 + cut - 1) / cut;
                     begins = pt.b;
                 }
                 break;
             }
-            pt = np;
-            left -= pt.s1 - pt.s0;
-            i = 0;
+            pt = qt;
+            i = s0 = 0;
             clear();
         }
     }
