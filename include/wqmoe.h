@@ -540,7 +540,7 @@ wq_status dense_lora_gemm(const void* d_x, int64_t x_stride, int M, int K, int N
  *               values, or E4M3 codes (dtype WQ_E4M3)
  *   d_k_scales, d_v_scales  device float [pages, kv_heads, page_size], a scale
  *               for each row of codes; both NULL: k_scale and v_scale are those
- *               of every row (finite, > 0)
+ *               of every row (within 2^-100 and 2^100)
  * Limits: page_size a multiple of 16, at most 4096; head_dim a multiple of 16,
  * at most 256; pages * page_size < 2^31; kv_heads <= 65535.  A 16-bit cache is
  * of the call's act dtype.
@@ -559,10 +559,10 @@ typedef struct wq_kv_cache {
 /*
  * wq_kv_cache_write: token t's rows into slot d_slots[t] = page * page_size +
  * position; a slot outside [0, pages * page_size) (-1, a padding token) writes
- * nothing, and the rest of the cache stays as it was.  Codes as wq_rms_norm's:
- *   row scales  c = max(max|v| / 448, 2^-100), written; code of v * (1 / c)
- *   k_scale ..  code of v / k_scale (v / v_scale for the values)
- * clamped to +-448, ties to even; a NaN's code is one, the row scale skips it.
+ * nothing, and the rest of the cache stays as it was.  Codes of v / c in float32
+ * (of v * (1 / c) for c above 2^100), c the row's scale max(max|v| / 448, 2^-100), which is written, or k_scale (v_scale
+ * for the values); clamped to +-448, ties to even.  A NaN's code is one, the row
+ * scale skips it.
  * The slots of a call differ: of two tokens with one slot either's values may
  * be kept, not all of the same one.
  * wq_kv_cache_read: the rows of d_slots[t] back, code * scale rounded once to

@@ -17,7 +17,8 @@ def quantise(rows, quant, static=None):
     x = rows.float()
     if quant == "row":
         c = torch.clamp(torch.nan_to_num(x.abs(), nan=0.0, posinf=math.inf).amax(-1) / F8_MAX, min=2.0 ** -100)
-        y = x * (1.0 / c)[..., None]
+        c1 = c[..., None]
+        y = torch.where(c1 > 2.0 ** 100, x * (1.0 / c1), x / c1)
     else:
         c, y = None, x / torch.tensor(static, dtype=torch.float32)
     y = torch.where(y > F8_MAX, F8_MAX, torch.where(y < -F8_MAX, -F8_MAX, y))

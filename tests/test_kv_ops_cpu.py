@@ -59,7 +59,9 @@ CALLS = [lambda c: rows(True, c), lambda c: rows(False, c), attend]
     (dict(d_v_scales=None), INV), (dict(d_v_scales=FAKE + 3 * GB + 4), INV), (dict(dtype=wq.WQ_BF16), INV),
     (dict(d_k_scales=None, d_v_scales=None), INV),
     (dict(d_k_scales=None, d_v_scales=None, k_scale=1.0, v_scale=float("nan")), INV),
-    (dict(d_k_scales=None, d_v_scales=None, k_scale=-1.0, v_scale=1.0), INV)])
+    (dict(d_k_scales=None, d_v_scales=None, k_scale=-1.0, v_scale=1.0), INV),
+    (dict(d_k_scales=None, d_v_scales=None, k_scale=1e-31, v_scale=1.0), INV),
+    (dict(d_k_scales=None, d_v_scales=None, k_scale=1.0, v_scale=float("inf")), INV)])
 def test_cache_refusals(change, want):
     for call in CALLS:
         st, msg = call(desc(**change))

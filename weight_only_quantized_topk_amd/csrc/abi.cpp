@@ -1241,9 +1241,9 @@ wq_status kv_cache_args(const wq_kv_cache* c, int act_dtype, KvCacheView* out, c
     WQ_REQUIRE(e4m3 || (!c->d_k_scales && !c->d_v_scales), WQ_ERR_INVALID, "%s: scales of a 16-bit cache", who);
     WQ_REQUIRE(!rows || (c->d_k_scales && c->d_v_scales), WQ_ERR_INVALID,
                "%s: row scales for the keys and the values, or for neither", who);
-    WQ_REQUIRE(!e4m3 || rows || (std::isfinite(c->k_scale) && c->k_scale > 0.0f && std::isfinite(c->v_scale) &&
-                                 c->v_scale > 0.0f),
-               WQ_ERR_INVALID, "%s: k_scale and v_scale must be finite and > 0", who);
+    auto usable = [](float s) { return s >= 0x1p-100f && s <= 0x1p100f; };
+    WQ_REQUIRE(!e4m3 || rows || (usable(c->k_scale) && usable(c->v_scale)), WQ_ERR_INVALID,
+               "%s: k_scale and v_scale must be within 2^-100 and 2^100", who);
     const int64_t n = (int64_t)c->pages * c->page_size * c->kv_heads;  // rows: < 2^47
     const int64_t bytes = n * c->head_dim * (e4m3 ? 1 : 2);
     out->mode = !e4m3 ? wq::KV_16 : rows ? wq::KV_E4M3_ROW : wq::KV_E4M3_STATIC;

@@ -5,13 +5,19 @@
 // the rows of one head in a page lie next to each other, so attention reads a
 // page of a head as one piece.  A row (one token, one head) is 16-bit, or E4M3
 // codes with a scale of its own or one for all:
-//   row scale:  c = max(max|v| / 448, 2^-100), code = E4M3(v * (1 / c))
-//   static scale c given:                      code = E4M3(v / c)
+//   row scale:  c = max(max|v| / 448, 2^-100), written;  code = E4M3(v / c)
+//   static scale c given:                                code = E4M3(v / c)
 //   back:       v = code * c in float32, rounded once
-// (the codes and scales of rms_norm.hip).  Both kernels give a row LPR lanes of
-// 8 values each, keys and values by the same thread; a workgroup takes
-// consecutive tokens of one head, whose rows and scales are neighbours in the
-// cache where a prompt fills its pages.
+// v / c is the float32 quotient: one reciprocal a row, then a product and one
+// residual step, which gives the correctly rounded quotient where nothing over- or
+// underflows (10 instructions a value less than a division; static scales
+// 13.0 -> 12.1 us at the size below).  Both kernels give a row LPR lanes of 8
+// values each, keys and values by the same thread; a workgroup takes consecutive
+// tokens of one head, whose rows and scales are neighbours in the cache where a prompt
+// fills its pages.
+// HBM bound: 8192 tokens of 8 heads of 128, bf16 to codes and scales (51 MB) 12.0
+// us with a launch's 3 in it, 32768 back (204 MB) 31.5 us.  More tokens a thread
+// were slower (2: 12.8, 4: 15.0 us), as were non-temporal reads of the new rows (13.6).
 #include "common.hpp"
 #include "kv_common.hpp"
 #include "launch.hpp"
@@ -30,14 +36,30 @@ __device__ __forceinline__ float clamp_e4m3(float v) {
     return v < -E4M3_MAX ? -E4M3_MAX : v;
 }
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(a), clamp_e4m3(b), 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(c), clamp_e4m3(d), w, true);
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
 template <bool BF16>
 __device__ __forceinline__ void widen(u32x4 d, float (&v)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = act_to_f32<BF16>((uint16_t)(d[j >> 1] >> (16 * (j & 1))));
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_max(float v) {
+    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, 0xF, 0xF,
+                                                               false)));
+}
+// over the LPR lanes of a row, in each of them: within 16 lanes by DPP
+template <int LPR>
+__device__ __forceinline__ float row_max(float v) {
+    v = dpp_max<0xB1>(v);   // quad_perm [1,0,3,2]
+    v = dpp_max<0x4E>(v);   // quad_perm [2,3,0,1]
+    v = dpp_max<0x141>(v);  // row_half_mirror
+    if constexpr (LPR > 8) v = dpp_max<0x140>(v);  // row_mirror
+    if constexpr (LPR > 16) v = fmaxf(v, __shfl_xor(v, 16, 64));
+    return v;
 }
 
 // one row's 8 values in this lane (zeros in lanes past the row) into the cache
@@ -47,26 +69,38 @@ __device__ __forceinline__ void put(u32x4 d, bool active, int64_t row, int D, in
     if constexpr (MODE == KV_16) {
         if (active) *reinterpret_cast<u32x4*>(cache + (row * D + at) * 2) = d;
     } else {
-        float v[8];
+        float v[8], c = static_scale;
         widen<BF16>(d, v);
         if constexpr (MODE == KV_E4M3_ROW) {
             float top = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-            const float c = fmaxf(top / E4M3_MAX, MIN_ROW_SCALE);
-            const float inv = 1.0f / c;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= inv;
+            top = row_max<LPR>(top);
+            c = fmaxf(top / E4M3_MAX, MIN_ROW_SCALE);
             if (active && at == 0) scales[row] = c;
+        }
+        const float inv = 1.0f / c;
+        u32x2 code;
+        if constexpr (MODE == KV_E4M3_ROW) {
+            // a bf16 row of the largest values, or an infinity: the product alone, whose residual may not be finite
+            const float cr = c > 0x1p100f ? 0.0f : c, ir = c > 0x1p100f ? 0.0f : inv;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float q = v[j] * inv;
+                v[j] = fmaf(fmaf(-q, cr, v[j]), ir, q);
+            }
+            // (at most 448 and a step, which the conversion rounds to 448)
+            code = u32x2{codes4(v[0], v[1], v[2], v[3]), codes4(v[4], v[5], v[6], v[7])};
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = v[j] / static_scale;
+            for (int j = 0; j < 8; ++j) {  // past the codes' range (the residual may be infinite): the product
+                const float q = v[j] * inv;
+                v[j] = fabsf(q) > 480.0f ? q : fmaf(fmaf(-q, c, v[j]), inv, q);
+            }
+            code = u32x2{codes4(clamp_e4m3(v[0]), clamp_e4m3(v[1]), clamp_e4m3(v[2]), clamp_e4m3(v[3])),
+                         codes4(clamp_e4m3(v[4]), clamp_e4m3(v[5]), clamp_e4m3(v[6]), clamp_e4m3(v[7]))};
         }
-        if (active)
-            *reinterpret_cast<u32x2*>(cache + row * D + at) =
-                u32x2{codes4(v[0], v[1], v[2], v[3]), codes4(v[4], v[5], v[6], v[7])};
+        if (active) *reinterpret_cast<u32x2*>(cache + row * D + at) = code;
     }
 }
 
@@ -76,16 +110,16 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvRowsArgs g) {
     const int64_t t = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
     const int h = blockIdx.y;
     if (t >= g.T) return;  // (whole rows: the lanes of a row's maximum leave together)
-    const int64_t slot = g.slots[t];
-    if (slot < 0 || slot >= (int64_t)g.pages * g.page_size) return;
-    const uint32_t page = (uint32_t)slot / (uint32_t)g.page_size, off = (uint32_t)slot - page * g.page_size;
-    const int64_t row = ((int64_t)page * g.kv_heads + h) * g.page_size + off;
     const bool active = at < g.D;
+    const int64_t slot = g.slots[t];
     u32x4 k = {0, 0, 0, 0}, v = {0, 0, 0, 0};
     if (active) {
         k = ldg128(g.k16 + t * g.k_stride + (int64_t)h * g.D + at);
         v = ldg128(g.v16 + t * g.v_stride + (int64_t)h * g.D + at);
     }
+    if (slot < 0 || slot >= (int64_t)g.pages * g.page_size) return;
+    const uint32_t page = (uint32_t)slot / (uint32_t)g.page_size, off = (uint32_t)slot - page * g.page_size;
+    const int64_t row = ((int64_t)page * g.kv_heads + h) * g.page_size + off;
     put<BF16, MODE, LPR>(k, active, row, g.D, at, g.k, g.ks, g.k_scale);
     put<BF16, MODE, LPR>(v, active, row, g.D, at, g.v, g.vs, g.v_scale);
 }
@@ -110,7 +144,8 @@ __device__ __forceinline__ u32x4 get(const uint8_t* cache, const float* scales, 
     }
 }
 
-template <bool BF16, int MODE, int LPR>
+// NT: non-temporal stores
+template <bool BF16, int MODE, int LPR, bool NT>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvRowsArgs g) {
     const int lane = threadIdx.x % LPR, at = 8 * lane;
     const int64_t t = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
@@ -124,15 +159,29 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvRowsArgs g) {
         k = get<BF16, MODE>(g.k, g.ks, g.k_scale, row, g.D, at);
         v = get<BF16, MODE>(g.v, g.vs, g.v_scale, row, g.D, at);
     }
-    *reinterpret_cast<u32x4*>(g.k16 + t * g.k_stride + (int64_t)h * g.D + at) = k;
-    *reinterpret_cast<u32x4*>(g.v16 + t * g.v_stride + (int64_t)h * g.D + at) = v;
+    u32x4* ko = reinterpret_cast<u32x4*>(g.k16 + t * g.k_stride + (int64_t)h * g.D + at);
+    u32x4* vo = reinterpret_cast<u32x4*>(g.v16 + t * g.v_stride + (int64_t)h * g.D + at);
+    if constexpr (NT) {
+        __builtin_nontemporal_store(k, ko);
+        __builtin_nontemporal_store(v, vo);
+    } else {
+        *ko = k;
+        *vo = v;
+    }
 }
 
+// Rows read from codes and more than the L2s hold (8 x 4 MB) are stored past them: 134
+// MB 43 -> 31.5 us, 34 MB 10.9 -> 10.0 us.  Not copies of 16-bit rows (2 x 134 MB into
+// memory that the last-level cache holds: 48 -> 55 us)
 template <bool BF16, int MODE, int LPR>
 void launch_lpr(const KvRowsArgs& g, bool write, hipStream_t s) {
     const dim3 grid((unsigned)(((int64_t)g.T + 256 / LPR - 1) / (256 / LPR)), g.kv_heads);
-    if (write) hipLaunchKernelGGL((kv_write_kernel<BF16, MODE, LPR>), grid, dim3(256), 0, s, g);
-    else hipLaunchKernelGGL((kv_read_kernel<BF16, MODE, LPR>), grid, dim3(256), 0, s, g);
+    if (write)
+        hipLaunchKernelGGL((kv_write_kernel<BF16, MODE, LPR>), grid, dim3(256), 0, s, g);
+    else if (MODE != KV_16 && (int64_t)g.T * g.kv_heads * g.D * 4 >= (32 << 20))
+        hipLaunchKernelGGL((kv_read_kernel<BF16, MODE, LPR, MODE != KV_16>), grid, dim3(256), 0, s, g);
+    else
+        hipLaunchKernelGGL((kv_read_kernel<BF16, MODE, LPR, false>), grid, dim3(256), 0, s, g);
 }
 
 template <bool BF16, int MODE>
