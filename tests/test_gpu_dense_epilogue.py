@@ -130,6 +130,18 @@ def test_long_sums(kind, M, N, K):
     check(bits, group, act, M, N, K, True, None, "in place")
 
 
+@pytest.mark.parametrize("kind", ["w4", "w8b"])
+@pytest.mark.parametrize("M,N,K", [(129, 1040, 128), (200, 32992, 128), (300, 32992, 128), (520, 32992, 256), (1000, 16400, 1024),
+                                   (129, 1040, 8192), (129, 8208, 4096), (200, 8208, 2048), (1000, 1040, 4096), (129, 2064, 1024),
+                                   (1000, 528, 1024), (4096, 144, 1024), (16, 20480, 256), (32, 20480, 256), (100, 20480, 256),
+                                   (7, 20480, 256)])
+def test_plans(kind, M, N, K):
+    """Every tile shape, split of K and cut by columns of the dispatch, ends of rows and columns within them."""
+    bits, group, act, ao = KINDS[kind]
+    check(bits, group, act, M, N, K, True, "relu", "in place" if M % 2 else "strided")
+    _weights.clear()
+
+
 def test_values_that_overflow():
     """A sum beyond the type's range, an infinite bias, a NaN in one row of x: each in its own outputs."""
     need_gpu()
