@@ -51,6 +51,10 @@ constexpr int TILE = 32;           // tokens of a wave's step
 // head_dim rounded up, and the waves a SIMD (workgroups a CU) that its registers leave room for
 constexpr int dim_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 constexpr int waves_of(int DM) { return DM == 256 ? 2 : DM == 128 ? 3 : 4; }
+template <int MODE, int DM>
+constexpr bool q_in_lds = MODE == KV_16 && DM == 256;
+template <int MODE, int DM>
+constexpr int join_channels = q_in_lds<MODE, DM> ? 128 : DM;  // (leaves Q room for two workgroups a CU)
 constexpr float M_NONE = -3.4028234e38f;  // the running maximum before any score
 constexpr float M_SLACK = 8.0f;    // scores may pass it by this much (exponents of 2)
 constexpr float LN2 = 0.693147180559945309f;
@@ -181,6 +185,8 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
     constexpr int KL = DM / KD;                   // such loads a token row
     constexpr int VEC = DM / 16;                  // V channels of a lane
     constexpr int VD = VEC * ELT / 4;             // their dwords
+    constexpr int JC = join_channels<MODE, DM>;   // channels that the waves join at a time
+    constexpr int LD = JC + 4;
     extern __shared__ __attribute__((aligned(16))) float lds[];
 
     const int D = FULL ? DM : g.D;
@@ -278,15 +284,26 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
             h.rows = ((int64_t)(h.good ? page : 0) * g.kv_heads + kvh) * g.page_size + (u - col * page16) * KV_TOKENS;
             return h;
         };
-        // Q, the B operand of every K step: head r, the channels in K's order
-        u32x4 qv[DM / 32];
+        // Q, the B operand of every K step: head r, the channels in K's order; in registers, or where there are
+        // too few of them (16-bit rows at DM 256, 104 bytes a lane spilled) in LDS, each lane its own: 64 sequences
+        // of up to 8192 tokens, 8 heads of 256: 408 against 516 us.  E4M3 rows leave room: 38 against 42 us
+        // (16 x up to 4096)
+        constexpr bool QLDS = q_in_lds<MODE, DM>;
+        u32x4 qv[QLDS ? 1 : DM / 32];
+        u32x4* qs = reinterpret_cast<u32x4*>(lds + 2 * NW * 16 + NW * nh * LD) + wave * (DM / 32) * 64 + lane;
         auto qload = [&](int b) {
 #pragma unroll
             for (int c = 0; c < DM / 32; ++c) {
                 const int ch = F8 ? 64 * (c / 2) + 16 * q4 + 8 * (c % 2) : 32 * c + 8 * q4;
-                qv[c] = u32x4{0, 0, 0, 0};
-                if (r < nh && ch < D) qv[c] = ldg128(g.q + (int64_t)b * g.q_stride + (int64_t)(head0 + r) * D + ch);
+                u32x4 v = {0, 0, 0, 0};
+                if (r < nh && ch < D) v = ldg128(g.q + (int64_t)b * g.q_stride + (int64_t)(head0 + r) * D + ch);
+                if constexpr (QLDS) qs[64 * c] = v;
+                else qv[c] = v;
             }
+        };
+        auto q_at = [&](int c) {
+            if constexpr (QLDS) return qs[64 * c];
+            else return qv[c];
         };
 
         int s0 = __builtin_amdgcn_readfirstlane(share.off);  // the sequence's first step in the share
@@ -342,10 +359,10 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
                             const uint32_t w0 = kv[s][c][2 * half], w1 = kv[s][c][2 * half + 1];
                             const u32x4 a = {codes2<BF16>(w0, false), codes2<BF16>(w0, true), codes2<BF16>(w1, false),
                                              codes2<BF16>(w1, true)};
-                            sc[s] = mfma16x16x32<BF16>(a, qv[2 * c + half], sc[s]);
+                            sc[s] = mfma16x16x32<BF16>(a, q_at(2 * c + half), sc[s]);
                         }
                     } else {
-                        sc[s] = mfma16x16x32<BF16>(kv[s][c], qv[c], sc[s]);
+                        sc[s] = mfma16x16x32<BF16>(kv[s][c], q_at(c), sc[s]);
                     }
                 }
                 if constexpr (ROW) sc[s] *= ksv[s];
@@ -437,56 +454,59 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
             }
 
             // join the waves: lane l holds channels [4 VEC q4, +4 VEC) of head r
-            constexpr int LD = DM + 4;
             float* lm = lds;                  // [NW][16]
             float* ll = lds + NW * 16;        // [NW][16]
             float* lacc = lds + 2 * NW * 16;  // [NW][nh][LD]
             l += __shfl_xor(l, 16, 64);
             l += __shfl_xor(l, 32, 64);
-            __syncthreads();  // the sequence before is read
-            if (q4 == 0) {
-                lm[wave * 16 + r] = m;
-                ll[wave * 16 + r] = l;
-            }
-            if (r < nh) {
-                float* o = lacc + (wave * nh + r) * LD + 4 * VEC * q4;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int e = 0; e < VEC; e += 4)
-                        *reinterpret_cast<f32x4*>(o + VEC * k + e) =
-                            f32x4{acc[e][k], acc[e + 1][k], acc[e + 2][k], acc[e + 3][k]};
-            }
-            __syncthreads();
             const int steps = steps_of(g, pt.len);
             const bool whole = s0 == 0 && pt.s1 == steps;
-            const int quads = D / 4;
-            for (int id = threadIdx.x; id < nh * quads; id += NW * 64) {
-                const int hd = id / quads, c = 4 * (id - hd * quads);
-                float mx = lm[hd], sum = 0.0f;
 #pragma unroll
-                for (int w = 1; w < NW; ++w) mx = fmaxf(mx, lm[w * 16 + hd]);
-                f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    const float f = __builtin_amdgcn_exp2f(lm[w * 16 + hd] - mx);
-                    sum += f * ll[w * 16 + hd];
-                    o += f * *reinterpret_cast<const f32x4*>(lacc + (w * nh + hd) * LD + c);
+            for (int jc = 0; jc < DM; jc += JC) {
+                __syncthreads();  // what was there is read
+                if (jc == 0 && q4 == 0) {
+                    lm[wave * 16 + r] = m;
+                    ll[wave * 16 + r] = l;
                 }
-                const int64_t head = head0 + hd;
-                if (whole) {
-                    // no token with a weight: zeros, and -inf
-                    const float inv = sum == 0.0f ? 0.0f : g.v_scale / sum;
-                    *reinterpret_cast<u32x2*>(g.out + (int64_t)pt.b * g.out_stride + head * D + c) =
-                        u32x2{f32_to_act2<BF16>(o[0] * inv, o[1] * inv), f32_to_act2<BF16>(o[2] * inv, o[3] * inv)};
-                    if (g.lse && c == 0)
-                        g.lse[(int64_t)pt.b * g.heads + head] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * LN2;
-                } else {
-                    const int64_t slot = (int64_t)(2 * blockIdx.x + (s0 == 0)) * g.heads + head;
-                    *reinterpret_cast<f32x4*>(g.part_o + slot * D + c) = o;
-                    if (c == 0) {
-                        g.part_ml[2 * slot] = mx;
-                        g.part_ml[2 * slot + 1] = sum;
+                if (r < nh && (JC == DM || 4 * VEC * q4 / JC == jc / JC)) {
+                    float* o = lacc + (wave * nh + r) * LD + 4 * VEC * q4 - jc;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int e = 0; e < VEC; e += 4)
+                            *reinterpret_cast<f32x4*>(o + VEC * k + e) =
+                                f32x4{acc[e][k], acc[e + 1][k], acc[e + 2][k], acc[e + 3][k]};
+                }
+                __syncthreads();
+                const int quads = min(D - jc, JC) / 4;
+                for (int id = threadIdx.x; id < nh * quads; id += NW * 64) {
+                    const int hd = id / quads, c = 4 * (id - hd * quads);
+                    float mx = lm[hd], sum = 0.0f;
+#pragma unroll
+                    for (int w = 1; w < NW; ++w) mx = fmaxf(mx, lm[w * 16 + hd]);
+                    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) {
+                        const float f = __builtin_amdgcn_exp2f(lm[w * 16 + hd] - mx);
+                        sum += f * ll[w * 16 + hd];
+                        o += f * *reinterpret_cast<const f32x4*>(lacc + (w * nh + hd) * LD + c);
+                    }
+                    const int64_t head = head0 + hd;
+                    const bool first = jc == 0 && c == 0;
+                    if (whole) {
+                        // no token with a weight: zeros, and -inf
+                        const float inv = sum == 0.0f ? 0.0f : g.v_scale / sum;
+                        *reinterpret_cast<u32x2*>(g.out + (int64_t)pt.b * g.out_stride + head * D + jc + c) =
+                            u32x2{f32_to_act2<BF16>(o[0] * inv, o[1] * inv), f32_to_act2<BF16>(o[2] * inv, o[3] * inv)};
+                        if (g.lse && first)
+                            g.lse[(int64_t)pt.b * g.heads + head] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * LN2;
+                    } else {
+                        const int64_t slot = (int64_t)(2 * blockIdx.x + (s0 == 0)) * g.heads + head;
+                        *reinterpret_cast<f32x4*>(g.part_o + slot * D + jc + c) = o;
+                        if (first) {
+                            g.part_ml[2 * slot] = mx;
+                            g.part_ml[2 * slot + 1] = sum;
+                        }
                     }
                 }
             }
@@ -593,7 +613,8 @@ template <bool BF16, int MODE, int DM, bool FULL, bool NT>
 void launch_kernel(const PagedAttnArgs& g, hipStream_t s) {
     const int group = g.heads / g.kv_heads;
     const int nh = std::min(group, 16);
-    const size_t lds = (2 * NW * 16 + (size_t)NW * nh * (DM + 4)) * sizeof(float);
+    const size_t lds = (2 * NW * 16 + (size_t)NW * nh * (join_channels<MODE, DM> + 4)) * sizeof(float) +
+                       (q_in_lds<MODE, DM> ? NW * (DM / 32) * 64 * 16 : 0);  // what is joined, and Q
     auto kern = paged_attention_kernel<BF16, MODE, DM, FULL, NT>;
     if (lds > 65536)
         (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
