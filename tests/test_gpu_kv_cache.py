@@ -154,3 +154,27 @@ def test_the_same_slot_read_twice_and_graph_and_stream():
         torch.cuda.synchronize()
         same(cache, host)
         assert all(torch.equal(a, b) for a, b in zip(got, wq.kv_cache_read(cache, to, torch.float16)))
+
+
+@pytest.mark.parametrize("quant", [None, "row", "static"])
+def test_two_tokens_with_one_slot(quant):
+    """Of the two either's values are kept, and the other rows are their own."""
+    need_gpu()
+    x = torch.randn((40, 3, 80), generator=torch.Generator().manual_seed(5)).half()
+    slots = torch.arange(40)
+    slots[31] = 2
+    cache, host = make("f16", quant, 4, 3, 16, 80)
+    wq.kv_cache_write(x.cuda(), -x.cuda(), cache, slots.cuda())
+    one, _ = make("f16", quant, 4, 3, 16, 80)
+    rest = slots.clone()
+    rest[31] = -1
+    wq.kv_cache_write(x.cuda(), -x.cuda(), one, rest.cuda())
+    other, _ = make("f16", quant, 4, 3, 16, 80)
+    rest[2], rest[31] = -1, 2
+    wq.kv_cache_write(x.cuda(), -x.cuda(), other, rest.cuda())
+    for a, b, c in zip(cache, one, other):
+        if isinstance(a, torch.Tensor):
+            eq_b, eq_c = bits(a) == bits(b), bits(a) == bits(c)
+            assert bool((eq_b | eq_c).all())
+            eq_b[0, :, 2] = True
+            assert bool(eq_b.all())

@@ -265,3 +265,42 @@ def test_no_sequences():
                                   torch.empty((0, 4), dtype=torch.int32, device="cuda"),
                                   torch.empty(0, dtype=torch.int32, device="cuda"), want_lse=True)
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+@pytest.mark.parametrize("quant", [None, "row"])
+def test_shares_of_more_steps_than_a_block_of_pages(quant):
+    """Many heads and long sequences: a workgroup's share goes on past the 32 steps whose pages it has fetched at once,
+    within a sequence and from one to the next."""
+    check("f16", quant, 256, 1, 32, 16, [9001, 260, 8400, 0, 70])
+
+
+def test_pages_before_the_window_may_be_gone():
+    need_gpu()
+    for P, window, n in ((16, 100, 1000), (48, 17, 650), (64, 640, 700)):
+        query, cache, host, table = make("bf16", "row", 2, P, 128, [n, n - 3])
+        q, qd = query(4)
+        lengths = torch.tensor([n, n - 3], dtype=torch.int32).cuda()
+        want = wq.paged_attention(qd, cache, table.cuda(), lengths, window=window, want_lse=True)
+        for b, length in enumerate((n, n - 3)):
+            table[b, :(length - window) // P] = torch.tensor([-1, 1 << 30])[b]
+        got = wq.paged_attention(qd, cache, table.cuda(), lengths, window=window, want_lse=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("quant", [None, "static"])
+def test_the_largest_workgroup_in_a_graph(quant):
+    """16 heads of 256 a workgroup: more than 64 KB of LDS, asked for by a captured call as by any other."""
+    need_gpu()
+    query, cache, host, table = make("bf16", quant, 2, 32, 256, [700, 1, 90])
+    q, qd = query(32)
+    qd, table = qd.contiguous(), table.cuda()
+    lengths = torch.tensor([700, 1, 90], dtype=torch.int32).cuda()
+    wq.paged_attention(qd, cache, table, lengths)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = wq.paged_attention(qd, cache, table, lengths)
+    for k in range(3):
+        qd.copy_(torch.roll(qd, 1, 1))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held, wq.paged_attention(qd, cache, table, lengths))

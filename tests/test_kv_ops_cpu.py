@@ -116,6 +116,11 @@ def test_attention_refusals(change, want):
     assert st == want, (change, msg)
 
 
+def test_scales_whose_product_is_not_finite():
+    fixed = desc(k_scale=2.0 ** 100, v_scale=1.0, d_k_scales=None, d_v_scales=None)
+    assert attend(fixed, scale=3e38)[0] == INV and attend(fixed, scale=1.0)[0] in NO_DEVICE
+
+
 def test_attention_allowed():
     for change in (dict(lse=None), dict(out=at(4 * GB + 8192), os=8192, qs=8192), dict(width=1, ws=None, nb=0)):
         st, msg = attend(**change)
@@ -169,6 +174,7 @@ def test_write_and_read_binding_refusals():
     refused(lambda: w(k=x.float()), TypeError, ValueError)
     refused(lambda: w(v=x.half()), TypeError)
     refused(lambda: w(k=torch.zeros((3, 2, 16), dtype=BFT)))
+    refused(lambda: w(k=torch.zeros((), dtype=BFT)))
     refused(lambda: w(k=torch.zeros((3, 3, 32), dtype=BFT)))
     refused(lambda: w(v=torch.zeros((4, 2, 32), dtype=BFT)))
     refused(lambda: w(k=torch.zeros((3, 2, 64), dtype=BFT)[:, :, ::2]))
@@ -245,9 +251,9 @@ def test_dense_workspace_and_forms():
     f = wq.dense_epilogue_workspace_bytes
     assert f(8, 64, 4096, 4096) == 0 and f(8, 0, 4096, 4096) == 0 and f(8, 64, 100, 64) == 0
     assert f(4, 5, 256, 64, True) > 0
-    many = f(8, 200, 4096, 128)
+    many = f(8, 129, 8192, 1040)
     assert many > 0  # K is split there
-    big = dict(M=200, K=4096, N=128, rs=128)
+    big = dict(M=129, K=8192, N=1040, rs=1040)
     assert dense(8, nb=many - 1, **big)[0] == INV
     for change in (dict(ws=None), dict(ws=at(8 * GB + 16)), dict(ws=at(3 * GB)), dict(ws=at(5 * GB)), dict(ws=at(GB))):
         assert dense(8, **{**big, **change})[0] == INV, change

@@ -1398,7 +1398,9 @@ wq_status wq_paged_attention(const wq_kv_cache* c, const void* d_q, int64_t q_st
         WQ_REQUIRE(!bad, WQ_ERR_INVALID, "%s: %s", who, bad);
         bad = attn_limits(B, heads, c->kv_heads, c->page_size, table_width);
         WQ_REQUIRE(!bad, WQ_ERR_UNSUPPORTED, "%s: %s", who, bad);
-        WQ_REQUIRE(std::isfinite(scale), WQ_ERR_INVALID, "%s: scale must be finite", who);
+        const bool fixed = view.mode == wq::KV_E4M3_STATIC;
+        const float qk_scale = (float)((double)scale * (fixed ? (double)c->k_scale : 1.0) * 1.4426950408889634);
+        WQ_REQUIRE(std::isfinite(qk_scale), WQ_ERR_INVALID, "%s: scale (times k_scale) must be finite", who);
         const AttnLayout L =
             attn_layout(B, heads, c->kv_heads, c->head_dim, c->page_size, table_width, window);
         if (B == 0) return ok();  // (empty arrays may have no address)
@@ -1439,7 +1441,6 @@ wq_status wq_paged_attention(const wq_kv_cache* c, const void* d_q, int64_t q_st
         for (const Span8& a : in) WQ_TRY(check_dev(a.p, a.name, cur));
         for (const Span8& a : out)
             if (a.p) WQ_TRY(check_dev(a.p, a.name, cur));
-        const bool fixed = view.mode == wq::KV_E4M3_STATIC;
         uint8_t* ws = static_cast<uint8_t*>(d_workspace);
         wq::PagedAttnArgs g{};
         g.k = static_cast<const uint8_t*>(c->d_k);
@@ -1458,7 +1459,7 @@ wq_status wq_paged_attention(const wq_kv_cache* c, const void* d_q, int64_t q_st
         }
         g.q_stride = q_stride;
         g.out_stride = out_stride;
-        g.qk_scale = (float)((double)scale * (fixed ? (double)c->k_scale : 1.0) * 1.4426950408889634);
+        g.qk_scale = qk_scale;
         g.v_scale = fixed ? c->v_scale : 1.0f;
         g.B = B;
         g.heads = heads;

@@ -10,14 +10,13 @@
 //   back:       v = code * c in float32, rounded once
 // v / c is the float32 quotient: one reciprocal a row, then a product and one
 // residual step, which gives the correctly rounded quotient where nothing over- or
-// underflows (10 instructions a value less than a division; static scales
-// 13.0 -> 12.1 us at the size below).  Both kernels give a row LPR lanes of 8
+// underflows (10 instructions a value less than a division: 0.9 us at the size below).  Both kernels give a row LPR lanes of 8
 // values each, keys and values by the same thread; a workgroup takes consecutive
 // tokens of one head, whose rows and scales are neighbours in the cache where a prompt
 // fills its pages.
-// HBM bound: 8192 tokens of 8 heads of 128, bf16 to codes and scales (51 MB) 12.0
+// HBM bound: 8192 tokens of 8 heads of 128, bf16 to codes and scales (51 MB) 11.1
 // us with a launch's 3 in it, 32768 back (204 MB) 31.5 us.  More tokens a thread
-// were slower (2: 12.8, 4: 15.0 us), as were non-temporal reads of the new rows (13.6).
+// were slower (by 0.8 and 3 us for 2 and 4), as were non-temporal reads of the new rows (by 1.6).
 #include "common.hpp"
 #include "kv_common.hpp"
 #include "launch.hpp"

@@ -30,12 +30,26 @@
 // seldom rescaled.
 //
 // Split over the length: every workgroup reads the batch's lengths and finds
-// from them alone the same cut: the batch's tiles over the grid's pieces, at least
-// min_tiles a piece, equal pieces within a sequence, so one long sequence among short ones is
-// shared out.  The first pieces of all sequences are numbered in order; a
-// sequence in one piece is written at once, the pieces of others as (O, max, sum) in float32 to the
-// workspace, joined in ascending order by a second kernel.  No atomics: the same inputs
-// and grid give the same bits.
+// from them alone the same cut: the sequences' steps (a tile for each of 4 waves, 128
+// tokens; a sequence of none has one step) one after another in as many equal shares as the
+// chip holds workgroups (256 CUs x 4, 3 or 2 by the registers that head_dim takes),
+// so one long sequence among short ones is shared out and no workgroup waits for another.
+// A workgroup goes through its share without a pause between sequences: the rows of the next step are
+// asked for as the registers of this one come free, and the pages of 32 steps
+// by one vector load a block ahead.  (Pages read singly by scalar loads cost 3 to
+// 5 % more; a whole tile more in flight does not fit in the registers.)  A sequence that lies in one share is written at
+// once; the pieces of the others, at most two a share, go as (O, max, sum) in
+// float32 to the workspace and are joined in ascending order by a second
+// kernel.  No atomics: the same inputs and grid give the same bits.  Caches
+// of few tokens a sequence, and batches that fill the chip with short sequences, have a workgroup a
+// sequence and no second kernel (the rule is at paged_attn_splits).
+//
+// Measured (device time in a graph; a large copy reaches 5.2 TB/s here): one
+// sequence of 131072 tokens, 32 heads over 8 of 128 in bf16 (537 MB) 98 to 100 us;
+// 61 sequences of up to 8192 tokens, E4M3 rows (536 MB) 104 us; 256 of up to 1024,
+// 16 heads of 64 (538 MB) 107 us: 5.0 to 5.4 TB/s, the rate of reading.  Short
+// ones are bound by two launches, the walk over lengths and tables and the join:
+// 9 us for one sequence of 1024 tokens (4 MB), of these 4 to 5 the second kernel.
 #include "common.hpp"
 #include "kv_common.hpp"
 #include "launch.hpp"

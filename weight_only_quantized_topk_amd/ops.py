@@ -824,6 +824,8 @@ def kv_cache_write(k, v, cache: KVCache, slots, stream=None) -> KVCache:
     dt, dev = k.dtype, k.device
     act = act_code(dt)
     d = _kv_desc(cache, dt, dev)
+    if k.dim() != 3:
+        raise ValueError("k must be [T, kv_heads, head_dim], got %s" % list(k.shape))
     T, H, D = k.shape[0], d.kv_heads, d.head_dim
     _int32(T=T)
     ks, vs = _head_rows(k, "k", T, H, D, dt, dev), _head_rows(v, "v", T, H, D, dt, dev)
