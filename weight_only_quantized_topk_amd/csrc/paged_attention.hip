@@ -678,14 +678,24 @@ void launch_type(const PagedAttnArgs& g, hipStream_t s) {
 }  // namespace
 
 // Shares: as many as are resident at once on 256 CUs, none smaller than a tile a
-// wave.  A workgroup a sequence, and no second kernel, where they are
-// short and enough to fill the GPU (16 heads of 64, 256 sequences of up to 1024: 106
-// against 121 us in shares), or shorter than two steps of a workgroup.
+// wave.  A workgroup a sequence and no second kernel where none is long (a step
+// takes it 0.6, 1.1 or 2.7 us at DM 64, 128, 256, the join and its launch 4 to 8): device time, split against
+// not, 8 heads of 64 / 128 / 256 in bf16,
+//   up to 500 tokens, 1 sequence        8.0 /  6.5    8.9 /  8.6   14.4 / 17.4 us
+//                    32 sequences      14.8 /  7.3   17.3 / 10.9   30.7 / 22.4
+//   up to 1009 tokens, 1 sequence       8.1 /  9.0    9.0 / 12.9   15.9 / 25.9
+//                      8 sequences     11.8 /  9.4   15.1 / 13.5   24.5 / 27.4
+//                     16 sequences     16.0 /  9.3   17.2 / 13.9   32.9 / 28.0
+//                     64 sequences     21.8 / 17.3   36.3 / 35.5   76.5 / 77.0
+//   up to 2000 tokens, 1 sequence       9.6 / 14.2   11.7 / 21.5   17.0 / 45.2
+//                     64 sequences     36.8 / 36.0   59.8 / 64.4    135 / 136
+// (8 waves a workgroup there: 64 or 128 KB a step keep a CU busy as it is, 17.2 -> 18.9 us at 32 sequences of 1009)
 int paged_attn_splits(int B, int heads, int kv_heads, int D, int64_t max_tokens) {
-    constexpr int SHORT = 1024, TWO_STEPS = 2 * NW * TILE;
-    const int RESIDENT = 256 * waves_of(dim_of(D));
+    const int DM = dim_of(D), RESIDENT = 256 * waves_of(DM);
     const int units = kv_heads * ((heads / kv_heads + 15) / 16);
-    if (max_tokens <= TWO_STEPS || (max_tokens <= SHORT && (int64_t)B * units >= RESIDENT)) return 0;
+    // (a window may begin anywhere in 16 tokens)
+    const int64_t whole = ((int64_t)B * units >= (DM == 256 ? 128 : 64) ? 1024 : DM == 256 ? 256 : 512) + KV_TOKENS;
+    if (max_tokens <= whole) return 0;
     const int64_t steps = (max_tokens + NW * TILE - 1) / (NW * TILE);
     return (int)std::min<int64_t>((RESIDENT + units - 1) / units, B * steps);
 }
