@@ -586,10 +586,11 @@ wq_status wq_kv_cache_read(const wq_kv_cache* c, const int64_t* d_slots, int T, 
  *   lse = log sum_t exp(s_t)
  * Scores and sums are float32, the weights of the values two 16-bit parts
  * (right to 2^-16 in bf16 and over E4M3 values, 2^-22 in fp16); out is rounded once.
+ *   scale (times k_scale) finite
  *   d_q, d_out [B, heads, head_dim] act dtype, row strides in elements (>=
  *     heads * head_dim, multiples of 8)
  *   d_block_table device int32 [B, table_width]: the page of each page_size
- *     tokens; entries past a sequence's end are not read.  An entry outside
+ *     tokens; entries past a sequence's end or before its window do not matter.  An entry outside
  *     [0, pages) holds no tokens
  *   d_lengths device int32 [B]; below 0 is 0, above table_width * page_size
  *     that.  A sequence without tokens (a padding row) gives zeros and an lse
