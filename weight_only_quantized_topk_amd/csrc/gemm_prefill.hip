@@ -45,6 +45,7 @@
 #include "launch.hpp"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace wq {
 
@@ -65,8 +66,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base) {
 __device__ __forceinline__ int lds_swz(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int lds_off(int row, int ch) { return row * PF_ROWB + ((ch ^ lds_swz(row)) << 4); }
 
+template <int STAGE>
+using PrefillArgs = std::conditional_t<STAGE == STAGE_DENSE, DenseArgs, GemmArgs>;
+
 template <int WBITS, bool BF16, int STAGE, int NW, int RT, int BM, int OCC>
-__global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(GemmArgs g) {
+__global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(PrefillArgs<STAGE> g) {
     constexpr int NT = NW * 64;
     constexpr int BN = NW * RT * 16;
     constexpr int TJ = BM / 16;               // 16-row token tiles
@@ -123,6 +127,8 @@ __global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(GemmArgs g) 
     u32x4 w8[RT];
     u32x2 w4[RT];
     uint32_t sc[RT];
+    int scale_row = g.n_out;
+    if constexpr (DENSE) scale_row = g.ld;
     // raw weights (and int4 group scale) of weight tile t for one K step
     auto wload_t = [&](int step, int t) {
         if constexpr (WBITS == 8) {
@@ -132,7 +138,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(GemmArgs g) 
             // cached: the token tiles of an expert re-read its weight tiles
             w4[t] = __builtin_amdgcn_raw_buffer_load_b64(wres, wlane, tile_at(t) * tile_stride + c * CHUNK_BYTES + 8 * half, 0);
             const int grp = g.groups > 1 ? c : 0;
-            sc[t] = ssrc[(size_t)grp * (DENSE ? g.ld : g.n_out) + tile_at(t) * TILE_ROWS];
+            sc[t] = ssrc[(size_t)grp * scale_row + tile_at(t) * TILE_ROWS];
         }
     };
     auto wload = [&](int step) {
@@ -543,14 +549,14 @@ size_t dense_large_slab_bytes(int M, int K, int N) {
 }
 
 template <int WBITS, bool BF16, int NW, int RT, int BM, int OCC>
-static void launch_dense_cfg(const GemmArgs& g, int ksplit, hipStream_t s) {
+static void launch_dense_cfg(const DenseArgs& g, int ksplit, hipStream_t s) {
     constexpr int BN = NW * RT * 16;
     const dim3 grid((g.n_out + BN - 1) / BN, (g.M + BM - 1) / BM, ksplit);
     hipLaunchKernelGGL((gemm_prefill_kernel<WBITS, BF16, STAGE_DENSE, NW, RT, BM, OCC>), grid, dim3(NW * 64), 0, s, g);
 }
 
 template <int WBITS, bool BF16>
-static void launch_dense_plan(GemmArgs g, const DensePlan& p, hipStream_t s) {
+static void launch_dense_plan(DenseArgs g, const DensePlan& p, hipStream_t s) {
     const int N = g.n_out;
     if (p.main > 0) {
         g.n_out = p.main;
@@ -573,7 +579,7 @@ static void launch_dense_plan(GemmArgs g, const DensePlan& p, hipStream_t s) {
 
 void launch_dense_large(int wbits, bool bf16, const uint16_t* x, int M, int K, int N, const uint8_t* w,
                         const uint16_t* s, int groups, const Epilogue& ep, float* slabs, uint16_t* y, hipStream_t st) {
-    GemmArgs g{};
+    DenseArgs g{};
     g.a = x;
     g.w = w;
     g.s = s;

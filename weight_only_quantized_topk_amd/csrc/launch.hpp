@@ -108,10 +108,12 @@ struct GemmArgs {
     int a_direct;             // 1: A row = sorted position; 0: A row = token of the pair
     int cap;
     int y_act;                // large-batch DOWN without a K split: Y rows in the activation type
-    // STAGE_DENSE (x in a, y [M, n_out] in out)
-    int ld;                   // row length of y and of the scales (n_out of its columns are computed)
-    float* slabs;             // a K slice each [M, n_out], where K is split
-    Epilogue ep;              // applied where it is not
+};
+// one weight matrix (STAGE_DENSE): x in a, y [M, n_out] in out
+struct DenseArgs : GemmArgs {
+    int ld;        // row length of y and of the scales (n_out of its columns are computed)
+    float* slabs;  // a K slice each [M, n_out], where K is split
+    Epilogue ep;   // applied where it is not
 };
 
 // ---------------------------------------------------------------------------
