@@ -21,7 +21,7 @@
 //       VEC channels from VEC (l % 16) of the same 8 tokens, and the A operand of
 //       channel e of each is 4 byte permutations of its own registers.
 // No value crosses lanes but the running maximum, and nothing goes through LDS
-// until the waves' results are joined.  P is 16-bit in two parts (value, and
+// until the waves' results are joined (but Q where registers are short).  P is 16-bit in two parts (value, and
 // what that rounding left out), each multiplied by the same V operand: right to 2^-16
 // (bf16) or 2^-22 (fp16) of itself; with one part its rounding alone would be as
 // large as the output's.  Under E4M3 values P carries the row's scale, in bf16 for its range.
@@ -45,7 +45,7 @@
 // sequence and no second kernel (the rule is at paged_attn_splits).
 //
 // Measured (device time in a graph; a large copy reaches 5.2 TB/s here): one
-// sequence of 131072 tokens, 32 heads over 8 of 128 in bf16 (537 MB) 98 to 100 us;
+// sequence of 131072 tokens, 64 heads over 8 of 128 in bf16 (537 MB) 98 to 100 us;
 // 61 sequences of up to 8192 tokens, E4M3 rows (536 MB) 104 us; 256 of up to 1024,
 // 16 heads of 64 (538 MB) 107 us: 5.0 to 5.4 TB/s, the rate of reading.  Short
 // ones are bound by two launches, the walk over lengths and tables and the join:
