@@ -405,7 +405,7 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
             float top = x[0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
-            if (__any(top > m + M_SLACK)) {
+            if (__any(top - m > M_SLACK)) {  // (m + 8 may round up by 8 from 2^27 on: p of 2^16 is not finite in fp16)
                 top = fmaxf(top, m);
                 top = fmaxf(top, __shfl_xor(top, 16, 64));
                 top = fmaxf(top, __shfl_xor(top, 32, 64));
