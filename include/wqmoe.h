@@ -584,8 +584,9 @@ wq_status wq_kv_cache_read(const wq_kv_cache* c, const int64_t* d_slots, int T, 
  * d_lengths[b].  Query head h reads kv head h / (heads / kv_heads):
  *   s_t = scale * q . k_t;  out = sum_t exp(s_t) v_t / sum_t exp(s_t);
  *   lse = log sum_t exp(s_t)
- * Scores and sums are float32, the weights of the values two 16-bit parts
- * (right to 2^-16 in bf16 and over E4M3 values, 2^-22 in fp16); out is rounded once.
+ * Scores and sums are float32, the weights of the values two 16-bit parts: right
+ * to 2^-16 of themselves in bf16 and over E4M3 values, over fp16 ones to 2^-22 of
+ * themselves or 2^-38 of the sequence's largest, if that is more; out is rounded once.
  *   scale (times k_scale) finite
  *   d_q, d_out [B, heads, head_dim] act dtype, row strides in elements (>=
  *     heads * head_dim, multiples of 8)

@@ -23,10 +23,10 @@
 // No value crosses lanes but the running maximum, and nothing goes through LDS
 // until the waves' results are joined (but Q where registers are short).  P is 16-bit in two parts (value, and
 // what that rounding left out), each multiplied by the same V operand: right to 2^-16
-// (bf16) or 2^-22 (fp16) of itself; with one part its rounding alone would be as
+// (bf16) or 2^-22 (fp16, or 2^-38 of the largest if that is more) of itself; with one part its rounding alone would be as
 // large as the output's.  Under E4M3 values P carries the row's scale, in bf16 for its range.
 // Scores, statistics and sums are float32.  The maximum is raised only
-// when a score passes it by 2^8, so p is up to 2^8 and the accumulators are
+// when a score passes it by 2^8 (fp16: 2^2), so p is up to that and the accumulators are
 // seldom rescaled.
 //
 // Split over the length: every workgroup reads the batch's lengths and finds
@@ -70,7 +70,18 @@ constexpr bool q_in_lds = MODE == KV_16 && DM == 256;
 template <int MODE, int DM>
 constexpr int join_channels = q_in_lds<MODE, DM> ? 128 : DM;  // (leaves Q room for two workgroups a CU)
 constexpr float M_NONE = -3.4028234e38f;  // the running maximum before any score
-constexpr float M_SLACK = 8.0f;    // scores may pass it by this much (exponents of 2)
+// scores may pass the running maximum by SLACK, and weights are held times 2^BIAS (exponents of 2).  fp16 weights
+// need the bias: their least step is 2^-24, so without one (p up to 2^8) the second part of a weight below 2^-3 was
+// short and one below 2^-25 was nothing, which the sum still had: behind one token 2^25 above all others a long
+// context's output lost up to a quarter (500 tokens in a workgroup).  With 2^13, and a slack of 2 so that p 2^13 stays below
+// 2^15, the two parts are right to 2^-38 of the largest weight; times are the same (256 sequences of up to 1024, 16 heads of 64:
+// 106 us).  bf16 has float32's exponents
+template <bool PBF>
+constexpr float SLACK = PBF ? 8.0f : 2.0f;
+template <bool PBF>
+constexpr float BIAS = PBF ? 0.0f : 13.0f;
+template <bool PBF>
+constexpr float UNBIAS = PBF ? 1.0f : 0x1p-13f;
 constexpr float LN2 = 0.693147180559945309f;
 
 // a sequence's tokens [lo, len), its first tile beginning at lo rounded down to
@@ -405,7 +416,7 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
             float top = x[0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
-            if (__any(top - m > M_SLACK)) {  // (m + 8 may round up by 8 from 2^27 on: p of 2^16 is not finite in fp16)
+            if (__any(top - m > SLACK<PBF>)) {  // (m + SLACK may round up past a score from 2^25 on)
                 top = fmaxf(top, m);
                 top = fmaxf(top, __shfl_xor(top, 16, 64));
                 top = fmaxf(top, __shfl_xor(top, 32, 64));
@@ -418,7 +429,7 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
             u32x4 phi, plo;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                x[j] = __builtin_amdgcn_exp2f(x[j] - m);
+                x[j] = __builtin_amdgcn_exp2f(x[j] - m + BIAS<PBF>);
                 l += x[j];
                 if constexpr (ROW) x[j] *= vsv[j / 4][j % 4];
             }
@@ -501,7 +512,7 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
                     f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int w = 0; w < NW; ++w) {
-                        const float f = __builtin_amdgcn_exp2f(lm[w * 16 + hd] - mx);
+                        const float f = __builtin_amdgcn_exp2f(lm[w * 16 + hd] - mx) * UNBIAS<PBF>;
                         sum += f * ll[w * 16 + hd];
                         o += f * *reinterpret_cast<const f32x4*>(lacc + (w * nh + hd) * LD + c);
                     }
