@@ -586,7 +586,7 @@ wq_status wq_kv_cache_read(const wq_kv_cache* c, const int64_t* d_slots, int T, 
  *   lse = log sum_t exp(s_t)
  * Scores and sums are float32, the weights of the values two 16-bit parts: right
  * to 2^-16 of themselves in bf16 and over E4M3 values, over fp16 ones to 2^-22 of
- * themselves or 2^-38 of the sequence's largest, if that is more; out is rounded once.
+ * themselves or 2^-37 of the sequence's largest, if that is more; out is rounded once.
  *   scale (times k_scale) finite
  *   d_q, d_out [B, heads, head_dim] act dtype, row strides in elements (>=
  *     heads * head_dim, multiples of 8)
@@ -600,8 +600,10 @@ wq_status wq_kv_cache_read(const wq_kv_cache* c, const int64_t* d_slots, int T, 
  *   d_workspace: wq_paged_attention_workspace_bytes() bytes; 0 (NULL allowed)
  *     where no sequence can be long enough to be split.  What it holds does not matter
  * Rows of the cache outside a sequence do not reach its output, whatever they
- * hold.  A NaN in its own keys or query is one in the heads that read it, and
- * an infinite or NaN value an infinity or NaN in its channel.  The split of a sequence
+ * hold.  A NaN in its own keys or query is one in the heads that read it, a NaN
+ * value one in its channel.  An infinite value is one of its sign in its channel, or
+ * NaN beside one of the other sign or where its weight is less than 2^-37 (fp16)
+ * or 2^-100 (bf16) of the largest.  The split of a sequence
  * goes by all of the batch's lengths: its last bits may differ with the batch,
  * and are the same for the same call.
  * Limits: heads a multiple of kv_heads; B, heads <= 65535; table_width *

@@ -23,7 +23,7 @@
 // No value crosses lanes but the running maximum, and nothing goes through LDS
 // until the waves' results are joined (but Q where registers are short).  P is 16-bit in two parts (value, and
 // what that rounding left out), each multiplied by the same V operand: right to 2^-16
-// (bf16) or 2^-22 (fp16, or 2^-38 of the largest if that is more) of itself; with one part its rounding alone would be as
+// (bf16) or 2^-22 (fp16, or 2^-37 of the largest if that is more) of itself; with one part its rounding alone would be as
 // large as the output's.  Under E4M3 values P carries the row's scale, in bf16 for its range.
 // Scores, statistics and sums are float32.  The maximum is raised only
 // when a score passes it by 2^8 (fp16: 2^2), so p is up to that and the accumulators are
@@ -74,7 +74,7 @@ constexpr float M_NONE = -3.4028234e38f;  // the running maximum before any scor
 // need the bias: their least step is 2^-24, so without one (p up to 2^8) the second part of a weight below 2^-3 was
 // short and one below 2^-25 was nothing, which the sum still had: behind one token 2^25 above all others a long
 // context's output lost up to a quarter (500 tokens in a workgroup).  With 2^13, and a slack of 2 so that p 2^13 stays below
-// 2^15, the two parts are right to 2^-38 of the largest weight; times are the same (256 sequences of up to 1024, 16 heads of 64:
+// 2^15, the two parts are right to 2^-37 of the largest weight; times are the same (256 sequences of up to 1024, 16 heads of 64:
 // 106 us).  bf16 has float32's exponents
 template <bool PBF>
 constexpr float SLACK = PBF ? 8.0f : 2.0f;
@@ -188,11 +188,27 @@ __device__ __forceinline__ Dwords<BYTES / 4> load_bytes(__amdgpu_buffer_rsrc_t r
     return r;
 }
 
-// a pair of floats as 16-bit values and what their rounding left out
+// a pair of weights as 16-bit values and what their rounding left out
 template <bool BF16>
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
     hi = f32_to_act2<BF16>(a, b);
     lo = f32_to_act2<BF16>(a - act_to_f32<BF16>((uint16_t)hi), b - act_to_f32<BF16>((uint16_t)(hi >> 16)));
+}
+// The same beside values that may be infinite: both parts above 0 where the weight is, so that an infinity times
+// either is itself (0 or less than 0 made the channel NaN).  The first part is rounded towards 0; the second is
+// raised by 2^-23 of the weight (bf16), or to fp16's least step.  As many instructions as above or fewer
+template <bool BF16>
+__device__ __forceinline__ void split2_above(float a, float b, uint32_t& hi, uint32_t& lo) {
+    if constexpr (BF16) {
+        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+        hi = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+        lo = f32_to_act2<true>(fmaf(a, 1.0f + 0x1p-23f, -__uint_as_float(ua & 0xffff0000u)),
+                               fmaf(b, 1.0f + 0x1p-23f, -__uint_as_float(ub & 0xffff0000u)));
+    } else {
+        hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+        const float ha = f16_to_f32((uint16_t)hi), hb = f16_to_f32((uint16_t)(hi >> 16));
+        lo = f32_to_act2<false>(__builtin_amdgcn_fmed3f(a - ha, ha, 0x1p-24f), __builtin_amdgcn_fmed3f(b - hb, hb, 0x1p-24f));
+    }
 }
 
 // DM: head_dim rounded up to 64, 128 or 256 (FULL: it is DM)
@@ -436,7 +452,8 @@ __global__ __launch_bounds__(NW * 64, waves_of(DM)) void paged_attention_kernel(
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t hi, lo;
-                split2<PBF>(x[2 * j], x[2 * j + 1], hi, lo);
+                if constexpr (F8) split2<PBF>(x[2 * j], x[2 * j + 1], hi, lo);
+                else split2_above<BF16>(x[2 * j], x[2 * j + 1], hi, lo);
                 phi[j] = hi;
                 plo[j] = lo;
             }
