@@ -439,7 +439,9 @@ wq_status sparse24_w4a16_gemm(const void* d_x, int M, int K, int N, const void* 
  * beyond that (or with act-order) the grouped GEMM of this library with one
  * expert and top-1: up to 24 rows the small-batch kernel, up to 192 the
  * large-batch kernel with 64-row tiles, above that 128-row tiles; fp32
- * accumulation, rounded once to the activation type.
+ * accumulation, rounded once to the activation type.  int4: the large-batch kernel
+ * multiplies by code * scale rounded to fp16 (2^-11 of each weight); the others by the
+ * exact code, with the scale on the fp32 sum of its group.
  *   d_x [M, K] act dtype; d_y [M, N] act dtype
  *   d_w_packed, d_scales: wq_pack_w4 / wq_pack_w8 output for E = 1, n_out = N,
  *     k_in = K (no gate/up interleave); int4 group_size 128 or -1, int8 -1
@@ -463,7 +465,7 @@ wq_status dense_w8a16_gemm(const void* d_x, int M, int K, int N, const void* d_w
                            void* d_y, int act_dtype, void* d_workspace, size_t workspace_bytes, void* stream);
 
 /*
- * The same with an epilogue on the fp32 sums, rounded once:
+ * The same with an epilogue on the fp32 sums, which are rounded once, after it:
  *   y[m, n] = f(sum_k x[m, k] W[n, k] + bias[n]) + residual[m, n]
  *   d_bias      [N] act dtype, or NULL
  *   activation  f: WQ_ACT_NONE, WQ_ACT_RELU, WQ_ACT_SILU (z / (1 + exp(-z))),
@@ -474,7 +476,11 @@ wq_status dense_w8a16_gemm(const void* d_x, int M, int K, int N, const void* d_w
  *   dense_epilogue_workspace_bytes(wbits, ...) bytes of workspace, 256-byte
  *               aligned (NULL allowed for 0): K slices of a large batch that leaves most of the GPU
  *               idle, the act-order gather
- * One launch without act-order and a split of K (any number of rows).  Limits:
+ * Up to 128 rows, and above where one round of workgroups covers the output, one
+ * launch and exact int4 codes; otherwise the large-batch kernel (int4 weights rounded to
+ * fp16 as above): one launch, two where columns are left over from full rounds of
+ * tiles, and one more for a split of K.  Act-order adds one.  So a row's last
+ * bits may differ with the number of rows.  Limits:
  * those above, M <= 65535 * 64, K and N <= 2^24.  y and the workspace must not
  * overlap anything else.
  */

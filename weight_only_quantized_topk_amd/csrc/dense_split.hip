@@ -11,13 +11,16 @@
 // Numerics as dense_decode.hip: int4 codes exact, the group's scale on the float32 sum of
 // its 128 channels, int8 exact, the column's scale at the end; partial sums in wave order.
 //
-// The bound is a CU's own reading: K (RT tiles of weights + 16 R rows of x) at
-// about 64 bytes a clock, so the tile is the smallest with which the grid is one round
-// (256 workgroups), and beyond that the streaming kernel, which shares its rows through
-// LDS, is ahead.  Against it (K = 4096, int4 / int8, us): M = 4, N = 4096 15.1
-// / 20.5 -> 6.3 / 6.5; M = 29, N = 4096 18.4 / 23.2 -> 9.1 / 8.5; M = 64, N = 6144
-// 26.7 / 30.5 -> 15.9 / 15.8; M = 128, N = 4096 27.5 / 31.3 -> 16.3 / 15.8; K =
-// 14336: M = 29, N = 4096 55 / 74 -> 21.7 / 22.6.
+// The bound is latency: at K = 4096 a wave has 4 chunks (int4) or 8 (int8) of which
+// up to 3 are in flight, so one or two waits for memory are not hidden, and a launch and the
+// join of 8 waves stand beside them.  (A workgroup's own reading, K (RT tiles + 16 R rows of x), is far less:
+// 0.19 MB at M = 29, N = 4096, 1.3 of the 8.7 us at 64 bytes a clock.)  Measured, a 1024 channels
+// cost what STEP_US says, growing with the tile, so the tile is the smallest with which the
+// grid is one round (256 workgroups); beyond that the streaming kernel, which shares
+// its rows through LDS, is ahead.  Against it (N = 4096, K = 4096, int4 / int8, us): M = 4 14.5
+// / 19.9 -> 5.5 / 6.2; M = 29 17.7 / 23.0 -> 8.7 / 8.3; M = 128 25.6 / 29.9 -> 16.0 / 15.4; K =
+// 14336: M = 29 54 / 73 -> 21.6 / 25.1.  The reading of weights and x alone would take 1.8 / 3.4 us at M = 29,
+// K = 4096 and 6.1 / 11.6 at K = 14336.
 #include "common.hpp"
 #include "epilogue.hpp"
 #include "launch.hpp"

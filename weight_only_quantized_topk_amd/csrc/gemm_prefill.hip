@@ -35,10 +35,13 @@
 // One weight matrix with an epilogue (STAGE_DENSE) is the same kernel without
 // the sort: token row p is row p of x, the last workgroup's missing weight tiles
 // read the last one and store nothing (n_out any multiple of 16), and the float32
-// sums go through bias, activation and residual to y.
+// sums go through bias, activation and residual to y.  Its int4 weights are rounded
+// to fp16 after their scale as above, which the kernels of few rows do not do:
+// a float32 sum of each group's 128 channels would need as many accumulators again, and
+// the 512 x 128 shape has no registers for them.
 //
-// DOWN may split K over gridDim.z slices when its output grid is too small to
-// fill the chip: slice z writes its partial sums to its own fp32 slab of Y and
+// DOWN and STAGE_DENSE may split K over gridDim.z slices when their output grid is too
+// small to fill the chip: slice z writes its partial sums to its own fp32 slab (of Y) and
 // the combine kernel adds the slabs in ascending order (deterministic).
 #include "common.hpp"
 #include "epilogue.hpp"
@@ -101,7 +104,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void gemm_prefill_kernel(PrefillArgs<
 
     constexpr int KCHUNK = WFmt<WBITS>::KCHUNK;
     const int C = g.k_in / KCHUNK;  // packed chunks per 16-row tile
-    // K slice of this workgroup (only DOWN is ever split)
+    // K slice of this workgroup (DOWN and STAGE_DENSE may be split)
     const int nsteps = g.k_in / PF_BK;
     const int step0 = (int)((long)blockIdx.z * nsteps / gridDim.z);
     const int step_end = (int)((long)(blockIdx.z + 1) * nsteps / gridDim.z);
@@ -481,8 +484,10 @@ int launch_gemm_prefill(int wbits, bool bf16, int stage, const GemmArgs& g, hipS
 // ------------------------------------------------------- one weight matrix
 // The shapes as STAGE_DENSE takes them, with the microseconds of a K step (64
 // channels) when 1, 2 or 3 workgroups share a CU, as measured over 160..1024 rows,
-// 560..20480 outputs, K 1024..14336 (int8; int4 about a tenth more).  512 x 128 does
-// the most a step; the others are for what does not fill its rounds.
+// 560..20480 outputs, K 1024..14336, of int8 weights.  One table for both types: over 160, 256,
+// 512 and 1024 rows of 4096 -> 4096 / 6144, 14336 -> 4096 and 7168 -> 20480 a call takes 0.83 to 1.03 of the
+// expected time in int8, 0.85 to 1.09 in int4.  512 x 128 does the most a step; the
+// others are for what does not fill its rounds.
 struct DenseShape {
     int bn, bm, per_cu;
     float step_us[3];

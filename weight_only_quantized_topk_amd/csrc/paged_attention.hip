@@ -10,7 +10,7 @@
 // of 2 operations a value for each of the group's G heads, so at most 2 G
 // operations a byte (4 G for codes): HBM bound.
 //
-// The cache is read once, straight to registers.  A wave takes tiles of 32
+// The cache is read once for every 16 heads of a group begun, straight to registers.  A wave takes tiles of 32
 // tokens; the group's heads (up to 16 at a time) are the 16 columns of
 // v_mfma_f32_16x16x32:
 //   S^T [token, head] = K Q^T: lane l holds 8 channels of token l % 16 as they lie
@@ -45,11 +45,13 @@
 // sequence and no second kernel (the rule is at paged_attn_splits).
 //
 // Measured (device time in a graph; a large copy reaches 5.2 TB/s here): one
-// sequence of 131072 tokens, 64 heads over 8 of 128 in bf16 (537 MB) 98 to 100 us;
-// 61 sequences of up to 8192 tokens, E4M3 rows (536 MB) 104 us; 256 of up to 1024,
-// 16 heads of 64 (538 MB) 107 us: 5.0 to 5.4 TB/s, the rate of reading.  Short
+// sequence of 131072 tokens, 64 heads over 8 of 128 in bf16 (537 MB) 99.6 us;
+// 61 sequences of up to 8192 tokens, E4M3 rows (536 MB) 105 us; 256 of up to 1024,
+// 16 heads of 64 (538 MB) 106 us: 5.1 to 5.4 TB/s, the rate of reading.  Far from it: widths that run
+// padded (16 sequences of up to 4096, 8 heads of 32 in E4M3 rows 23 us, 3.6 by their bytes), groups of more than 16 heads (2 groups
+// of 17 of 128, the same lengths: 24.8 us, of 16 21.0, by their bytes 6.5).  Short
 // ones are bound by two launches, the walk over lengths and tables and the join:
-// 9 us for one sequence of 1024 tokens (4 MB), of these 4 to 5 the second kernel.
+// 9 us for one sequence of 1024 tokens (4 MB), of these 3 to 4 the second kernel.
 #include "common.hpp"
 #include "kv_common.hpp"
 #include "launch.hpp"
@@ -667,10 +669,12 @@ void launch_kernel(const PagedAttnArgs& g, hipStream_t s) {
 
 // Non-temporal loads where the keys and values are more than the last-level
 // cache (256 MB) holds from one step to the next: one sequence of 131072 tokens, 8
-// heads of 128 in bf16 (537 MB), 98 against 105 us; 61 sequences of up to 8192 in
-// E4M3 (536 MB) 114 against 119.  A cache that fits is read from there (56 MB: 22
-// against 26), and sequences of a workgroup each are slower with them (116
-// against 106 us, 256 x up to 1024 tokens, 16 heads of 64)
+// heads of 128 in bf16 (537 MB), 99.5 against 105 us; 61 sequences of up to 8192 in
+// E4M3 (536 MB) 105 against 111.  A cache that fits is read from there (56 MB: 20.8
+// against 24.1), and sequences of a workgroup each are slower with them (119
+// against 107 us, 256 x up to 1024 tokens, 16 heads of 64).  The host knows the whole cache's size only, not
+// what a batch reads of it: a small batch in a large pool, called again and again over the same pages, gets them too (7 sequences
+// under a window of 4096, 56 MB of a pool of 2 GB: 25.6 us)
 template <bool BF16, int MODE, int DM, bool FULL>
 void launch_full(const PagedAttnArgs& g, hipStream_t s) {
     const int64_t bytes = (int64_t)g.pages * g.page_size * g.kv_heads * g.D * (MODE == KV_16 ? 4 : 2);
@@ -721,6 +725,9 @@ void launch_type(const PagedAttnArgs& g, hipStream_t s) {
 //   up to 2000 tokens, 1 sequence       9.6 / 14.2   11.7 / 21.5   17.0 / 45.2
 //                     64 sequences     36.8 / 36.0   59.8 / 64.4    135 / 136
 // (8 waves a workgroup there: 64 or 128 KB a step keep a CU busy as it is, 17.2 -> 18.9 us at 32 sequences of 1009)
+// max_tokens is what the block table has room for: under a table wider than the lengths short
+// sequences are split as long ones are (32 of up to 500 tokens, 8 heads of 128: 11.1 us with a table of 500 tokens, 16.8 with one
+// of 131072)
 int paged_attn_splits(int B, int heads, int kv_heads, int D, int64_t max_tokens) {
     const int DM = dim_of(D), RESIDENT = 256 * waves_of(DM);
     const int units = kv_heads * ((heads / kv_heads + 15) / 16);

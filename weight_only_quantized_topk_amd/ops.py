@@ -702,7 +702,8 @@ def dense_w4a16_gemm(x, N: int, w_packed, scales, group_size: int = 128, k_perm=
     packed by pack_w4 with E = 1; lora: the rows' adapters, added to y.  With a
     bias [N], an activation ("relu", "silu", "gelu", "gelu_tanh") or a residual
     [M, N] (rows may be strided; may be out): y = activation(x W^T + bias) +
-    residual, rounded once (workspace: dense_epilogue_workspace_bytes)."""
+    residual in float32, then rounded (workspace: dense_epilogue_workspace_bytes).
+    Large batches take each weight, code times scale, rounded to fp16."""
     if bias is not None or activation is not None or residual is not None:
         return _dense_epilogue(4, x, N, w_packed, scales, group_size, k_perm, out, workspace, stream, lora, bias,
                                activation, residual)
