@@ -10,7 +10,8 @@
 //   back:       v = code * c in float32, rounded once
 // v / c is the float32 quotient: one reciprocal a row, then a product and one
 // residual step, which gives the correctly rounded quotient where nothing over- or
-// underflows (10 instructions a value less than a division: 0.9 us at the size below).  Both kernels give a row LPR lanes of 8
+// underflows (10 instructions a value less than a division: 0.9 us at the size below); the residual is
+// taken as q c - v, whose zero is +0, so that q - 0 keeps the sign of a zero q.  Both kernels give a row LPR lanes of 8
 // values each, keys and values by the same thread; a workgroup takes consecutive
 // tokens of one head, whose rows and scales are neighbours in the cache where a prompt
 // fills its pages.
@@ -86,7 +87,7 @@ __device__ __forceinline__ void put(u32x4 d, bool active, int64_t row, int D, in
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float q = v[j] * inv;
-                v[j] = fmaf(fmaf(-q, cr, v[j]), ir, q);
+                v[j] = fmaf(-fmaf(q, cr, -v[j]), ir, q);
             }
             // (at most 448 and a step, which the conversion rounds to 448)
             code = u32x2{codes4(v[0], v[1], v[2], v[3]), codes4(v[4], v[5], v[6], v[7])};
@@ -94,7 +95,7 @@ __device__ __forceinline__ void put(u32x4 d, bool active, int64_t row, int D, in
 #pragma unroll
             for (int j = 0; j < 8; ++j) {  // past the codes' range (the residual may be infinite): the product
                 const float q = v[j] * inv;
-                v[j] = fabsf(q) > 480.0f ? q : fmaf(fmaf(-q, c, v[j]), inv, q);
+                v[j] = fabsf(q) > 480.0f ? q : fmaf(-fmaf(q, c, -v[j]), inv, q);
             }
             code = u32x2{codes4(clamp_e4m3(v[0]), clamp_e4m3(v[1]), clamp_e4m3(v[2]), clamp_e4m3(v[3])),
                          codes4(clamp_e4m3(v[4]), clamp_e4m3(v[5]), clamp_e4m3(v[6]), clamp_e4m3(v[7]))};
