@@ -35,3 +35,27 @@ def test_infinite_values(act, D, B, H, G, n):
         rest = [c for c in range(D) if c not in (1, 3, 5)]
         assert_near(got[..., rest], want[..., rest], tol[..., rest], act)
         assert bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("act,gaps", [("f16", [0.0, 5.0, 11.0, 16.5, 20.0, 23.0, 25.5]), ("bf16", [0.0, 16.5, 25.5, 45.0, 60.0, 69.0])])
+@pytest.mark.parametrize("n,first,at", [(300, 0, 3), (300, 200, 3), (300, 3, 290), (3001, 5, 2900), (3001, 2900, 5)])
+def test_infinite_values_of_small_weight(act, gaps, n, first, at):
+    """The infinity's weight is exp(-gap) of the largest, seen before or after it: down to 2^-37 (fp16) and 2^-100 (bf16)."""
+    need_gpu()
+    D, H = 64, len(gaps)
+    say("small weights", act, n, first, at)
+    dt = TYPES[act]
+    k = torch.zeros((1, n, H, D), dtype=dt, device="cuda")
+    v = torch.ones((1, n, H, D), dtype=dt, device="cuda")
+    k[..., 0] = -60000.0  # of no weight
+    k[0, first, :, 0] = 0
+    for h, gap in enumerate(gaps):
+        k[0, at, h, 0] = -gap
+    v[0, at, :, 2], v[0, at, :, 7] = math.inf, -math.inf
+    q = torch.zeros((1, H, D), dtype=dt, device="cuda")
+    q[..., 0] = 1
+    cache, table, lengths = paged(k, v)
+    out = wq.paged_attention(q, cache, table, lengths, scale=1.0)[0]
+    assert bool((out[:, 2] == math.inf).all()) and bool((out[:, 7] == -math.inf).all()), out[:, [2, 7]]
+    rest = [c for c in range(D) if c not in (2, 7)]
+    assert float((out[:, rest].float() - 1).abs().max()) <= 2.0 ** -7  # (the weights' mean of ones: bf16's step)
